@@ -31,7 +31,9 @@ __all__ = [
     "moe_masked_slab_to_expand", "moe_scatter_rows", "upscale_fp8_to_bf16",
     "requant_weight_block_ue8m0", "mxq_mfma_scale_bytes", "mfma_scales",
     "mxq_copy16", "moe_layout_scatter_quant", "moe_layout_noalloc",
-    "mxq_gather_read16", "mxq_fill_rows16",
+    "mxq_gather_read16", "mxq_fill_rows16", "SCORE_FNS", "moe_route",
+    "moe_route_backward", "moe_scatter_rows_backward",
+    "moe_combine_backward",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -101,6 +103,14 @@ _SIGNATURES = {
                                         _i32, _i64, _p, _p, _p, _p, _p, _p, _p,
                                         _i64, _i32, _i32, _p, _i64, _p, _i64,
                                         _p]),
+    "moe_route": (_i32, [_p, _i32, _i64, _i64, _i32, _i32, _i32, _p, _i32,
+                         _i32, _i32, ctypes.c_float, _p, _p, _p]),
+    "moe_route_backward": (_i32, [_p, _p, _i32, _i64, _p, _i64, _i32, _i32,
+                                  _i32, _i32, ctypes.c_float, _p, _i64, _p]),
+    "moe_scatter_rows_backward": (_i32, [_p, _i32, _i64, _i64, _p, _i64, _i32,
+                                         _i32, _p, _i64, _i32, _p]),
+    "moe_combine_backward": (_i32, [_p, _i32, _i64, _p, _i64, _i64, _p, _p,
+                                    _i64, _i32, _i32, _p, _i64, _p, _p]),
     "mxq_status_string": (ctypes.c_char_p, [_i32]),
     "mxq_abi_version": (_i32, []),
 }
@@ -139,6 +149,20 @@ def _check(fn: str, status: int) -> None:
 
 def _stream(t: torch.Tensor) -> int:
     return torch.cuda.current_stream(t.device).cuda_stream
+
+
+def _call(fn: str, t: torch.Tensor, *args) -> None:
+    """Run entry point ``fn`` on the current stream of t's device, which need
+    not be the current one; raises on an error status."""
+    f = getattr(lib(), fn)
+    dev = t.device.index
+    if dev == torch.cuda.current_device():
+        st = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+    if st != MXQ_OK:
+        raise MxqError(fn, st)
 
 
 def _ptr(t: torch.Tensor | None) -> int | None:
@@ -296,6 +320,86 @@ def mxq_mfma_scale_bytes(rows: int, H: int, tile_m: int = 32) -> int:
     if r < 0:
         raise ValueError("invalid arguments to mxq_mfma_scale_bytes")
     return int(r)
+
+
+# ------------------------------------------------------------------- router
+
+SCORE_FNS = {"softmax": 0, "sigmoid": 1}
+
+
+def _logits(logits: torch.Tensor, name: str = "logits") -> int:
+    _dev(logits, name)
+    return _rows(logits, name, tuple(OUT_DTYPES))
+
+
+def _dense(t: torch.Tensor, name: str, dtype, shape, like: torch.Tensor):
+    """A contiguous tensor of exactly this dtype and shape, on the inputs'
+    device."""
+    _dev(t, name, like)
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or \
+            not t.is_contiguous():
+        raise ValueError("%s must be contiguous %s %s"
+                         % (name, dtype, list(shape)))
+    return t
+
+
+def moe_route(logits: torch.Tensor, K: int, scoring: str = "softmax",
+              bias: torch.Tensor | None = None, num_groups: int = 1,
+              top_groups: int = 1, renormalize: bool = True,
+              weight_scale: float = 1.0, ids: torch.Tensor | None = None,
+              weights: torch.Tensor | None = None):
+    """Top-k routing of ``logits [T, E]`` (bf16 or float32): ``(topk_ids
+    int32 [T, K], topk_weights float32 [T, K])``, as ``moe_layout`` and
+    ``moe_combine`` take them (see ``moe_route`` in mxq.h).  ``scoring`` is
+    ``"softmax"`` or ``"sigmoid"``; ``bias`` (float32 [E]) takes part in the
+    choice only.  Where fewer than K experts can be chosen the id is -1 and
+    the weight 0."""
+    ld = _logits(logits)
+    T, E = logits.shape
+    if bias is not None:
+        _dense(bias, "bias", torch.float32, (E,), logits)
+    if ids is None:
+        ids = torch.empty((T, K), dtype=torch.int32, device=logits.device)
+    else:
+        _dense(ids, "ids", torch.int32, (T, K), logits)
+    if weights is None:
+        weights = torch.empty((T, K), dtype=torch.float32,
+                              device=logits.device)
+    else:
+        _dense(weights, "weights", torch.float32, (T, K), logits)
+    _call("moe_route", logits, _ptr(logits), OUT_DTYPES[logits.dtype], ld, T,
+          E, K, SCORE_FNS[scoring], _ptr(bias), num_groups, top_groups,
+          int(renormalize), weight_scale, _ptr(ids), _ptr(weights))
+    return ids, weights
+
+
+def moe_route_backward(grad_weights: torch.Tensor, logits: torch.Tensor,
+                       topk_ids: torch.Tensor, scoring: str = "softmax",
+                       renormalize: bool = True, weight_scale: float = 1.0,
+                       grad_logits: torch.Tensor | None = None
+                       ) -> torch.Tensor:
+    """Gradient of ``moe_route``'s weights to its logits, with the forward
+    call's arguments and its ids: ``grad_logits [T, E]`` in the logits'
+    dtype."""
+    ld = _logits(logits)
+    T, E = logits.shape
+    _dev(topk_ids, "topk_ids", logits)
+    if topk_ids.dim() != 2:
+        raise ValueError("topk_ids must be int32 [T, K]")
+    K = topk_ids.shape[1]
+    _dense(topk_ids, "topk_ids", torch.int32, (T, K), logits)
+    _dense(grad_weights, "grad_weights", torch.float32, (T, K), logits)
+    if grad_logits is None:
+        grad_logits = torch.empty((T, E), dtype=logits.dtype,
+                                  device=logits.device)
+    _dev(grad_logits, "grad_logits", logits)
+    ld_g = _rows(grad_logits, "grad_logits", (logits.dtype,))
+    _at_least(grad_logits, "grad_logits", T, E)
+    _call("moe_route_backward", logits, _ptr(grad_weights), _ptr(logits),
+          OUT_DTYPES[logits.dtype], ld, _ptr(topk_ids), T, E, K,
+          SCORE_FNS[scoring], int(renormalize), weight_scale,
+          _ptr(grad_logits), ld_g)
+    return grad_logits
 
 
 # ------------------------------------------------------------------- layout
@@ -755,6 +859,67 @@ def moe_combine(y: torch.Tensor, src2dst: torch.Tensor,
                            code, _stream(y))
     _check("moe_combine", st)
     return out
+
+
+def moe_scatter_rows_backward(grad_rows: torch.Tensor, src2dst: torch.Tensor,
+                              out_dtype: torch.dtype | None = None,
+                              out: torch.Tensor | None = None
+                              ) -> torch.Tensor:
+    """Gradient of the expert sort: ``out [T, H]``, for every token the fp32
+    sum of its rows of ``grad_rows [num_rows, H]`` (bf16 or float32), in the
+    rows' dtype unless ``out_dtype`` or ``out`` says otherwise."""
+    _dev(grad_rows, "grad_rows")
+    ld = _rows(grad_rows, "grad_rows", tuple(OUT_DTYPES))
+    num_rows, H = grad_rows.shape
+    K = _src2dst(src2dst, grad_rows, None)
+    T = src2dst.shape[0]
+    if out is None:
+        out = torch.empty((T, H), dtype=out_dtype or grad_rows.dtype,
+                          device=grad_rows.device)
+    _dev(out, "out", grad_rows)
+    ld_o = _rows(out, "out", tuple(OUT_DTYPES))
+    _at_least(out, "out", T, H)
+    _call("moe_scatter_rows_backward", grad_rows, _ptr(grad_rows),
+          OUT_DTYPES[grad_rows.dtype], ld, num_rows, _ptr(src2dst), T, K, H,
+          _ptr(out), ld_o, OUT_DTYPES[out.dtype])
+    return out
+
+
+def moe_combine_backward(grad_out: torch.Tensor, y: torch.Tensor,
+                         src2dst: torch.Tensor, topk_weights: torch.Tensor,
+                         grad_y: torch.Tensor | None = None,
+                         grad_weights: torch.Tensor | None = None):
+    """Gradient of ``moe_combine(y, src2dst, topk_weights)`` for ``grad_out
+    [T, H]`` (bf16 or float32): ``(grad_y bf16 [num_rows, H], grad_weights
+    float32 [T, K])``.  Rows of ``grad_y`` that are no destination keep the
+    contents of a given ``grad_y``."""
+    _dev(grad_out, "grad_out")
+    ld_g = _rows(grad_out, "grad_out", tuple(OUT_DTYPES))
+    T, H = grad_out.shape
+    K = _src2dst(src2dst, grad_out, T)
+    _dev(y, "y", grad_out)
+    ld_y = _rows(y, "y", (torch.bfloat16,))
+    num_rows = y.shape[0]
+    if y.shape[1] != H:
+        raise ValueError("y must be [num_rows, %d]" % H)
+    _dense(topk_weights, "topk_weights", torch.float32, (T, K), grad_out)
+    if grad_y is None:
+        grad_y = torch.empty((num_rows, H), dtype=torch.bfloat16,
+                             device=y.device)
+    _dev(grad_y, "grad_y", grad_out)
+    ld_gy = _rows(grad_y, "grad_y", (torch.bfloat16,))
+    _at_least(grad_y, "grad_y", num_rows, H)
+    if grad_weights is None:
+        grad_weights = torch.empty((T, K), dtype=torch.float32,
+                                   device=y.device)
+    else:
+        _dense(grad_weights, "grad_weights", torch.float32, (T, K), grad_out)
+    if T and K:
+        _call("moe_combine_backward", grad_out, _ptr(grad_out),
+              OUT_DTYPES[grad_out.dtype], ld_g, _ptr(y), ld_y, num_rows,
+              _ptr(src2dst), _ptr(topk_weights), T, K, H, _ptr(grad_y), ld_gy,
+              _ptr(grad_weights))
+    return grad_y, grad_weights
 
 
 def mxq_e4m3_encode_f32(x: torch.Tensor) -> torch.Tensor:

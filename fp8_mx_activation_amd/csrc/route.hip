@@ -1,0 +1,604 @@
+// moe_route, moe_route_backward: the router in front of the layout.
+//
+// Forward, per token: scores s_e = softmax(l)_e or 1 / (1 + exp(-l_e));
+// choice values c_e = s_e (+ bias_e); the K largest c_e among the experts of
+// the best groups, equal values by lowest index; weights from the unbiased
+// scores of the chosen.  Backward: the gradient of the weights to the logits
+// (the choice itself has none).
+//
+// One wavefront per token; lane i owns the PER consecutive experts from
+// i * PER, so a row is one vector load per lane, and the lowest lane that
+// holds the maximum also holds the lowest index.  Each of the K choices is
+// one wavefront maximum of ordered integer keys (DPP, no LDS memory).
+//
+// Choice values are computed and compared in 64 bits wherever they come out
+// of an exponential: near a tie two experts' values lie closer than fp32
+// rounding, and the choice would then hang on the rounding of exp.  A softmax
+// without bias or groups keeps the order of its logits, so there the fp32
+// logits themselves are the keys and no exponential is taken for the choice.
+// The weights are computed in 64 bits (at most K exponentials per token, one
+// per lane) and rounded once to fp32.
+//
+// Bound: a row of E logits is 0.5-4 KB, so even 8192 tokens are one or two
+// microseconds of HBM time; the kernel is bound by the K dependent
+// reductions of one wavefront.
+#include "mxq_device.hpp"
+#include "mxq_host.hpp"
+
+namespace {
+
+using namespace mxq;
+
+constexpr float kFltMax = 3.402823466e38f;
+
+// ------------------------------------------------- wavefront reductions
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp32(uint32_t old, uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)old, (int)v, CTRL, ROWS,
+                                               0xF, false);
+}
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint64_t dpp64(uint64_t old, uint64_t v) {
+  const uint32_t lo = dpp32<CTRL, ROWS>((uint32_t)old, (uint32_t)v);
+  const uint32_t hi =
+      dpp32<CTRL, ROWS>((uint32_t)(old >> 32), (uint32_t)(v >> 32));
+  return ((uint64_t)hi << 32) | lo;
+}
+
+__device__ __forceinline__ uint64_t lane63(uint64_t v) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), 63);
+  return ((uint64_t)hi << 32) | lo;
+}
+
+// Each step combines a lane with one below it (rows of 16 lanes by shifts of
+// 1, 2, 4 and 8, then across rows), so lane 63 ends with the whole
+// wavefront's value.  A lane with no source keeps `old`.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint64_t max_step(uint64_t v) {
+  return max(v, dpp64<CTRL, ROWS>(v, v));
+}
+
+__device__ __forceinline__ uint64_t wave_max64(uint64_t v) {
+  v = max_step<0x111, 0xF>(v);
+  v = max_step<0x112, 0xF>(v);
+  v = max_step<0x114, 0xF>(v);
+  v = max_step<0x118, 0xF>(v);
+  v = max_step<0x142, 0xA>(v);
+  v = max_step<0x143, 0xC>(v);
+  return lane63(v);
+}
+
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double sum_step(double v) {
+  const uint64_t t = dpp64<CTRL, ROWS>(0, __builtin_bit_cast(uint64_t, v));
+  return v + __builtin_bit_cast(double, t);
+}
+
+__device__ __forceinline__ double wave_sum64(double v) {
+  v = sum_step<0x111, 0xF>(v);
+  v = sum_step<0x112, 0xF>(v);
+  v = sum_step<0x114, 0xF>(v);
+  v = sum_step<0x118, 0xF>(v);
+  v = sum_step<0x142, 0xA>(v);
+  v = sum_step<0x143, 0xC>(v);
+  return __builtin_bit_cast(double, lane63(__builtin_bit_cast(uint64_t, v)));
+}
+
+// ------------------------------------------------------------ ordered keys
+
+// Integer whose unsigned order is the order of the value.  Key 0 stands for
+// "not to be chosen": no value above -inf maps to it.
+__device__ __forceinline__ uint64_t key_of(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v + 0.0);  // -0 is 0
+  const uint64_t k = (b >> 63) ? ~b : b | (1ull << 63);
+  return v > -__builtin_inf() ? k : 0;
+}
+
+__device__ __forceinline__ double value_of(uint64_t k) {
+  const uint64_t b = (k >> 63) ? k & ~(1ull << 63) : ~k;
+  return __builtin_bit_cast(double, b);
+}
+
+// --------------------------------------------------------------- row access
+
+// The lane's PER logits from e0 on; -inf (never chosen, score 0) past E and
+// for NaN; +inf counts as the largest finite value.
+template <int PER, bool BF16>
+__device__ __forceinline__ void load_logits(const void* row, int E, int e0,
+                                            bool vec, float (&l)[PER]) {
+  float raw[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) raw[i] = -__builtin_inff();
+  if constexpr (BF16) {
+    const uint16_t* p = static_cast<const uint16_t*>(row);
+    if (PER % 4 == 0 && vec && e0 + PER <= E) {
+#pragma unroll
+      for (int i = 0; i + 3 < PER; i += 4) {
+        const uint2 w = *reinterpret_cast<const uint2*>(p + e0 + i);
+        raw[i] = bf16_lo(w.x);
+        raw[i + 1] = bf16_hi(w.x);
+        raw[i + 2] = bf16_lo(w.y);
+        raw[i + 3] = bf16_hi(w.y);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (e0 + i < E) raw[i] = __uint_as_float((uint32_t)p[e0 + i] << 16);
+    }
+  } else {
+    const float* p = static_cast<const float*>(row);
+    if (PER % 4 == 0 && vec && e0 + PER <= E) {
+#pragma unroll
+      for (int i = 0; i + 3 < PER; i += 4) {
+        const float4 w = *reinterpret_cast<const float4*>(p + e0 + i);
+        raw[i] = w.x;
+        raw[i + 1] = w.y;
+        raw[i + 2] = w.z;
+        raw[i + 3] = w.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (e0 + i < E) raw[i] = p[e0 + i];
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const float v = raw[i];
+    l[i] = v != v ? -__builtin_inff() : (v > kFltMax ? kFltMax : v);
+  }
+}
+
+template <int PER, bool BF16>
+__device__ __forceinline__ void store_row(void* row, int E, int e0, bool vec,
+                                          const float (&g)[PER]) {
+  if constexpr (BF16) {
+    uint16_t* p = static_cast<uint16_t*>(row);
+    uint16_t h[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      h[i] = __builtin_bit_cast(uint16_t, (__bf16)g[i]);
+    if (PER % 4 == 0 && vec && e0 + PER <= E) {
+#pragma unroll
+      for (int i = 0; i + 3 < PER; i += 4)
+        *reinterpret_cast<uint2*>(p + e0 + i) =
+            uint2{(uint32_t)h[i] | ((uint32_t)h[i + 1] << 16),
+                  (uint32_t)h[i + 2] | ((uint32_t)h[i + 3] << 16)};
+    } else {
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (e0 + i < E) p[e0 + i] = h[i];
+    }
+  } else {
+    float* p = static_cast<float*>(row);
+    if (PER % 4 == 0 && vec && e0 + PER <= E) {
+#pragma unroll
+      for (int i = 0; i + 3 < PER; i += 4)
+        *reinterpret_cast<float4*>(p + e0 + i) =
+            float4{g[i], g[i + 1], g[i + 2], g[i + 3]};
+    } else {
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (e0 + i < E) p[e0 + i] = g[i];
+    }
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ float logit_at(const void* row, int e) {
+  float v;
+  if constexpr (BF16)
+    v = __uint_as_float(
+        (uint32_t)static_cast<const uint16_t*>(row)[e] << 16);
+  else
+    v = static_cast<const float*>(row)[e];
+  return v != v ? -__builtin_inff() : (v > kFltMax ? kFltMax : v);
+}
+
+__device__ __forceinline__ double sigmoid64(float l) {
+  return 1.0 / (1.0 + exp(-(double)l));
+}
+
+// ------------------------------------------------------------------ forward
+
+struct RouteArgs {
+  const void* logits;
+  int64_t ld;  // elements
+  int64_t T;
+  int32_t E, K;
+  int32_t sigmoid;
+  const float* bias;  // or null
+  int32_t groups, top_groups;
+  int32_t renorm;
+  float scale;
+  int32_t vec;  // rows start on 16 bytes
+  int32_t* ids;
+  float* weights;
+};
+
+constexpr int kMaxGroups = 64;
+
+template <int PER, bool BF16>
+__global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int64_t t = (int64_t)blockIdx.x * (blockDim.x >> 6) +
+                    __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (t >= a.T) return;
+  const int E = a.E;
+  const int e0 = lane * PER;
+  const char* row = static_cast<const char*>(a.logits) +
+                    t * a.ld * (BF16 ? 2 : 4);
+  float l[PER];
+  load_logits<PER, BF16>(row, E, e0, a.vec != 0, l);
+
+  // the row's maximum, for the softmax's exponentials
+  float top = -__builtin_inff();
+  double z = 0.0;
+  const bool plain = !a.sigmoid && a.bias == nullptr && a.groups == 1;
+  if (!a.sigmoid) {
+    float m = l[0];
+#pragma unroll
+    for (int i = 1; i < PER; ++i) m = fmaxf(m, l[i]);
+    const uint64_t k = wave_max64(key_of((double)m));
+    top = k ? (float)value_of(k) : 0.0f;
+  }
+
+  uint64_t key[PER];
+  if (plain) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) key[i] = key_of((double)l[i]);
+    if (!a.renorm) {
+      double part = 0.0;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) part += exp((double)l[i] - (double)top);
+      z = wave_sum64(part);
+    }
+  } else {
+    double s[PER];
+    if (a.sigmoid) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) s[i] = sigmoid64(l[i]);
+    } else {
+      double part = 0.0;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        s[i] = exp((double)l[i] - (double)top);
+        part += s[i];
+      }
+      z = wave_sum64(part);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) s[i] = s[i] / z;
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const bool live = l[i] > -__builtin_inff();
+      double c = s[i];
+      if (a.bias != nullptr && e0 + i < E) c += (double)a.bias[e0 + i];
+      key[i] = live ? key_of(c) : 0;
+    }
+  }
+
+  if (a.groups > 1) {
+    // Group value: the sum of the group's two largest choice values.  A
+    // group without a live expert has none and is kept only when too few
+    // groups have one (nothing of it can be chosen either way).
+    const int gs = E / a.groups;
+    uint64_t mine = 0;  // lane g: the key of group g's value
+    for (int g = 0; g < a.groups; ++g) {
+      const int lo = g * gs, hi = lo + gs;
+      uint64_t m1 = 0;
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (e0 + i >= lo && e0 + i < hi) m1 = max(m1, key[i]);
+      const uint64_t first = wave_max64(m1);
+      uint64_t gk = 0;
+      if (first != 0) {
+        // the lowest lane that holds it drops its first copy
+        const bool owner =
+            lane == __ffsll((unsigned long long)__ballot(m1 == first)) - 1;
+        bool dropped = !owner;
+        uint64_t m2 = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          if (e0 + i < lo || e0 + i >= hi) continue;
+          if (!dropped && key[i] == first)
+            dropped = true;
+          else
+            m2 = max(m2, key[i]);
+        }
+        const uint64_t second = wave_max64(m2);
+        gk = key_of(value_of(first) + (second ? value_of(second) : 0.0));
+      }
+      if (lane == g) mine = gk;
+    }
+    uint64_t kept = 0;  // bit g: group g may be chosen from
+    for (int n = 0; n < a.top_groups; ++n) {
+      const uint64_t best = wave_max64(mine);
+      if (best == 0) break;
+      const int g = __ffsll((unsigned long long)__ballot(mine == best)) - 1;
+      kept |= 1ull << g;
+      if (lane == g) mine = 0;
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int g = min((e0 + i) / gs, kMaxGroups - 1);
+      if (!((kept >> g) & 1)) key[i] = 0;
+    }
+  }
+
+  // K choices; lane j keeps the j-th
+  int my_id = -1;
+  float my_l = -__builtin_inff();
+  for (int j = 0; j < a.K; ++j) {
+    uint64_t m = key[0];
+#pragma unroll
+    for (int i = 1; i < PER; ++i) m = max(m, key[i]);
+    const uint64_t best = wave_max64(m);
+    if (best == 0) break;  // nothing left: ids from here on stay -1
+    const int from = __ffsll((unsigned long long)__ballot(m == best)) - 1;
+    int at = 0;
+    float lv = 0.0f;
+    bool found = false;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      if (!found && key[i] == best) {
+        found = true;
+        at = i;
+        lv = l[i];
+        if (lane == from) key[i] = 0;
+      }
+    }
+    const int id = from * PER + __builtin_amdgcn_readlane(at, from);
+    const int lb =
+        __builtin_amdgcn_readlane(__builtin_bit_cast(int, lv), from);
+    if (lane == j) {
+      my_id = id;
+      my_l = __builtin_bit_cast(float, lb);
+    }
+  }
+
+  double p = 0.0;
+  if (my_id >= 0) {
+    if (a.sigmoid) {
+      p = sigmoid64(my_l);
+    } else {
+      p = exp((double)my_l - (double)top);
+      if (!a.renorm) p = p / z;
+    }
+  }
+  if (a.renorm) {
+    const double total = wave_sum64(p);
+    p = total > 0.0 ? p / total : 0.0;
+  }
+  if (lane < a.K) {
+    a.ids[t * a.K + lane] = my_id;
+    a.weights[t * a.K + lane] = (float)((double)a.scale * p);
+  }
+}
+
+// ----------------------------------------------------------------- backward
+
+struct RouteBackArgs {
+  const float* grad;  // [T, K]
+  const void* logits;
+  int64_t ld;
+  const int32_t* ids;
+  int64_t T;
+  int32_t E, K;
+  int32_t sigmoid, renorm;
+  float scale;
+  int32_t vec_in, vec_out;
+  void* out;
+  int64_t ld_out;
+};
+
+// With q_j the chosen scores over their sum: renormalized weights give
+// ds_j = scale / sum * (g_j - sum_i q_i g_i), others ds_j = scale * g_j.
+// Sigmoid scores: dl_j = ds_j s_j (1 - s_j).  Softmax scores: the
+// renormalized form depends on the chosen logits alone, dl_j = scale * q_j *
+// (g_j - sum_i q_i g_i); the other reads the whole row, dl_e = scale * p_e *
+// (g_e [e chosen] - sum_j p_j g_j).  In 64 bits, rounded once.
+template <int PER, bool BF16>
+__global__ __launch_bounds__(256) void route_backward_kernel(RouteBackArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int64_t t = (int64_t)blockIdx.x * (blockDim.x >> 6) +
+                    __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (t >= a.T) return;
+  const int E = a.E;
+  const int e0 = lane * PER;
+  const char* row = static_cast<const char*>(a.logits) +
+                    t * a.ld * (BF16 ? 2 : 4);
+  char* out = static_cast<char*>(a.out) + t * a.ld_out * (BF16 ? 2 : 4);
+  int id = -1;
+  double g = 0.0;
+  float lj = -__builtin_inff();
+  if (lane < a.K) {
+    id = a.ids[t * a.K + lane];
+    if (id < 0 || id >= E) {
+      id = -1;
+    } else {
+      g = (double)a.grad[t * a.K + lane];
+      lj = logit_at<BF16>(row, id);
+    }
+  }
+  const bool has = lj > -__builtin_inff();
+  double d = 0.0;  // gradient of the lane's chosen logit
+  float res[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) res[i] = 0.0f;
+  if (a.sigmoid) {
+    const double s = has ? sigmoid64(lj) : 0.0;
+    double ds = (double)a.scale * g;
+    if (a.renorm) {
+      const double total = wave_sum64(s);
+      const double inv = total > 0.0 ? 1.0 / total : 0.0;
+      ds = (double)a.scale * inv * (g - wave_sum64(s * inv * g));
+    }
+    d = has ? ds * s * (1.0 - s) : 0.0;
+  } else if (a.renorm) {
+    const uint64_t k = wave_max64(key_of((double)lj));
+    const double top = k ? value_of(k) : 0.0;
+    const double x = has ? exp((double)lj - top) : 0.0;
+    const double total = wave_sum64(x);
+    const double q = total > 0.0 ? x / total : 0.0;
+    d = (double)a.scale * q * (g - wave_sum64(q * g));
+  } else {
+    float l[PER];
+    load_logits<PER, BF16>(row, E, e0, a.vec_in != 0, l);
+    float m = l[0];
+#pragma unroll
+    for (int i = 1; i < PER; ++i) m = fmaxf(m, l[i]);
+    const uint64_t k = wave_max64(key_of((double)m));
+    const double top = k ? value_of(k) : 0.0;
+    double part = 0.0;
+    double x[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      x[i] = exp((double)l[i] - top);
+      part += x[i];
+    }
+    const double z = wave_sum64(part);
+    const double inv = z > 0.0 ? 1.0 / z : 0.0;
+    const double pj = has ? exp((double)lj - top) * inv : 0.0;
+    d = (double)a.scale * pj * g;
+    const double dot = wave_sum64(pj * g) * (double)a.scale;
+    double full[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) full[i] = -x[i] * inv * dot;
+    for (int j = 0; j < a.K; ++j) {
+      const int idj = __builtin_amdgcn_readlane(id, j);
+      const uint64_t db = __builtin_bit_cast(uint64_t, d);
+      const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)db, j);
+      const uint32_t hi =
+          (uint32_t)__builtin_amdgcn_readlane((int)(db >> 32), j);
+      const double dj =
+          __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        if (idj == e0 + i) full[i] += dj;
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) res[i] = (float)full[i];
+    store_row<PER, BF16>(out, E, e0, a.vec_out != 0, res);
+    return;
+  }
+  // An id that occurs twice adds up.
+  const float df = (float)d;
+  for (int j = 0; j < a.K; ++j) {
+    const int idj = __builtin_amdgcn_readlane(id, j);
+    const float dj = __builtin_bit_cast(
+        float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, df), j));
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      if (idj == e0 + i) res[i] += dj;
+  }
+  store_row<PER, BF16>(out, E, e0, a.vec_out != 0, res);
+}
+
+// Wavefronts per block: four once there are more tokens than CUs; below
+// that one, so that every token has a CU of its own.
+inline int route_waves(int64_t T) { return T > 256 ? 4 : 1; }
+
+inline bool row_vec(const void* p, int64_t ld, int64_t esz) {
+  return aligned16(p) && (ld * esz) % 16 == 0;
+}
+
+template <bool BF16, typename F>
+void by_experts(int32_t E, F&& f) {
+  if (E <= 64)
+    f(std::integral_constant<int, 1>{});
+  else if (E <= 128)
+    f(std::integral_constant<int, 2>{});
+  else if (E <= 256)
+    f(std::integral_constant<int, 4>{});
+  else if (E <= 512)
+    f(std::integral_constant<int, 8>{});
+  else
+    f(std::integral_constant<int, 16>{});
+}
+
+}  // namespace
+
+extern "C" mxq_status moe_route(const void* logits, mxq_out_dtype dtype,
+                                int64_t ld_logits, int64_t T, int32_t E,
+                                int32_t K, mxq_score_fn score,
+                                const float* bias, int32_t num_groups,
+                                int32_t top_groups, int32_t renormalize,
+                                float weight_scale, int32_t* topk_ids,
+                                float* topk_weights, void* stream) {
+  if (dtype != MXQ_OUT_BF16 && dtype != MXQ_OUT_F32)
+    return MXQ_ERR_UNSUPPORTED;
+  if (score != MXQ_SCORE_SOFTMAX && score != MXQ_SCORE_SIGMOID)
+    return MXQ_ERR_UNSUPPORTED;
+  if (T < 0 || T > INT32_MAX || E < 1 || K < 1 || K > MXQ_MAX_TOPK || K > E ||
+      num_groups < 1 || num_groups > E || E % num_groups != 0 ||
+      top_groups < 1 || top_groups > num_groups ||
+      K > E / num_groups * top_groups)
+    return MXQ_ERR_INVALID_ARGUMENT;
+  if (E > MXQ_MAX_ROUTE_EXPERTS || num_groups > kMaxGroups)
+    return MXQ_ERR_UNSUPPORTED;
+  if (T == 0) return MXQ_OK;
+  if (logits == nullptr || topk_ids == nullptr || topk_weights == nullptr ||
+      ld_logits < E)
+    return MXQ_ERR_INVALID_ARGUMENT;
+  const int waves = route_waves(T);
+  RouteArgs a{logits,     ld_logits,  T,
+              E,          K,          score == MXQ_SCORE_SIGMOID,
+              bias,       num_groups, top_groups,
+              renormalize != 0, weight_scale,
+              row_vec(logits, ld_logits, dtype == MXQ_OUT_BF16 ? 2 : 4),
+              topk_ids,   topk_weights};
+  const unsigned blocks = (unsigned)ceil_div(T, waves);
+  hipStream_t s = as_stream(stream);
+  if (dtype == MXQ_OUT_BF16)
+    by_experts<true>(E, [&](auto per) {
+      route_kernel<decltype(per)::value, true>
+          <<<blocks, waves * 64, 0, s>>>(a);
+    });
+  else
+    by_experts<false>(E, [&](auto per) {
+      route_kernel<decltype(per)::value, false>
+          <<<blocks, waves * 64, 0, s>>>(a);
+    });
+  return launch_status();
+}
+
+extern "C" mxq_status moe_route_backward(
+    const float* grad_weights, const void* logits, mxq_out_dtype dtype,
+    int64_t ld_logits, const int32_t* topk_ids, int64_t T, int32_t E,
+    int32_t K, mxq_score_fn score, int32_t renormalize, float weight_scale,
+    void* grad_logits, int64_t ld_grad, void* stream) {
+  if (dtype != MXQ_OUT_BF16 && dtype != MXQ_OUT_F32)
+    return MXQ_ERR_UNSUPPORTED;
+  if (score != MXQ_SCORE_SOFTMAX && score != MXQ_SCORE_SIGMOID)
+    return MXQ_ERR_UNSUPPORTED;
+  if (T < 0 || T > INT32_MAX || E < 1 || K < 1 || K > MXQ_MAX_TOPK)
+    return MXQ_ERR_INVALID_ARGUMENT;
+  if (E > MXQ_MAX_ROUTE_EXPERTS) return MXQ_ERR_UNSUPPORTED;
+  if (T == 0) return MXQ_OK;
+  if (grad_weights == nullptr || logits == nullptr || topk_ids == nullptr ||
+      grad_logits == nullptr || ld_logits < E || ld_grad < E)
+    return MXQ_ERR_INVALID_ARGUMENT;
+  const int64_t esz = dtype == MXQ_OUT_BF16 ? 2 : 4;
+  const int waves = route_waves(T);
+  RouteBackArgs a{grad_weights, logits, ld_logits, topk_ids, T, E, K,
+                  score == MXQ_SCORE_SIGMOID, renormalize != 0, weight_scale,
+                  row_vec(logits, ld_logits, esz),
+                  row_vec(grad_logits, ld_grad, esz), grad_logits, ld_grad};
+  const unsigned blocks = (unsigned)ceil_div(T, waves);
+  hipStream_t s = as_stream(stream);
+  if (dtype == MXQ_OUT_BF16)
+    by_experts<true>(E, [&](auto per) {
+      route_backward_kernel<decltype(per)::value, true>
+          <<<blocks, waves * 64, 0, s>>>(a);
+    });
+  else
+    by_experts<false>(E, [&](auto per) {
+      route_backward_kernel<decltype(per)::value, false>
+          <<<blocks, waves * 64, 0, s>>>(a);
+    });
+  return launch_status();
+}

@@ -54,6 +54,7 @@ extern "C" {
 #define MXQ_MAX_TOPK 64
 #define MXQ_MAX_ASSIGNMENTS (1 << 24) /* T*K limit of moe_layout */
 #define MXQ_MAX_HIDDEN 32768 /* moe_scatter_quant stages one row in LDS */
+#define MXQ_MAX_ROUTE_EXPERTS 1024 /* moe_route: global experts of a row */
 /* Static device scratch of moe_layout_noalloc, per device (1 MiB). */
 #define MXQ_LAYOUT_NOALLOC_SCRATCH_BYTES (1u << 20)
 
@@ -85,6 +86,9 @@ typedef enum { MXQ_RULE_NO_CLIP = 0, MXQ_RULE_OCP_FLOOR = 1 } mxq_scale_rule;
 
 typedef enum { MXQ_OUT_BF16 = 0, MXQ_OUT_F32 = 1 } mxq_out_dtype;
 
+/* Score function of the router. */
+typedef enum { MXQ_SCORE_SOFTMAX = 0, MXQ_SCORE_SIGMOID = 1 } mxq_score_fn;
+
 /* ------------------------------------------------------------ host-only */
 
 /* Static row count of the compact layout that no routing can exceed
@@ -110,6 +114,51 @@ size_t moe_layout_workspace_bytes(int64_t T, int32_t K, int32_t E);
 
 /* Workspace bytes requant_per_token_to_per_tensor needs. */
 size_t requant_workspace_bytes(int64_t T, int32_t H);
+
+/* ----------------------------------------------------------------- router */
+
+/* Top-k routing in front of the layout: what moe_layout takes as topk_ids
+ * and moe_combine as topk_weights, from the router's logits.
+ *
+ *   logits        bf16 or fp32 (dtype) [T, ld_logits], the first E columns.
+ *   score         s_e = softmax over the row, or 1 / (1 + exp(-l_e)).
+ *   bias          fp32 [E] or NULL, added to the scores for the choice only.
+ *   num_groups    G groups of E/G consecutive experts; with G > 1 only
+ *   top_groups    experts of the top_groups groups with the largest sum of
+ *                 their two largest choice values may be chosen.
+ *   topk_ids      int32 [T, K]: the K largest choice values, largest first;
+ *                 equal values by lowest index (groups too).
+ *   topk_weights  fp32 [T, K]: weight_scale * s, divided by the sum of the
+ *                 chosen s if renormalize != 0 (0 if that sum is 0).
+ * Choice values are s_e (+ bias_e) in fp64; without bias and groups a softmax
+ * chooses by the logits, whose order it keeps.  An expert whose logit or
+ * choice value is -inf or NaN is never chosen: where fewer than K are left
+ * the id is -1 (which moe_layout skips) and the weight 0.  A logit of +inf
+ * counts as the largest finite value.
+ * 1 <= K <= min(MXQ_MAX_TOPK, E / G * top_groups), E % G == 0;
+ * E <= MXQ_MAX_ROUTE_EXPERTS and G <= 64, else MXQ_ERR_UNSUPPORTED. */
+mxq_status moe_route(const void* logits, mxq_out_dtype dtype,
+                     int64_t ld_logits, int64_t T, int32_t E, int32_t K,
+                     mxq_score_fn score, const float* bias,
+                     int32_t num_groups, int32_t top_groups,
+                     int32_t renormalize, float weight_scale,
+                     int32_t* topk_ids, float* topk_weights, void* stream);
+
+/* Gradient of moe_route's weights to its logits, the ids held fixed.
+ *
+ *   grad_weights  fp32 [T, K]; logits, topk_ids, score, renormalize and
+ *                 weight_scale as in the forward call.
+ *   grad_logits   [T, ld_grad] in the logits' dtype: all E columns of every
+ *                 row are written.  Ids outside [0, E) add nothing; an id
+ *                 that occurs twice in a row adds up.
+ * grad_logits must not overlap logits. */
+mxq_status moe_route_backward(const float* grad_weights, const void* logits,
+                              mxq_out_dtype dtype, int64_t ld_logits,
+                              const int32_t* topk_ids, int64_t T, int32_t E,
+                              int32_t K, mxq_score_fn score,
+                              int32_t renormalize, float weight_scale,
+                              void* grad_logits, int64_t ld_grad,
+                              void* stream);
 
 /* ----------------------------------------------------------------- layout */
 
@@ -392,6 +441,47 @@ mxq_status moe_combine(const void* y_bf16, int64_t ld_y, int64_t num_rows,
                        const int32_t* src2dst, const float* topk_weights,
                        int64_t T, int32_t K, int32_t H, void* out,
                        int64_t ld_out, mxq_out_dtype out_dtype, void* stream);
+
+/* ----------------------------------------------------------- gradients */
+
+/* Gradient of the expert sort (row src2dst[t, j] of the layout takes token
+ * row t, as moe_scatter_rows writes it):
+ *   grad_x[t, i] = sum over j of grad_rows[src2dst[t, j], i],
+ * summed in fp32 in ascending j and rounded once.
+ *
+ *   grad_rows  bf16 or fp32 (rows_dtype) [num_rows, ld_rows].
+ *   src2dst    int32 [T, K]; entries < 0 or >= num_rows add nothing.
+ *   grad_x     bf16 or fp32 (x_dtype) [T, ld_x]; a token without a row gets 0.
+ * H must be a multiple of 8; rows start on 16 bytes. */
+mxq_status moe_scatter_rows_backward(const void* grad_rows,
+                                     mxq_out_dtype rows_dtype, int64_t ld_rows,
+                                     int64_t num_rows, const int32_t* src2dst,
+                                     int64_t T, int32_t K, int32_t H,
+                                     void* grad_x, int64_t ld_x,
+                                     mxq_out_dtype x_dtype, void* stream);
+
+/* Gradient of moe_combine.  For every (t, j) with d = src2dst[t, j] in
+ * [0, num_rows):
+ *   grad_y[d, i]       = bf16(topk_weights[t, j] * grad_out[t, i])
+ *   grad_weights[t, j] = sum over i of grad_out[t, i] * y[d, i]   (fp32)
+ * and grad_weights[t, j] = 0 for the others.
+ *
+ *   grad_out      bf16 or fp32 (grad_dtype) [T, ld_g].
+ *   y             bf16 [num_rows, ld_y]; may be NULL without grad_weights.
+ *   topk_weights  fp32 [T, K]; may be NULL without grad_y.
+ *   grad_y        bf16 [num_rows, ld_gy] or NULL.  Rows that are no
+ *                 destination are not written.  Must not overlap y.
+ *   grad_weights  fp32 [T, K] or NULL.
+ * Destinations must be distinct, as moe_layout makes them: a row named
+ * twice gets one of its gradients, not their sum.  H must be a multiple of 8
+ * and at most MXQ_MAX_HIDDEN (else MXQ_ERR_UNSUPPORTED). */
+mxq_status moe_combine_backward(const void* grad_out, mxq_out_dtype grad_dtype,
+                                int64_t ld_g, const void* y_bf16, int64_t ld_y,
+                                int64_t num_rows, const int32_t* src2dst,
+                                const float* topk_weights, int64_t T,
+                                int32_t K, int32_t H, void* grad_y_bf16,
+                                int64_t ld_gy, float* grad_weights,
+                                void* stream);
 
 /* ------------------------------------------------ psum (expanded) layout */
 
