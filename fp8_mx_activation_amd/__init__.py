@@ -33,7 +33,8 @@ __all__ = [
     "mxq_copy16", "moe_layout_scatter_quant", "moe_layout_noalloc",
     "mxq_gather_read16", "mxq_fill_rows16", "SCORE_FNS", "moe_route",
     "moe_route_backward", "moe_scatter_rows_backward",
-    "moe_combine_backward",
+    "moe_combine_backward", "ACTIVATIONS", "moe_expert_matmul",
+    "moe_expert_matmul_quant",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -111,6 +112,12 @@ _SIGNATURES = {
                                          _i32, _p, _i64, _i32, _p]),
     "moe_combine_backward": (_i32, [_p, _i32, _i64, _p, _i64, _i64, _p, _p,
                                     _i64, _i32, _i32, _p, _i64, _p, _p]),
+    "moe_expert_matmul": (_i32, [_p, _i64, _p, _i64, _i64, _i32, _p, _p, _i32,
+                                 _i32, _i32, _p, _p, _p, _i32, _p, _i64, _i64,
+                                 _p, _i64, _p]),
+    "moe_expert_matmul_quant": (_i32, [_p, _i64, _p, _i64, _i64, _i32, _p, _p,
+                                       _i32, _i32, _i32, _p, _p, _p, _i32,
+                                       _i64, _i32, _p, _i64, _p, _i64, _p]),
     "mxq_status_string": (ctypes.c_char_p, [_i32]),
     "mxq_abi_version": (_i32, []),
 }
@@ -828,6 +835,113 @@ def requant_per_token_to_per_tensor(q_in: torch.Tensor,
         _stream(qi))
     _check("requant_per_token_to_per_tensor", st)
     return q_out, tensor_scale
+
+
+# -------------------------------------------------------- experts' products
+
+ACTIVATIONS = {"none": 0, "silu": 1, "silu_mul": 2}
+
+
+def _matmul_inputs(q, scales, w, w_scales, expert_offsets, counts, fmt, act,
+                   bias, expected_m):
+    """Checked inputs of the experts' products: the C call's leading
+    arguments and the shape (rows, output columns)."""
+    _dev(q, "q")
+    _dev(scales, "scales", q)
+    code, G = SCALE_FORMATS[fmt]
+    ld_q = _rows(q, "q", _FP8)
+    ld_s = _rows(scales, "scales", _SCALE)
+    rows, H = q.shape
+    _at_least(scales, "scales", rows, H // G)
+    _dev(w, "w", q)
+    if w.dtype not in _FP8 or w.dim() != 3 or w.shape[2] != H or \
+            not w.is_contiguous():
+        raise ValueError("w must be contiguous fp8 [E, N, %d]" % H)
+    E, N, _ = w.shape
+    _dev(w_scales, "w_scales", q)
+    blocks = (E, -(-N // 128), -(-H // 128))
+    if w_scales.dtype not in _SCALE or tuple(w_scales.shape) != blocks or \
+            not w_scales.is_contiguous():
+        raise ValueError("w_scales must be contiguous uint8 %s"
+                         % (list(blocks),))
+    _dense(expert_offsets, "expert_offsets", torch.int32, (E + 1,), q)
+    _dense(counts, "counts", torch.int32, (E,), q)
+    if bias is not None:
+        _dense(bias, "bias", torch.float32, (E, N), q)
+    a = ACTIVATIONS[act]
+    if expected_m is None:
+        expected_m = -(-rows // E) if E else 0
+    args = (_ptr(q), ld_q, _ptr(scales), ld_s, rows, code, _ptr(w),
+            _ptr(w_scales), E, N, H, _ptr(expert_offsets), _ptr(counts),
+            _ptr(bias), a)
+    return args, rows, N // 2 if act == "silu_mul" else N, expected_m
+
+
+def moe_expert_matmul(q: torch.Tensor, scales: torch.Tensor, w: torch.Tensor,
+                      w_scales: torch.Tensor, expert_offsets: torch.Tensor,
+                      counts: torch.Tensor, fmt: str = "ue8m0_g128",
+                      act: str = "none", bias: torch.Tensor | None = None,
+                      residual: torch.Tensor | None = None,
+                      out: torch.Tensor | None = None,
+                      expected_m: int | None = None) -> torch.Tensor:
+    """Product of a layout's quantized rows ``q [num_rows, H]`` (with
+    ``scales`` in format ``fmt``) with the weights ``w [E, N, H]`` of their
+    experts (``w_scales`` as ``requant_weight_block_ue8m0`` returns them):
+    bf16 ``out [num_rows, N]``, or N/2 columns with ``act="silu_mul"``.
+    ``expert_offsets`` and ``counts`` are the layout's (``masked_m`` for a
+    slab); ``bias`` is float32 [E, N], ``residual`` bf16 rows added after the
+    activation.  Rows that hold no assignment keep the contents of a given
+    ``out``.  ``expected_m``, the rows a busy expert is expected to hold,
+    picks the kernel's shape; by default num_rows / E."""
+    args, rows, cols, m = _matmul_inputs(q, scales, w, w_scales,
+                                         expert_offsets, counts, fmt, act,
+                                         bias, expected_m)
+    ld_r = 0
+    if residual is not None:
+        _dev(residual, "residual", q)
+        ld_r = _rows(residual, "residual", (torch.bfloat16,))
+        _at_least(residual, "residual", rows, cols)
+    if out is None:
+        out = torch.empty((rows, cols), dtype=torch.bfloat16, device=q.device)
+    _dev(out, "out", q)
+    ld_o = _rows(out, "out", (torch.bfloat16,))
+    _at_least(out, "out", rows, cols)
+    _call("moe_expert_matmul", q, *args, _ptr(residual), ld_r, m, _ptr(out),
+          ld_o)
+    return out
+
+
+def moe_expert_matmul_quant(q: torch.Tensor, scales: torch.Tensor,
+                            w: torch.Tensor, w_scales: torch.Tensor,
+                            expert_offsets: torch.Tensor,
+                            counts: torch.Tensor, fmt: str = "ue8m0_g128",
+                            act: str = "silu_mul",
+                            bias: torch.Tensor | None = None,
+                            out_fmt: str = "ue8m0_g128",
+                            q_out: torch.Tensor | None = None,
+                            scales_out: torch.Tensor | None = None,
+                            expected_m: int | None = None):
+    """``moe_expert_matmul`` with its rows quantized for the next product:
+    ``(q_out, scales_out)`` in format ``out_fmt``, row-major, from the fp32
+    values."""
+    args, rows, cols, m = _matmul_inputs(q, scales, w, w_scales,
+                                         expert_offsets, counts, fmt, act,
+                                         bias, expected_m)
+    code, G = SCALE_FORMATS[out_fmt]
+    if q_out is None:
+        q_out = _empty_rows_u8(rows, cols, q.device)
+    if scales_out is None:
+        scales_out = torch.empty((rows, cols // G), dtype=torch.uint8,
+                                 device=q.device)
+    _dev(q_out, "q_out", q)
+    _dev(scales_out, "scales_out", q)
+    ld_o = _rows(q_out, "q_out", _FP8)
+    ld_so = _rows(scales_out, "scales_out", _SCALE)
+    _at_least(q_out, "q_out", rows, cols)
+    _at_least(scales_out, "scales_out", rows, cols // G)
+    _call("moe_expert_matmul_quant", q, *args, m, code, _ptr(q_out), ld_o,
+          _ptr(scales_out), ld_so)
+    return q_out, scales_out
 
 
 def moe_combine(y: torch.Tensor, src2dst: torch.Tensor,

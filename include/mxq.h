@@ -54,6 +54,7 @@ extern "C" {
 #define MXQ_MAX_TOPK 64
 #define MXQ_MAX_ASSIGNMENTS (1 << 24) /* T*K limit of moe_layout */
 #define MXQ_MAX_HIDDEN 32768 /* moe_scatter_quant stages one row in LDS */
+#define MXQ_MAX_MATMUL_LD (1 << 22) /* moe_expert_matmul: row stride, bytes */
 #define MXQ_MAX_ROUTE_EXPERTS 1024 /* moe_route: global experts of a row */
 /* Static device scratch of moe_layout_noalloc, per device (1 MiB). */
 #define MXQ_LAYOUT_NOALLOC_SCRATCH_BYTES (1u << 20)
@@ -85,6 +86,15 @@ typedef enum {
 typedef enum { MXQ_RULE_NO_CLIP = 0, MXQ_RULE_OCP_FLOOR = 1 } mxq_scale_rule;
 
 typedef enum { MXQ_OUT_BF16 = 0, MXQ_OUT_F32 = 1 } mxq_out_dtype;
+
+/* Activation of the experts' products.  MXQ_ACT_SILU_MUL takes the first
+ * half of the N outputs as gate, the second as factor: silu(a[n]) *
+ * a[N/2 + n], N/2 columns; silu(x) = x / (1 + exp(-x)). */
+typedef enum {
+  MXQ_ACT_NONE = 0,
+  MXQ_ACT_SILU = 1,
+  MXQ_ACT_SILU_MUL = 2
+} mxq_act;
 
 /* Score function of the router. */
 typedef enum { MXQ_SCORE_SOFTMAX = 0, MXQ_SCORE_SIGMOID = 1 } mxq_score_fn;
@@ -421,6 +431,68 @@ mxq_status requant_per_token_to_per_tensor(
     const void* q_in_fp8, int64_t ld_in, const float* token_scales, int64_t T,
     int32_t H, void* q_out_fp8, int64_t ld_out, float* tensor_scale,
     void* workspace, size_t workspace_bytes, void* stream);
+
+/* --------------------------------------------------- experts' products */
+
+/* Product of the layout's quantized rows with each expert's weights, with
+ * the end of the row fused [P1 impl. items 2-3: the grouped product consumes
+ * the rows the scatter wrote; P4 impl. item 3: fp8 rows with e8m0 scales go
+ * into it as they are].  For the live rows r of expert e, in fp32:
+ *   a[r, n] = sum over k of dec(q[r, k]) * dec(w[e, n, k]) + bias[e, n]
+ *   out[r]  = bf16(act(a[r]) + residual[r])
+ *
+ *   q_fp8, scales   e4m3 [num_rows, ld_q] and scale bytes [num_rows, ld_s]
+ *                   in format fmt, row-major, as moe_scatter_quant,
+ *                   moe_layout_scatter_quant and mx_quant_live_rows write
+ *                   them.  H must be a multiple of the group.
+ *   w_fp8, w_scales e4m3 [E, N, H] and one scale byte per 128 x 128 block
+ *                   [E, ceil(N/128), ceil(H/128)], contiguous, as
+ *                   requant_weight_block_ue8m0 writes them.
+ *   expert_offsets  int32 [E + 1] and
+ *   counts          int32 [E], from moe_layout: counts (compact) or masked_m
+ *                   (masked; a slab drops what exceeds its capacity).  The
+ *                   live rows of expert e are the first counts[e] from
+ *                   expert_offsets[e], at most up to expert_offsets[e + 1]
+ *                   and num_rows.  Regions must not overlap.
+ *   bias            fp32 [E, N] or NULL.
+ *   residual        bf16 [num_rows, ld_r] or NULL; may be out itself (same
+ *                   stride).
+ *   expected_m      rows a busy expert is expected to hold (a host guess,
+ *                   such as T * K / experts); it picks the kernel's shape.
+ *                   Any value gives a right result; a different shape may
+ *                   add in another order.
+ *   out             bf16 [num_rows, ld_out], N columns (N/2 for
+ *                   MXQ_ACT_SILU_MUL), a multiple of 4.  Rows that are not
+ *                   live are not written.
+ * Rows of q start on 16 bytes, rows of residual and out on 8; H <= MXQ_MAX_HIDDEN and ld_q <=
+ * MXQ_MAX_MATMUL_LD, else MXQ_ERR_UNSUPPORTED.  Sums are fp32, but for the
+ * matrix unit's own 32-product groups, in which it drops what lies more than
+ * 13 bits below the group's largest product.  Scale byte 255 and e4m3 NaN
+ * bytes in a live row or its expert's weights give NaN in what they enter. */
+mxq_status moe_expert_matmul(const void* q_fp8, int64_t ld_q,
+                             const uint8_t* scales, int64_t ld_s,
+                             int64_t num_rows, mxq_scale_fmt fmt,
+                             const void* w_fp8, const uint8_t* w_scales,
+                             int32_t E, int32_t N, int32_t H,
+                             const int32_t* expert_offsets,
+                             const int32_t* counts, const float* bias,
+                             mxq_act act, const void* residual_bf16,
+                             int64_t ld_r, int64_t expected_m, void* out_bf16,
+                             int64_t ld_out, void* stream);
+
+/* moe_expert_matmul with its fp32 rows quantized for the next product
+ * instead of rounded to bf16: e4m3 payload q_out [num_rows, ld_out] and scale
+ * bytes scales_out [num_rows, ld_so], row-major, in format out_fmt, by the
+ * rule of moe_scatter_quant (smallest exponent without clipping).  The
+ * output columns must be a multiple of out_fmt's group.  Groups whose values
+ * are not all finite have unspecified bytes. */
+mxq_status moe_expert_matmul_quant(
+    const void* q_fp8, int64_t ld_q, const uint8_t* scales, int64_t ld_s,
+    int64_t num_rows, mxq_scale_fmt fmt, const void* w_fp8,
+    const uint8_t* w_scales, int32_t E, int32_t N, int32_t H,
+    const int32_t* expert_offsets, const int32_t* counts, const float* bias,
+    mxq_act act, int64_t expected_m, mxq_scale_fmt out_fmt, void* q_out,
+    int64_t ld_out, uint8_t* scales_out, int64_t ld_so, void* stream);
 
 /* ------------------------------------------------------------- combine */
 

@@ -125,3 +125,115 @@ def combine_backward(g, y, src2dst, w, grad_y):
                 gy[d] = w[t, j] * g[t]
                 gw[t, j] = (g[t] * y[d]).sum()
     return gy, gw
+
+
+# --------------------------------------------------------- experts' products
+
+def e4m3_values() -> np.ndarray:
+    """The 256 OCP e4m3fn values (0x7F and 0xFF are NaN)."""
+    v = np.zeros(256)
+    for b in range(256):
+        e, m = (b >> 3) & 15, b & 7
+        x = m * 2.0 ** -9 if e == 0 else (8 + m) * 2.0 ** (e - 10)
+        if (b & 0x7F) == 0x7F:
+            x = np.nan
+        v[b] = -x if b >> 7 else x
+    return v
+
+
+E4M3 = e4m3_values()
+
+
+def dequant_rows(q, scales, group):
+    two = 2.0 ** (scales.astype(np.float64) - 127)
+    return E4M3[q] * np.repeat(two, group, 1)[:, :q.shape[1]]
+
+
+def dequant_weight(w, ws):
+    two = 2.0 ** (ws.astype(np.float64) - 127)
+    two = np.repeat(np.repeat(two, 128, 0), 128, 1)
+    return E4M3[w] * two[:w.shape[0], :w.shape[1]]
+
+
+def live_rows(offsets, counts, rows, e):
+    """First row and number of live rows of expert e."""
+    first = int(offsets[e])
+    n = min(int(counts[e]), int(offsets[e + 1]) - first, rows - first)
+    return first, max(n, 0) if first >= 0 else 0
+
+
+def expert_matmul(q, scales, group, w, ws, offsets, counts, bias, act,
+                  residual, cols):
+    """fp64 rows [num_rows, cols] (NaN where not live) and how far the matrix
+    unit's evaluation may be off, carried through the activation.
+
+    The unit aligns the 32 products that a lane's registers hold to the
+    largest one's exponent and drops what lies below 2^-13 of it (measured:
+    2^13 below is kept, 2^14 is not), so each product is off by less than
+    2^-13 of the largest, and a group by 32 * 2^-13 = 2^-8 of it.  A lane's
+    registers hold two runs of 16 channels; whichever they are, the group's
+    largest is at most the sum of both runs' largest, so all groups together
+    are off by at most 2^-8 of the sum over runs of max|x| max|w|.  Each of
+    the H additions after that is off by at most one fp32 step, 2^-23 of the
+    sum of absolute products."""
+    rows, H = q.shape
+    out = np.full((rows, cols), np.nan)
+    err = np.zeros((rows, cols))
+    for e in range(w.shape[0]):
+        a, n = live_rows(offsets, counts, rows, e)
+        if n == 0:
+            continue
+        x = dequant_rows(q[a:a + n], scales[a:a + n], group)
+        m = dequant_weight(w[e], ws[e])
+        y = x @ m.T
+        size = np.abs(x) @ np.abs(m).T
+        if bias is not None:
+            y = y + bias[e].astype(np.float64)
+            size = size + np.abs(bias[e])
+        run = [np.abs(v).reshape(v.shape[0], -1, 16).max(-1) for v in (x, m)]
+        d = (H + 1) * 2.0 ** -23 * size + 2.0 ** -8 * (run[0] @ run[1].T)
+        if act != "none":
+            # |silu'| < 1.1; exp, sum and quotient are off by a few steps
+            gate = y[:, :cols] if act == "silu_mul" else y
+            dg = d[:, :cols] if act == "silu_mul" else d
+            with np.errstate(over="ignore"):
+                s = gate / (1 + np.exp(-gate))
+            ds = 1.1 * dg + 2.0 ** -21 * np.abs(s)
+            if act == "silu_mul":
+                u, du = y[:, cols:], d[:, cols:]
+                y, d = s * u, ds * np.abs(u) + (np.abs(s) + ds) * du
+                d += 2.0 ** -23 * np.abs(y)
+            else:
+                y, d = s, ds
+        if residual is not None:
+            y = y + residual[a:a + n]
+            d = d + 2.0 ** -23 * np.abs(y)
+        out[a:a + n], err[a:a + n] = y, d
+    return out, err
+
+
+def check_quantized(y, err, q, scales, group, live):
+    """Payload and scale bytes stand for y: the exponent is that of the
+    group's largest value within its error, the payload within half a step
+    (2^-4 of the value, 2^-10 below the smallest normal payload)."""
+    y, err, q, scales = y[live], err[live], q[live], scales[live]
+    n = y.shape[0]
+    amax = np.abs(y).reshape(n, -1, group)
+    at = amax.max(-1)
+    slack = err.reshape(n, -1, group).max(-1)
+
+    def exponent(v):
+        with np.errstate(divide="ignore"):
+            m, e = np.frexp(v)
+        e = np.where(m > 0.875, e - 8, e - 9)
+        return np.where(v > 0, np.clip(e, -127, 127), -127)
+
+    e = scales.astype(np.int64) - 127
+    lo = exponent(np.maximum(at - slack, 0))
+    hi = exponent(at + slack)
+    assert ((e >= lo) & (e <= hi)).all(), "scale exponents"
+    two = np.repeat(2.0 ** e, group, 1)
+    back = E4M3[q] * two
+    off = np.abs(back - y)
+    assert (off <= 2.0 ** -4 * 1.0001 * (np.abs(y) + err) + 2.0 ** -10 * two
+            + err).all(), "payload"

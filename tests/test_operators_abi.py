@@ -123,3 +123,55 @@ def test_binding_refuses_host_tensors(mxq):
               lambda: mxq.moe_combine_backward(g, y, ids, w)):
         with pytest.raises(ValueError, match="must be a GPU tensor"):
             c()
+
+
+def test_expert_matmul_validation(mxq):
+    ok = dict(q=FAKE, ldq=256, s=FAKE, lds=2, rows=8, fmt=0, w=FAKE, ws=FAKE,
+              E=2, N=256, H=256, off=FAKE, cnt=FAKE, bias=None, act=0,
+              res=None, ldr=0, m=4, out=FAKE, ldo=256)
+
+    def call(**kw):
+        a = dict(ok, **kw)
+        return mxq.lib().moe_expert_matmul(
+            a["q"], a["ldq"], a["s"], a["lds"], a["rows"], a["fmt"], a["w"],
+            a["ws"], a["E"], a["N"], a["H"], a["off"], a["cnt"], a["bias"],
+            a["act"], a["res"], a["ldr"], a["m"], a["out"], a["ldo"], None)
+
+    assert call(rows=0) == 0
+    assert call(fmt=2) == UNSUPPORTED
+    assert call(act=3) == UNSUPPORTED
+    assert call(H=32896, ldq=32896, lds=257) == UNSUPPORTED
+    assert call(ldq=(1 << 22) + 16) == UNSUPPORTED
+    for bad in (dict(E=0), dict(E=1025), dict(N=0), dict(H=0), dict(H=192),
+                dict(H=16, fmt=1), dict(rows=-1), dict(rows=1 << 31),
+                dict(m=-1), dict(N=255, act=2), dict(N=254),
+                dict(N=260, act=2, ldo=127), dict(q=None), dict(s=None),
+                dict(w=None), dict(ws=None), dict(off=None), dict(cnt=None),
+                dict(out=None), dict(q=FAKE + 8), dict(ldq=264),
+                dict(ldq=240), dict(lds=1), dict(w=FAKE + 8),
+                dict(out=FAKE + 4), dict(ldo=252), dict(ldo=258),
+                dict(res=FAKE + 4, ldr=256), dict(res=FAKE, ldr=252),
+                dict(res=FAKE, ldr=258)):
+        assert call(**bad) == INVALID, bad
+
+
+def test_expert_matmul_quant_validation(mxq):
+    ok = dict(q=FAKE, ldq=256, s=FAKE, lds=2, rows=8, fmt=0, w=FAKE, ws=FAKE,
+              E=2, N=256, H=256, off=FAKE, cnt=FAKE, bias=None, act=0, m=4,
+              of=0, out=FAKE, ldo=256, so=FAKE, ldso=8)
+
+    def call(**kw):
+        a = dict(ok, **kw)
+        return mxq.lib().moe_expert_matmul_quant(
+            a["q"], a["ldq"], a["s"], a["lds"], a["rows"], a["fmt"], a["w"],
+            a["ws"], a["E"], a["N"], a["H"], a["off"], a["cnt"], a["bias"],
+            a["act"], a["m"], a["of"], a["out"], a["ldo"], a["so"],
+            a["ldso"], None)
+
+    assert call(rows=0) == 0
+    assert call(of=2) == UNSUPPORTED
+    for bad in (dict(N=192), dict(N=128, act=2), dict(N=48, of=1),
+                dict(so=None), dict(out=None), dict(out=FAKE + 8),
+                dict(ldo=264), dict(ldo=240), dict(ldso=1),
+                dict(of=1, ldso=7)):
+        assert call(**bad) == INVALID, bad
