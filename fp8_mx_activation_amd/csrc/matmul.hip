@@ -196,6 +196,389 @@ __global__ __launch_bounds__(64 * NG * KS) void matmul_small_kernel(
   }
 }
 
+// ------------------------------------------------------------ many rows
+//
+// A block of four wavefronts, one per SIMD, owns TM = 64 XF token rows of one
+// expert by 256 weight rows; each wavefront multiplies 32 XF tokens by 128
+// weight rows in 32x32x64 steps (64 XF accumulators per lane).  K goes by in
+// steps of 128 channels, held in LDS twice: while one step is multiplied, the
+// next is on its way from memory straight into LDS.
+//
+// LDS rows are 128 bytes; 16-byte chunk c of row r sits at chunk c ^ (r & 7),
+// so that the 32 rows a fragment read touches spread over all banks.  The
+// copy into LDS is linear, hence the chunk order is turned on its global side.
+//
+// Half step h of step k: the fragments of half 1 are read from LDS while half
+// 0 is multiplied, and those of the next step's half 0 while half 1 is.  So a
+// step's buffer is free, and the next one has to have landed, at the one
+// barrier between its halves; the load of step k + 2 is issued right after it
+// and has a whole step to arrive.
+//
+// A gated tile takes 128 gate rows and the 128 factor rows of the same
+// outputs; a wavefront holds both for 64 outputs.
+
+__device__ __forceinline__ v4i buffer_of(const void* base, uint32_t bytes) {
+  const uint64_t p = reinterpret_cast<uint64_t>(base);
+  v4i r;
+  r.x = __builtin_amdgcn_readfirstlane((int)(uint32_t)p);
+  r.y = __builtin_amdgcn_readfirstlane((int)(uint32_t)(p >> 32) & 0xFFFF);
+  r.z = __builtin_amdgcn_readfirstlane((int)bytes);
+  r.w = 0x00020000;  // raw 32-bit data, no swizzle
+  return r;
+}
+
+// 16 bytes per lane from `buf` at voff + soff into LDS at lds + 16 * lane.
+// The lane's address registers are the only operands: nothing is returned to
+// registers, so there is no result to wait for but the vmcnt before the next
+// barrier.
+__device__ __forceinline__ void copy_to_lds(const v4i& buf, uint32_t lds,
+                                            uint32_t voff, uint32_t soff) {
+  asm volatile(
+      "s_mov_b32 m0, %0\n\t"
+      "s_nop 0\n\t"
+      "buffer_load_dwordx4 %1, %2, %3 offen lds"
+      :
+      : "s"(lds), "v"(voff), "s"(buf), "s"(soff));
+}
+
+// Every load issued so far has landed, in this wavefront and (after the
+// barrier) in the block; LDS reads issued so far have returned.
+__device__ __forceinline__ void landed_barrier() {
+  __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+  asm volatile("s_barrier" ::: "memory");
+}
+
+// The tile a block works on.  Experts' tiles are numbered expert by expert,
+// from device data; every wavefront finds its block's by itself.  Runs of
+// consecutive tiles go to one XCD (block b runs on XCD b % 8), and within a
+// run eight row tiles share a column of weights, so the 32 CUs of an XCD
+// read a window of 8 by 4 tiles through their L2.
+struct TileOf {
+  int e, m0, n;
+};
+
+constexpr int kGroupM = 8;
+
+template <int TM>
+__device__ __forceinline__ bool find_tile(const MatmulArgs& a, int tiles_n,
+                                          TileOf& t) {
+  const int lane = threadIdx.x & 63;
+  const int per = (a.E + 63) / 64;  // experts per lane, consecutive
+  int mine = 0;
+  for (int i = 0; i < per; ++i) {
+    const int e = lane * per + i;
+    if (e < a.E) mine += (expert_rows(a, e).count + TM - 1) / TM;
+  }
+  int upto = mine;  // row tiles of lanes up to this one
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int v = __shfl_up(upto, d);
+    if (lane >= d) upto += v;
+  }
+  const int tiles_m = __builtin_amdgcn_readlane(upto, 63);
+  const int64_t total = (int64_t)tiles_m * tiles_n;
+  const int64_t run = (total + 7) / 8;
+  const int64_t at = (int64_t)(blockIdx.x & 7) * run + (blockIdx.x >> 3);
+  if ((int64_t)(blockIdx.x >> 3) >= run || at >= total) return false;
+  const int64_t group = at / ((int64_t)kGroupM * tiles_n);
+  const int gm = min(kGroupM, tiles_m - (int)group * kGroupM);
+  const int in = (int)(at - group * kGroupM * tiles_n);
+  t.n = in / gm;
+  const int m = (int)group * kGroupM + in % gm;
+  const int owner = __ffsll((unsigned long long)__ballot(upto > m)) - 1;
+  int first = __builtin_amdgcn_readlane(upto - mine, owner);
+  int e = owner * per;
+  for (int i = 0; i < per; ++i) {
+    const int c = (expert_rows(a, owner * per + i).count + TM - 1) / TM;
+    e = owner * per + i;
+    if (m < first + c) break;
+    first += c;
+  }
+  t.e = __builtin_amdgcn_readfirstlane(e);
+  t.m0 = __builtin_amdgcn_readfirstlane((m - first) * TM);
+  return true;
+}
+
+constexpr int kStageLd = 132;  // floats per staged token (128 channels + pad)
+
+template <int XF>
+constexpr int tile_lds_bytes() {
+  const int loop = 2 * (64 * XF + 256) * 128;
+  const int end = 64 * XF * kStageLd * 4;
+  return loop > end ? loop : end;
+}
+
+template <int G, int XF, int OUT>
+__global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs a,
+                                                             int32_t tiles_n) {
+  constexpr int TM = 64 * XF;
+  constexpr int kX = TM * 128;             // bytes of a step's token rows
+  constexpr int kStage = kX + 256 * 128;   // and with its weight rows
+  constexpr int kXCopies = TM / 32;        // 1 KB copies per wavefront
+  constexpr int kWCopies = 8;
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  TileOf t;
+  if (!find_tile<TM>(a, tiles_n, t)) return;
+  const ExpertRows er = expert_rows(a, t.e);
+  const int rows = min(er.count - t.m0, TM);  // live rows of this tile
+  const int64_t row0 = er.first + t.m0;
+  const bool gated = a.act == kActSiluMul;
+  const int n0 = t.n * (gated ? 128 : 256);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  const int r32 = lane & 31, g = lane >> 5;
+  const int H = a.H;
+  const int nsteps = (H + 127) / 128;
+  const int nwb = (a.N + 127) / 128;
+
+  // weight row (within the expert's matrix) of local row lr of the tile
+  auto weight_row = [&](int lr) {
+    if (!gated) return min(n0 + lr, a.N - 1);
+    const int c = min(n0 + (lr >> 7) * 64 + (lr & 63), a.NO - 1);
+    return (lr & 64) ? a.NO + c : c;
+  };
+
+  // copies: lane l of copy i brings chunk (l & 7) ^ (l >> 3) of row
+  // 8 (wave + 4 i) + (l >> 3)
+  const int chunk = (lane & 7) ^ (lane >> 3);
+  uint32_t xoff[kXCopies], woff[kWCopies];
+  const int64_t wfirst = n0;
+#pragma unroll
+  for (int i = 0; i < kXCopies; ++i) {
+    const int r = 8 * (wave + 4 * i) + (lane >> 3);
+    xoff[i] = (uint32_t)(min(r, rows - 1) * (int)a.ld_q + 16 * chunk);
+  }
+#pragma unroll
+  for (int i = 0; i < kWCopies; ++i) {
+    const int r = 8 * (wave + 4 * i) + (lane >> 3);
+    woff[i] = (uint32_t)((weight_row(r) - wfirst) * H + 16 * chunk);
+  }
+  const v4i xbuf = buffer_of(a.q + row0 * a.ld_q,
+                             (uint32_t)((rows - 1) * a.ld_q + H));
+  const v4i wbuf = buffer_of(a.w + ((int64_t)t.e * a.N + wfirst) * H,
+                             (uint32_t)((a.N - wfirst) * H > 0xFFFFFFFFll
+                                            ? 0xFFFFFFFFll
+                                            : (a.N - wfirst) * H));
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(
+      __attribute__((address_space(3))) uint8_t*)lds;
+  // In a last step that ends inside the 128 channels, chunks past H repeat
+  // chunk 0 of the step: in bounds, and cleared when they are read.
+  auto step_back = [&](int k) {
+    return (uint32_t)(k * 128 + 16 * chunk >= H ? 16 * chunk : 0);
+  };
+  auto copy_piece = [&](int k, int i, uint32_t back) {
+    const int k0 = k * 128;
+    const uint32_t at = lds0 + (k & 1) * kStage + wave * 1024;
+    if (i < kXCopies)
+      copy_to_lds(xbuf, at + i * 4096, xoff[i] - back, k0);
+    else
+      copy_to_lds(wbuf, at + kX + (i - kXCopies) * 4096,
+                  woff[i - kXCopies] - back, k0);
+  };
+
+  // Scales of a step: one byte per row (G = 128), or the four of its blocks
+  // (G = 32).  A row's last four bytes are read whole where the last step has
+  // fewer blocks, and shifted: what shifts in is 2^-127, on cleared payload.
+  const int nxs = H / G, nws = a.nbk;
+  const uint8_t* xs0 = a.s + row0 * a.ld_s;
+  const uint8_t* ws0 = a.ws + (int64_t)t.e * nwb * nws;
+  uint32_t xs[XF], wsr[4];
+#pragma unroll
+  for (int x = 0; x < XF; ++x)
+    xs[x] = (uint32_t)(min(wm * 32 * XF + x * 32 + r32, rows - 1) *
+                       (int)a.ld_s);
+#pragma unroll
+  for (int f = 0; f < 4; ++f)
+    wsr[f] = (uint32_t)(weight_row(wn * 128 + f * 32 + r32) / 128 * nws);
+  // of the current step, of the next one, and on their way for the one after
+  uint32_t sx[XF], sw[4], sx1[XF], sw1[4], sx2[XF], sw2[4];
+  auto load_scales = [&](uint32_t (&x)[XF], uint32_t (&w)[4], int k) {
+    const uint8_t* xk = xs0 + (G == 128 ? k : min(4 * k, nxs - 4));
+    const uint8_t* wk = ws0 + k;
+#pragma unroll
+    for (int i = 0; i < XF; ++i) {
+      if constexpr (G == 128)
+        x[i] = xk[xs[i]];
+      else
+        __builtin_memcpy(&x[i], xk + xs[i], 4);
+    }
+#pragma unroll
+    for (int f = 0; f < 4; ++f) w[f] = wk[wsr[f]];
+  };
+  auto use_scales = [&](const uint32_t (&x)[XF], const uint32_t (&w)[4],
+                        int k) {
+    const int shift = G == 128 ? 0 : 8 * (4 * k - min(4 * k, nxs - 4) + g);
+#pragma unroll
+    for (int i = 0; i < XF; ++i) sx[i] = G == 128 ? x[i] : x[i] >> shift;
+#pragma unroll
+    for (int f = 0; f < 4; ++f) sw[f] = w[f];
+  };
+
+  v16f acc[4][XF];
+#pragma unroll
+  for (int f = 0; f < 4; ++f)
+#pragma unroll
+    for (int x = 0; x < XF; ++x)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[f][x][i] = 0.0f;
+
+  // fragments of the two halves of a step, in 16-byte pieces
+  v4i fw[2][4][2], fx[2][XF][2];
+  constexpr int kPieces = 2 * (4 + XF);
+  auto read_piece = [&](int k, int h, int p, auto last) {
+    const int c = h * 4 + (p & 1) * 2 + g;
+    const int off = r32 * 128 + ((c ^ (r32 & 7)) * 16);
+    const uint8_t* stage = lds + (k & 1) * kStage;
+    v4i v = *reinterpret_cast<const v4i*>(
+        p < 8 ? stage + kX + (wn * 128 + (p >> 1) * 32) * 128 + off
+              : stage + (wm * 32 * XF + ((p - 8) >> 1) * 32) * 128 + off);
+    if constexpr (decltype(last)::value)
+      if (k * 128 + 16 * c >= H) v = v4i{0, 0, 0, 0};
+    if (p < 8)
+      fw[h][p >> 1][p & 1] = v;
+    else
+      fx[h][(p - 8) >> 1][p & 1] = v;
+  };
+
+  constexpr int kCopies = kXCopies + kWCopies;
+  constexpr int kMfma = 4 * XF;  // of a half step
+  using Yes = std::true_type;
+  using No = std::false_type;
+
+  load_scales(sx1, sw1, 0);
+#pragma unroll
+  for (int i = 0; i < kCopies; ++i) copy_piece(0, i, step_back(0));
+  landed_barrier();
+  use_scales(sx1, sw1, 0);
+  if (nsteps > 1) {
+    load_scales(sx2, sw2, 1);
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) copy_piece(1, i, step_back(1));
+  }
+#pragma unroll
+  for (int p = 0; p < kPieces; ++p) read_piece(0, 0, p, Yes{});
+
+  // One step.  `more`: another one follows; `copy`: and one after that;
+  // `last`: this is, and `next_last`: the next one is, the last.  Reads and
+  // copies are dealt out between the MFMAs, so that neither LDS nor the
+  // memory pipe gets them in one burst while the matrix unit waits.
+  auto step = [&](int k, auto more, auto copy, auto last, auto next_last) {
+#pragma unroll
+    for (int i = 0; i < kMfma; ++i) {
+#pragma unroll
+      for (int p = i * kPieces / kMfma; p < (i + 1) * kPieces / kMfma; ++p)
+        read_piece(k, 1, p, last);
+      const int f = i / XF, x = i % XF;
+      acc[f][x] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+          join(fw[0][f][0], fw[0][f][1]), join(fx[0][x][0], fx[0][x][1]),
+          acc[f][x], 0, 0, 0, (int)sw[f], 0, (int)sx[x]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    landed_barrier();
+    if constexpr (decltype(more)::value) {
+      // taken here, where they have landed: read any later, they would be
+      // waited for together with the copies issued below
+#pragma unroll
+      for (int x = 0; x < XF; ++x) {
+        sx1[x] = sx2[x];
+        asm volatile("" : "+v"(sx1[x]));
+      }
+#pragma unroll
+      for (int f = 0; f < 4; ++f) {
+        sw1[f] = sw2[f];
+        asm volatile("" : "+v"(sw1[f]));
+      }
+    }
+    if constexpr (decltype(copy)::value) load_scales(sx2, sw2, k + 2);
+    const uint32_t back = step_back(k + 2);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < kMfma; ++i) {
+      if constexpr (decltype(copy)::value) {
+#pragma unroll
+        for (int p = i * kCopies / kMfma; p < (i + 1) * kCopies / kMfma; ++p)
+          copy_piece(k + 2, p, back);
+      }
+      if constexpr (decltype(more)::value) {
+#pragma unroll
+        for (int p = i * kPieces / kMfma; p < (i + 1) * kPieces / kMfma; ++p)
+          read_piece(k + 1, 0, p, next_last);
+      }
+      const int f = i / XF, x = i % XF;
+      // the second half's scales are two bytes further where a step has four
+      acc[f][x] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+          join(fw[1][f][0], fw[1][f][1]), join(fx[1][x][0], fx[1][x][1]),
+          acc[f][x], 0, 0, 0, (int)sw[f], G == 128 ? 0 : 2, (int)sx[x]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (decltype(more)::value) use_scales(sx1, sw1, k + 1);
+  };
+  int k = 0;
+  for (; k + 2 < nsteps; ++k) step(k, Yes{}, Yes{}, No{}, No{});
+  if (k + 1 < nsteps) step(k++, Yes{}, No{}, No{}, Yes{});
+  step(k, No{}, No{}, Yes{}, No{});
+
+  // End of the rows: 128 output columns at a time go through LDS as fp32, so
+  // that a row's 128 columns end up in 16 neighbouring lanes: whole lines to
+  // memory, and a quantization group within a wavefront.
+  float* stage = reinterpret_cast<float*>(lds);
+  const int passes = gated ? 1 : 2;
+  for (int pass = 0; pass < passes; ++pass) {
+    __syncthreads();
+    if (gated || wn == pass) {
+#pragma unroll
+      for (int f = 0; f < 4; ++f) {
+        if (gated && f >= 2) break;
+#pragma unroll
+        for (int q4 = 0; q4 < 4; ++q4) {
+          // the lane's columns: four neighbours
+          const int c = (gated ? wn * 64 : 0) + f * 32 + 8 * q4 + 4 * g;
+          const int col = n0 + pass * 128 + c;
+          float b[4], bu[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            b[j] = bu[j] = 0.0f;
+            if (a.bias != nullptr) {
+              const float* br = a.bias + (int64_t)t.e * a.N;
+              const int cj = min(col + j, a.NO - 1);
+              b[j] = br[cj];
+              if (gated) bu[j] = br[a.NO + cj];
+            }
+          }
+#pragma unroll
+          for (int x = 0; x < XF; ++x) {
+            v4f v;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              v[j] = acc[f][x][4 * q4 + j] + b[j];
+              if (gated)
+                v[j] = silu(v[j]) *
+                       (acc[(f + 2) & 3][x][4 * q4 + j] + bu[j]);
+              else if (a.act == kActSilu)
+                v[j] = silu(v[j]);
+            }
+            *reinterpret_cast<v4f*>(
+                stage + (wm * 32 * XF + x * 32 + r32) * kStageLd + c) = v;
+          }
+        }
+      }
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int i = 0; i < TM / 16; ++i) {
+      const int tok = i * 16 + wave * 4 + (lane >> 4);
+      const int c = (lane & 15) * 8;
+      const int col = n0 + pass * 128 + c;
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = stage[tok * kStageLd + c + j];
+      store_channels<OUT>(a, row0 + min(tok, rows - 1), col,
+                          tok < rows && col < a.NO, v);
+    }
+  }
+}
+
 // ------------------------------------------------------------ entry points
 
 template <int G, int MT, int NG, int KS, int OUT>
@@ -216,8 +599,31 @@ mxq_status launch_small(const MatmulArgs& a, hipStream_t s) {
   return launch_status();
 }
 
+template <int G, int XF, int OUT>
+mxq_status launch_tile(const MatmulArgs& a, hipStream_t s) {
+  const int64_t tn = ceil_div(a.NO, a.act == kActSiluMul ? 128 : 256);
+  // every expert ends in at most one partial row tile
+  const int64_t tm = a.num_rows / (64 * XF) + a.E;
+  const int64_t blocks = ceil_div(tm * tn, 8) * 8;
+  if (blocks > INT32_MAX) return MXQ_ERR_UNSUPPORTED;
+  constexpr int lds = tile_lds_bytes<XF>();
+  auto* k = &matmul_tile_kernel<G, XF, OUT>;
+  if (hipFuncSetAttribute(reinterpret_cast<const void*>(k),
+                          hipFuncAttributeMaxDynamicSharedMemorySize,
+                          lds) != hipSuccess) {
+    (void)hipGetLastError();
+    return MXQ_ERR_HIP;
+  }
+  k<<<(unsigned)blocks, 256, lds, s>>>(a, (int32_t)tn);
+  return launch_status();
+}
+
 template <int G, int OUT>
 mxq_status launch(const MatmulArgs& a, int64_t expected, hipStream_t s) {
+  if (a.H >= 128) {  // a whole step: the tile kernel's scale reads need one
+    if (expected > 128) return launch_tile<G, 4, OUT>(a, s);
+    if (expected > 64) return launch_tile<G, 2, OUT>(a, s);
+  }
   if constexpr (OUT == kOutG128) {
     // a group of 128 outputs stays in one block: 128 weight rows, or 256
     if (a.act == kActSiluMul) return launch_small<G, 1, 4, 2, OUT>(a, s);
@@ -252,7 +658,8 @@ mxq_status checked(const void* q, int64_t ld_q, const uint8_t* scales,
   const int32_t NO = act == MXQ_ACT_SILU_MUL ? N / 2 : N;
   const int unit = OUT == kOutBf16 ? 4 : OUT == kOutG128 ? 128 : 32;
   if (NO % unit != 0) return MXQ_ERR_INVALID_ARGUMENT;
-  if (H > MXQ_MAX_HIDDEN) return MXQ_ERR_UNSUPPORTED;
+  if (H > MXQ_MAX_HIDDEN || (int64_t)N * H > INT32_MAX)
+    return MXQ_ERR_UNSUPPORTED;
   if (num_rows == 0) return MXQ_OK;
   if (q == nullptr || scales == nullptr || w == nullptr ||
       w_scales == nullptr || offsets == nullptr || counts == nullptr ||
@@ -261,7 +668,8 @@ mxq_status checked(const void* q, int64_t ld_q, const uint8_t* scales,
   if (!aligned16(q) || ld_q % 16 != 0 || ld_q < H || ld_s < H / G ||
       !aligned16(w) || ld_out < NO)
     return MXQ_ERR_INVALID_ARGUMENT;
-  if (ld_q > MXQ_MAX_MATMUL_LD) return MXQ_ERR_UNSUPPORTED;
+  if (ld_q > MXQ_MAX_MATMUL_LD || ld_s > MXQ_MAX_MATMUL_LD)
+    return MXQ_ERR_UNSUPPORTED;
   if constexpr (OUT == kOutBf16) {
     if (!aligned8(out) || ld_out % 4 != 0) return MXQ_ERR_INVALID_ARGUMENT;
     if (residual != nullptr &&

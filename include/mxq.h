@@ -54,7 +54,7 @@ extern "C" {
 #define MXQ_MAX_TOPK 64
 #define MXQ_MAX_ASSIGNMENTS (1 << 24) /* T*K limit of moe_layout */
 #define MXQ_MAX_HIDDEN 32768 /* moe_scatter_quant stages one row in LDS */
-#define MXQ_MAX_MATMUL_LD (1 << 22) /* moe_expert_matmul: row stride, bytes */
+#define MXQ_MAX_MATMUL_LD (1 << 22) /* moe_expert_matmul: row strides, bytes */
 #define MXQ_MAX_ROUTE_EXPERTS 1024 /* moe_route: global experts of a row */
 /* Static device scratch of moe_layout_noalloc, per device (1 MiB). */
 #define MXQ_LAYOUT_NOALLOC_SCRATCH_BYTES (1u << 20)
@@ -464,8 +464,8 @@ mxq_status requant_per_token_to_per_tensor(
  *   out             bf16 [num_rows, ld_out], N columns (N/2 for
  *                   MXQ_ACT_SILU_MUL), a multiple of 4.  Rows that are not
  *                   live are not written.
- * Rows of q start on 16 bytes, rows of residual and out on 8; H <= MXQ_MAX_HIDDEN and ld_q <=
- * MXQ_MAX_MATMUL_LD, else MXQ_ERR_UNSUPPORTED.  Sums are fp32, but for the
+ * Rows of q start on 16 bytes, rows of residual and out on 8; H <= MXQ_MAX_HIDDEN, N * H <
+ * 2^31, ld_q and ld_s <= MXQ_MAX_MATMUL_LD, else MXQ_ERR_UNSUPPORTED.  Sums are fp32, but for the
  * matrix unit's own 32-product groups, in which it drops what lies more than
  * 13 bits below the group's largest product.  Scale byte 255 and e4m3 NaN
  * bytes in a live row or its expert's weights give NaN in what they enter. */
