@@ -190,7 +190,9 @@ __global__ __launch_bounds__(64 * NG * KS) void matmul_small_kernel(
       }
       const bool live = in && base + tok < er.count;
       const int64_t row = er.first + min(base + tok, er.count - 1);
-      store_channels<OUT>(a, row, col, live, v);
+      u32x4 res{0, 0, 0, 0};
+      if constexpr (OUT == kOutBf16) res = load_residual(a, row, col);
+      store_channels<OUT>(a, row, col, live, v, res);
     }
     __syncthreads();
   }
@@ -204,8 +206,9 @@ __global__ __launch_bounds__(64 * NG * KS) void matmul_small_kernel(
 // steps of 128 channels, held in LDS twice: while one step is multiplied, the
 // next is on its way from memory straight into LDS.
 //
-// LDS rows are 128 bytes; 16-byte chunk c of row r sits at chunk c ^ (r & 7),
-// so that the 32 rows a fragment read touches spread over all banks.  The
+// LDS rows are 128 bytes; 16-byte chunk c of row r sits at chunk
+// c ^ ((r >> 1) & 7): 16 neighbouring rows of a fragment read then touch all
+// 64 banks once.  The
 // copy into LDS is linear, hence the chunk order is turned on its global side.
 //
 // Half step h of step k: the fragments of half 1 are read from LDS while half
@@ -299,12 +302,15 @@ __device__ __forceinline__ bool find_tile(const MatmulArgs& a, int tiles_n,
   return true;
 }
 
-constexpr int kStageLd = 132;  // floats per staged token (128 channels + pad)
+constexpr int kStageLd = 260;  // floats per staged token (256 weight rows + pad)
+constexpr int kScaleLd = 36;   // bytes per row of a scale chunk (32 + pad)
+constexpr int kMaxSteps = MXQ_MAX_HIDDEN / 128;
 
 template <int XF>
 constexpr int tile_lds_bytes() {
-  const int loop = 2 * (64 * XF + 256) * 128;
-  const int end = 64 * XF * kStageLd * 4;
+  const int loop = 2 * ((64 * XF + 256) * 128 + 64 * XF * kScaleLd) +
+                   3 * kMaxSteps;
+  const int end = 128 * kStageLd * 4;
   return loop > end ? loop : end;
 }
 
@@ -339,9 +345,8 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs a,
     return (lr & 64) ? a.NO + c : c;
   };
 
-  // copies: lane l of copy i brings chunk (l & 7) ^ (l >> 3) of row
-  // 8 (wave + 4 i) + (l >> 3)
-  const int chunk = (lane & 7) ^ (lane >> 3);
+  // copies: lane l of copy i fills place l & 7 of row 8 (wave + 4 i) + (l >> 3)
+  const int chunk = (lane & 7) ^ ((4 * wave + (lane >> 4)) & 7);
   uint32_t xoff[kXCopies], woff[kWCopies];
   const int64_t wfirst = n0;
 #pragma unroll
@@ -377,42 +382,74 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs a,
                   woff[i - kXCopies] - back, k0);
   };
 
-  // Scales of a step: one byte per row (G = 128), or the four of its blocks
-  // (G = 32).  A row's last four bytes are read whole where the last step has
-  // fewer blocks, and shifted: what shifts in is 2^-127, on cleared payload.
+  // Scales.  A step needs one byte of each token row (G = 128) or four
+  // (G = 32): fetched step by step they would cost a scattered load per
+  // fragment, so thread r brings 32 bytes of row r at a time into LDS (two
+  // such chunks, rows 36 bytes apart).  The tile's weight rows lie in at most
+  // three 128-row blocks; their scale bytes are all in LDS from the start.
+  constexpr int kPer = G == 128 ? 32 : 8;  // steps per chunk
+  uint8_t* xscale = lds + 2 * kStage;
+  uint8_t* wscale = xscale + 2 * TM * kScaleLd;
   const int nxs = H / G, nws = a.nbk;
-  const uint8_t* xs0 = a.s + row0 * a.ld_s;
-  const uint8_t* ws0 = a.ws + (int64_t)t.e * nwb * nws;
-  uint32_t xs[XF], wsr[4];
+  const uint8_t* xs_row =
+      a.s + (row0 + min((int)threadIdx.x, rows - 1)) * a.ld_s;
+  uint32_t xs_next[8];
+  auto fetch_scales = [&](int chunk_no) {
+    if (threadIdx.x >= TM) return;
+    const uint8_t* p = xs_row + chunk_no * 32;
+    const int left = nxs - chunk_no * 32;
 #pragma unroll
-  for (int x = 0; x < XF; ++x)
-    xs[x] = (uint32_t)(min(wm * 32 * XF + x * 32 + r32, rows - 1) *
-                       (int)a.ld_s);
+    for (int j = 0; j < 8; ++j) {
+      xs_next[j] = 0x7F7F7F7Fu;
+      if (4 * j + 4 <= left) {
+        __builtin_memcpy(&xs_next[j], p + 4 * j, 4);
+      } else {
+        for (int i = 4 * j; i < left; ++i)
+          xs_next[j] = (xs_next[j] & ~(0xFFu << (8 * (i & 3)))) |
+                       ((uint32_t)p[i] << (8 * (i & 3)));
+      }
+    }
+  };
+  auto put_scales = [&](int chunk_no) {
+    if (threadIdx.x >= TM) return;
+    uint32_t* d = reinterpret_cast<uint32_t*>(
+        xscale + ((chunk_no & 1) * TM + threadIdx.x) * kScaleLd);
 #pragma unroll
-  for (int f = 0; f < 4; ++f)
-    wsr[f] = (uint32_t)(weight_row(wn * 128 + f * 32 + r32) / 128 * nws);
-  // of the current step, of the next one, and on their way for the one after
-  uint32_t sx[XF], sw[4], sx1[XF], sw1[4], sx2[XF], sw2[4];
-  auto load_scales = [&](uint32_t (&x)[XF], uint32_t (&w)[4], int k) {
-    const uint8_t* xk = xs0 + (G == 128 ? k : min(4 * k, nxs - 4));
-    const uint8_t* wk = ws0 + k;
+    for (int j = 0; j < 8; ++j) d[j] = xs_next[j];
+  };
+  const int up_block = (a.NO + n0) / 128;  // of a gated tile's factor rows
+  for (int i = threadIdx.x; i < 3 * nws; i += 256) {
+    const int b = i / nws;
+    const int block = b == 0 ? n0 / 128
+                      : gated ? up_block + b - 1 : n0 / 128 + b;
+    if (block < nwb)
+      wscale[b * kMaxSteps + i % nws] =
+          a.ws[((int64_t)t.e * nwb + block) * nws + i % nws];
+  }
+  int wsoff[4];
 #pragma unroll
-    for (int i = 0; i < XF; ++i) {
-      if constexpr (G == 128)
-        x[i] = xk[xs[i]];
-      else
-        __builtin_memcpy(&x[i], xk + xs[i], 4);
+  for (int f = 0; f < 4; ++f) {
+    const int block = weight_row(wn * 128 + f * 32 + r32) / 128;
+    wsoff[f] = (gated && f >= 2 ? block - up_block + 1 : block - n0 / 128) *
+               kMaxSteps;
+  }
+  uint32_t sx[XF], sw[4], sx1[XF], sw1[4];  // of this step and the next one
+  auto read_scales = [&](int k) {
+    const uint8_t* chunk_at = xscale + ((k / kPer) & 1) * TM * kScaleLd;
+#pragma unroll
+    for (int x = 0; x < XF; ++x) {
+      const uint8_t* p = chunk_at + (wm * 32 * XF + x * 32 + r32) * kScaleLd;
+      sx1[x] = G == 128 ? p[k % kPer]
+                        : reinterpret_cast<const uint32_t*>(p)[k % kPer];
     }
 #pragma unroll
-    for (int f = 0; f < 4; ++f) w[f] = wk[wsr[f]];
+    for (int f = 0; f < 4; ++f) sw1[f] = wscale[wsoff[f] + k];
   };
-  auto use_scales = [&](const uint32_t (&x)[XF], const uint32_t (&w)[4],
-                        int k) {
-    const int shift = G == 128 ? 0 : 8 * (4 * k - min(4 * k, nxs - 4) + g);
+  auto use_scales = [&]() {
 #pragma unroll
-    for (int i = 0; i < XF; ++i) sx[i] = G == 128 ? x[i] : x[i] >> shift;
+    for (int x = 0; x < XF; ++x) sx[x] = G == 128 ? sx1[x] : sx1[x] >> (8 * g);
 #pragma unroll
-    for (int f = 0; f < 4; ++f) sw[f] = w[f];
+    for (int f = 0; f < 4; ++f) sw[f] = sw1[f];
   };
 
   v16f acc[4][XF];
@@ -428,7 +465,7 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs a,
   constexpr int kPieces = 2 * (4 + XF);
   auto read_piece = [&](int k, int h, int p, auto last) {
     const int c = h * 4 + (p & 1) * 2 + g;
-    const int off = r32 * 128 + ((c ^ (r32 & 7)) * 16);
+    const int off = r32 * 128 + ((c ^ ((r32 >> 1) & 7)) * 16);
     const uint8_t* stage = lds + (k & 1) * kStage;
     v4i v = *reinterpret_cast<const v4i*>(
         p < 8 ? stage + kX + (wn * 128 + (p >> 1) * 32) * 128 + off
@@ -446,16 +483,16 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs a,
   using Yes = std::true_type;
   using No = std::false_type;
 
-  load_scales(sx1, sw1, 0);
+  fetch_scales(0);
 #pragma unroll
   for (int i = 0; i < kCopies; ++i) copy_piece(0, i, step_back(0));
+  put_scales(0);
   landed_barrier();
-  use_scales(sx1, sw1, 0);
-  if (nsteps > 1) {
-    load_scales(sx2, sw2, 1);
+  if (nsteps > 1)
 #pragma unroll
     for (int i = 0; i < kCopies; ++i) copy_piece(1, i, step_back(1));
-  }
+  read_scales(0);
+  use_scales();
 #pragma unroll
   for (int p = 0; p < kPieces; ++p) read_piece(0, 0, p, Yes{});
 
@@ -476,21 +513,14 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs a,
       __builtin_amdgcn_sched_barrier(0);
     }
     landed_barrier();
-    if constexpr (decltype(more)::value) {
-      // taken here, where they have landed: read any later, they would be
-      // waited for together with the copies issued below
-#pragma unroll
-      for (int x = 0; x < XF; ++x) {
-        sx1[x] = sx2[x];
-        asm volatile("" : "+v"(sx1[x]));
-      }
-#pragma unroll
-      for (int f = 0; f < 4; ++f) {
-        sw1[f] = sw2[f];
-        asm volatile("" : "+v"(sw1[f]));
-      }
+    if constexpr (decltype(copy)::value) {
+      // one chunk ahead: fetched in a chunk's first step, put down in its
+      // second, where the loads have landed
+      const int next = (k / kPer + 1) * kPer;
+      if (k % kPer == 0 && next < nsteps) fetch_scales(k / kPer + 1);
+      if (k % kPer == 1 && next < nsteps) put_scales(k / kPer + 1);
     }
-    if constexpr (decltype(copy)::value) load_scales(sx2, sw2, k + 2);
+    if constexpr (decltype(more)::value) read_scales(k + 1);
     const uint32_t back = step_back(k + 2);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -512,69 +542,94 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs a,
           acc[f][x], 0, 0, 0, (int)sw[f], G == 128 ? 0 : 2, (int)sx[x]);
       __builtin_amdgcn_sched_barrier(0);
     }
-    if constexpr (decltype(more)::value) use_scales(sx1, sw1, k + 1);
+    if constexpr (decltype(more)::value) use_scales();
   };
   int k = 0;
   for (; k + 2 < nsteps; ++k) step(k, Yes{}, Yes{}, No{}, No{});
   if (k + 1 < nsteps) step(k++, Yes{}, No{}, No{}, Yes{});
   step(k, No{}, No{}, Yes{}, No{});
 
-  // End of the rows: 128 output columns at a time go through LDS as fp32, so
-  // that a row's 128 columns end up in 16 neighbouring lanes: whole lines to
-  // memory, and a quantization group within a wavefront.
+  // End of the rows.  128 token rows (64 of each wavefront row) at a time go
+  // through LDS as they are, so that a thread ends up with eight neighbouring
+  // channels of a row: gate and factor meet, a row is written in whole lines,
+  // and a quantization group lies within a wavefront.
   float* stage = reinterpret_cast<float*>(lds);
-  const int passes = gated ? 1 : 2;
-  for (int pass = 0; pass < passes; ++pass) {
-    __syncthreads();
-    if (gated || wn == pass) {
+  const int out_lanes = gated ? 16 : 32;  // threads per row
+  const int oc = (int)threadIdx.x % out_lanes * 8;
+  const int col = n0 + oc;
+  const int per = 256 / out_lanes;  // rows per round of the block
+  float b[8], bu[8];
 #pragma unroll
-      for (int f = 0; f < 4; ++f) {
-        if (gated && f >= 2) break;
+  for (int j = 0; j < 8; ++j) b[j] = bu[j] = 0.0f;
+  if (a.bias != nullptr) {
+    const float* br = a.bias + (int64_t)t.e * a.N;
 #pragma unroll
-        for (int q4 = 0; q4 < 4; ++q4) {
-          // the lane's columns: four neighbours
-          const int c = (gated ? wn * 64 : 0) + f * 32 + 8 * q4 + 4 * g;
-          const int col = n0 + pass * 128 + c;
-          float b[4], bu[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            b[j] = bu[j] = 0.0f;
-            if (a.bias != nullptr) {
-              const float* br = a.bias + (int64_t)t.e * a.N;
-              const int cj = min(col + j, a.NO - 1);
-              b[j] = br[cj];
-              if (gated) bu[j] = br[a.NO + cj];
-            }
-          }
-#pragma unroll
-          for (int x = 0; x < XF; ++x) {
-            v4f v;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              v[j] = acc[f][x][4 * q4 + j] + b[j];
-              if (gated)
-                v[j] = silu(v[j]) *
-                       (acc[(f + 2) & 3][x][4 * q4 + j] + bu[j]);
-              else if (a.act == kActSilu)
-                v[j] = silu(v[j]);
-            }
-            *reinterpret_cast<v4f*>(
-                stage + (wm * 32 * XF + x * 32 + r32) * kStageLd + c) = v;
-          }
-        }
-      }
+    for (int j = 0; j < 8; ++j) {
+      b[j] = br[min(col + j, a.NO - 1)];
+      if (gated) bu[j] = br[a.NO + min(col + j, a.NO - 1)];
     }
+  }
+  // where the gate of output oc stands in a staged row, and its factor
+  const int gate_at = gated ? (oc >> 6) * 128 + (oc & 63) : oc;
+#pragma unroll
+  for (int pass = 0; pass < XF / 2; ++pass) {
+    // token (of the tile) of staged row i
+    auto token = [&](int i) {
+      return (i >> 6) * 32 * XF + pass * 64 + (i & 63);
+    };
+    constexpr int kBatch = 4;
+    u32x4 res[2][kBatch];
+    auto ask = [&](u32x4 (&d)[kBatch], int i0) {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int tok = token(i0 + i * per + (int)threadIdx.x / out_lanes);
+        d[i] = load_residual(a, row0 + min(tok, rows - 1), col);
+      }
+    };
+    // the residual is asked for a batch ahead, first before the staging
+    if constexpr (OUT == kOutBf16) ask(res[0], 0);
+    __syncthreads();
+#pragma unroll
+    for (int f = 0; f < 4; ++f)
+#pragma unroll
+      for (int q4 = 0; q4 < 4; ++q4)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const v16f& v = acc[f][2 * pass + x];
+          *reinterpret_cast<v4f*>(stage +
+                                  (wm * 64 + x * 32 + r32) * kStageLd +
+                                  wn * 128 + f * 32 + 8 * q4 + 4 * g) =
+              v4f{v[4 * q4], v[4 * q4 + 1], v[4 * q4 + 2], v[4 * q4 + 3]};
+        }
     __syncthreads();
 #pragma unroll 1
-    for (int i = 0; i < TM / 16; ++i) {
-      const int tok = i * 16 + wave * 4 + (lane >> 4);
-      const int c = (lane & 15) * 8;
-      const int col = n0 + pass * 128 + c;
-      float v[8];
+    for (int i0 = 0; i0 < 128; i0 += 2 * kBatch * per) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = stage[tok * kStageLd + c + j];
-      store_channels<OUT>(a, row0 + min(tok, rows - 1), col,
-                          tok < rows && col < a.NO, v);
+      for (int h = 0; h < 2; ++h) {
+        const int ih = i0 + h * kBatch * per;
+        if constexpr (OUT == kOutBf16) {
+          if (ih + kBatch * per < 128) ask(res[1 - h], ih + kBatch * per);
+        }
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int at = ih + i * per + (int)threadIdx.x / out_lanes;
+          const int tok = token(at);
+          const float* src = stage + at * kStageLd + gate_at;
+          float v[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] = src[j] + b[j];
+          if (gated) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              v[j] = silu(v[j]) * (src[64 + j] + bu[j]);
+          } else if (a.act == kActSilu) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = silu(v[j]);
+          }
+          store_channels<OUT>(a, row0 + min(tok, rows - 1), col,
+                              tok < rows && col < a.NO, v, res[h][i]);
+        }
+      }
     }
   }
 }
@@ -620,10 +675,8 @@ mxq_status launch_tile(const MatmulArgs& a, hipStream_t s) {
 
 template <int G, int OUT>
 mxq_status launch(const MatmulArgs& a, int64_t expected, hipStream_t s) {
-  if (a.H >= 128) {  // a whole step: the tile kernel's scale reads need one
-    if (expected > 128) return launch_tile<G, 4, OUT>(a, s);
-    if (expected > 64) return launch_tile<G, 2, OUT>(a, s);
-  }
+  if (expected > 128) return launch_tile<G, 4, OUT>(a, s);
+  if (expected > 64) return launch_tile<G, 2, OUT>(a, s);
   if constexpr (OUT == kOutG128) {
     // a group of 128 outputs stays in one block: 128 weight rows, or 256
     if (a.act == kActSiluMul) return launch_small<G, 1, 4, 2, OUT>(a, s);

@@ -54,8 +54,18 @@ __device__ __forceinline__ ExpertRows expert_rows(const MatmulArgs& a, int e) {
   return ExpertRows{first, (int32_t)n};
 }
 
+// x / (1 + exp(-x)).  exp(-x) is the hardware's power of two of -x log2(e),
+// with the part of that product that fp32 cannot hold put back as a factor
+// 1 + ln(2) * rest: its error is a few 2^-24 wherever it counts, and the
+// hardware's reciprocal adds one step.  Beyond 2^+-126 the power is used as
+// it is (0 or infinity included, so silu(inf) = inf).
 __device__ __forceinline__ float silu(float x) {
-  return x / (1.0f + expf(-x));
+  constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
+  const float p = -x * kLog2e;
+  const float rest = fmaf(-x, kLog2e, -p);
+  const float e = __builtin_amdgcn_exp2f(p);
+  const float near = fmaf(e, rest * kLn2, e);
+  return x * __builtin_amdgcn_rcpf(1.0f + (fabsf(p) < 126.0f ? near : e));
 }
 
 // Power-of-two exponent of a group from the fp32 magnitude bits of its
@@ -66,40 +76,45 @@ __device__ __forceinline__ int pow2_exponent_f32(uint32_t m) {
   return e < -127 ? -127 : e;
 }
 
-// Eight finished channels from column c of row r.  The lanes of a group (4
-// for 32 channels, 16 for 128) hold neighbouring columns and are all here.
-// Quantization takes the fp32 values: the only rounding is the payload's.
+// The residual's eight channels from column c of row r (four where the row
+// ends after them: NO % 4 == 0), or zeros.  Reads inside the row only.
+__device__ __forceinline__ u32x4 load_residual(const MatmulArgs& a, int64_t r,
+                                               int c) {
+  u32x4 d{0, 0, 0, 0};
+  if (a.res == nullptr || c >= a.NO) return d;
+  const uint16_t* p = a.res + r * a.ld_r + c;
+  const bool whole = c + 8 <= a.NO;
+  if (a.vec && whole) return load16(p);
+  const uint2 lo = *reinterpret_cast<const uint2*>(p);
+  d.x = lo.x;
+  d.y = lo.y;
+  if (whole) {
+    const uint2 hi = *reinterpret_cast<const uint2*>(p + 4);
+    d.z = hi.x;
+    d.w = hi.y;
+  }
+  return d;
+}
+
+// Eight finished channels from column c of row r, with their residual.  The
+// lanes of a group (4 for 32 channels, 16 for 128) hold neighbouring columns
+// and are all here.  Quantization takes the fp32 values: the only rounding is
+// the payload's.
 template <int OUT>
 __device__ __forceinline__ void store_channels(const MatmulArgs& a, int64_t r,
-                                               int c, bool live,
-                                               float (&v)[8]) {
+                                               int c, bool live, float (&v)[8],
+                                               const u32x4& res) {
   if constexpr (OUT == kOutBf16) {
     if (!live) return;
-    const bool whole = c + 8 <= a.NO;  // else four columns (NO % 4 == 0)
-    if (a.res != nullptr) {
-      const uint16_t* p = a.res + r * a.ld_r + c;
-      u32x4 d{0, 0, 0, 0};
-      if (a.vec && whole) {
-        d = load16(p);
-      } else {
-        const uint2 lo = *reinterpret_cast<const uint2*>(p);
-        d.x = lo.x;
-        d.y = lo.y;
-        if (whole) {
-          const uint2 hi = *reinterpret_cast<const uint2*>(p + 4);
-          d.z = hi.x;
-          d.w = hi.y;
-        }
-      }
-      v[0] += bf16_lo(d.x);
-      v[1] += bf16_hi(d.x);
-      v[2] += bf16_lo(d.y);
-      v[3] += bf16_hi(d.y);
-      v[4] += bf16_lo(d.z);
-      v[5] += bf16_hi(d.z);
-      v[6] += bf16_lo(d.w);
-      v[7] += bf16_hi(d.w);
-    }
+    const bool whole = c + 8 <= a.NO;  // else four columns
+    v[0] += bf16_lo(res.x);
+    v[1] += bf16_hi(res.x);
+    v[2] += bf16_lo(res.y);
+    v[3] += bf16_hi(res.y);
+    v[4] += bf16_lo(res.z);
+    v[5] += bf16_hi(res.z);
+    v[6] += bf16_lo(res.w);
+    v[7] += bf16_hi(res.w);
     uint32_t p[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
