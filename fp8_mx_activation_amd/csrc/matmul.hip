@@ -211,11 +211,14 @@ __global__ __launch_bounds__(64 * NG * KS) void matmul_small_kernel(
 // 64 banks once.  The
 // copy into LDS is linear, hence the chunk order is turned on its global side.
 //
-// Half step h of step k: the fragments of half 1 are read from LDS while half
-// 0 is multiplied, and those of the next step's half 0 while half 1 is.  So a
-// step's buffer is free, and the next one has to have landed, at the one
-// barrier between its halves; the load of step k + 2 is issued right after it
-// and has a whole step to arrive.
+// A step is multiplied in two halves, A with the first half of the wavefront's
+// token fragments, B with the second.  B's token fragments are read from LDS
+// during A; the next step's weight fragments and first token fragments during
+// B, each weight fragment into the registers that its last MFMA has just left.
+// So most of a step's buffer is free when A begins and the rest when B does,
+// and the copies of the step after the next are dealt out evenly over the
+// whole step, one or two steps before they are waited for.  Copied in one half
+// only, they ask for 64 bytes a cycle, all that a CU's L1 can bring.
 //
 // A gated tile takes 128 gate rows and the 128 factor rows of the same
 // outputs; a wavefront holds both for 64 outputs.
@@ -244,10 +247,13 @@ __device__ __forceinline__ void copy_to_lds(const v4i& buf, uint32_t lds,
       : "s"(lds), "v"(voff), "s"(buf), "s"(soff));
 }
 
-// Every load issued so far has landed, in this wavefront and (after the
-// barrier) in the block; LDS reads issued so far have returned.
+// All but the last VM loads and copies and the last LGKM LDS reads issued so
+// far have landed, in this wavefront and, after the barrier, in every
+// wavefront of the block.
+template <int VM, int LGKM>
 __device__ __forceinline__ void landed_barrier() {
-  __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+  __builtin_amdgcn_s_waitcnt((VM & 15) | ((VM >> 4) << 14) | 0x70 |
+                             (LGKM << 8));
   asm volatile("s_barrier" ::: "memory");
 }
 
@@ -320,8 +326,6 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs a,
   constexpr int TM = 64 * XF;
   constexpr int kX = TM * 128;             // bytes of a step's token rows
   constexpr int kStage = kX + 256 * 128;   // and with its weight rows
-  constexpr int kXCopies = TM / 32;        // 1 KB copies per wavefront
-  constexpr int kWCopies = 8;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   TileOf t;
   if (!find_tile<TM>(a, tiles_n, t)) return;
@@ -345,19 +349,23 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs a,
     return (lr & 64) ? a.NO + c : c;
   };
 
-  // copies: lane l of copy i fills place l & 7 of row 8 (wave + 4 i) + (l >> 3)
+  // Copies: 8 rows (1 KB) each, lane l fills place l & 7 of row l >> 3.  The
+  // 64 rows of fragment f of both wavefront columns are two copies per
+  // wavefront, and so are those of fragment x of both wavefront rows.
   const int chunk = (lane & 7) ^ ((4 * wave + (lane >> 4)) & 7);
-  uint32_t xoff[kXCopies], woff[kWCopies];
+  const int crow = wave * 8 + (lane >> 3);
+  uint32_t xoff[XF][2], woff[4][2];
   const int64_t wfirst = n0;
 #pragma unroll
-  for (int i = 0; i < kXCopies; ++i) {
-    const int r = 8 * (wave + 4 * i) + (lane >> 3);
-    xoff[i] = (uint32_t)(min(r, rows - 1) * (int)a.ld_q + 16 * chunk);
-  }
+  for (int i = 0; i < 2; ++i) {
 #pragma unroll
-  for (int i = 0; i < kWCopies; ++i) {
-    const int r = 8 * (wave + 4 * i) + (lane >> 3);
-    woff[i] = (uint32_t)((weight_row(r) - wfirst) * H + 16 * chunk);
+    for (int x = 0; x < XF; ++x)
+      xoff[x][i] = (uint32_t)(min((i * XF + x) * 32 + crow, rows - 1) *
+                              (int)a.ld_q + 16 * chunk);
+#pragma unroll
+    for (int f = 0; f < 4; ++f)
+      woff[f][i] = (uint32_t)(
+          (weight_row(i * 128 + f * 32 + crow) - wfirst) * H + 16 * chunk);
   }
   const v4i xbuf = buffer_of(a.q + row0 * a.ld_q,
                              (uint32_t)((rows - 1) * a.ld_q + H));
@@ -372,16 +380,42 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs a,
   auto step_back = [&](int k) {
     return (uint32_t)(k * 128 + 16 * chunk >= H ? 16 * chunk : 0);
   };
-  auto copy_piece = [&](int k, int i, uint32_t back) {
-    const int k0 = k * 128;
-    const uint32_t at = lds0 + (k & 1) * kStage + wave * 1024;
-    if (i < kXCopies)
-      copy_to_lds(xbuf, at + i * 4096, xoff[i] - back, k0);
-    else
-      copy_to_lds(wbuf, at + kX + (i - kXCopies) * 4096,
-                  woff[i - kXCopies] - back, k0);
+  auto copy_w = [&](int k, int f, int i, uint32_t back) {
+    copy_to_lds(wbuf,
+                lds0 + (k & 1) * kStage + kX + (i * 128 + f * 32) * 128 +
+                    wave * 1024,
+                woff[f][i] - back, k * 128);
   };
-
+  auto copy_x = [&](int k, int x, int i, uint32_t back) {
+    copy_to_lds(xbuf,
+                lds0 + (k & 1) * kStage + (i * XF + x) * 32 * 128 +
+                    wave * 1024,
+                xoff[x][i] - back, k * 128);
+  };
+  // Copy c of half A of a step (8: weight fragments 0-2, token fragment 0),
+  // and of half B (the rest, those that half B reads first).
+  constexpr int kCopiesA = 8, kCopiesB = 2 * XF;
+  auto copy_a = [&](int k, int c, uint32_t back) {
+    if (c < 6)
+      copy_w(k, c >> 1, c & 1, back);
+    else
+      copy_x(k, 0, c & 1, back);
+  };
+  auto copy_b = [&](int k, int c, uint32_t back) {
+    if (XF == 4) {
+      if (c < 2)
+        copy_x(k, 1, c & 1, back);
+      else if (c < 4)
+        copy_w(k, 3, c & 1, back);
+      else
+        copy_x(k, c >> 1, c & 1, back);
+    } else {
+      if (c < 2)
+        copy_w(k, 3, c & 1, back);
+      else
+        copy_x(k, 1, c & 1, back);
+    }
+  };
   // Scales.  A step needs one byte of each token row (G = 128) or four
   // (G = 32): fetched step by step they would cost a scattered load per
   // fragment, so thread r brings 32 bytes of row r at a time into LDS (two
@@ -460,89 +494,134 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs a,
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[f][x][i] = 0.0f;
 
-  // fragments of the two halves of a step, in 16-byte pieces
-  v4i fw[2][4][2], fx[2][XF][2];
-  constexpr int kPieces = 2 * (4 + XF);
-  auto read_piece = [&](int k, int h, int p, auto last) {
-    const int c = h * 4 + (p & 1) * 2 + g;
-    const int off = r32 * 128 + ((c ^ ((r32 >> 1) & 7)) * 16);
-    const uint8_t* stage = lds + (k & 1) * kStage;
+  // fragments of a step, in the 16-byte pieces of its two MFMA steps
+  v4i fw[4][4], fx[XF][4];
+  auto read_rows = [&](int k, int p, int first_row, auto last) {
+    const int c = p * 2 + g;
     v4i v = *reinterpret_cast<const v4i*>(
-        p < 8 ? stage + kX + (wn * 128 + (p >> 1) * 32) * 128 + off
-              : stage + (wm * 32 * XF + ((p - 8) >> 1) * 32) * 128 + off);
+        lds + (k & 1) * kStage + first_row * 128 + r32 * 128 +
+        ((c ^ ((r32 >> 1) & 7)) * 16));
     if constexpr (decltype(last)::value)
       if (k * 128 + 16 * c >= H) v = v4i{0, 0, 0, 0};
-    if (p < 8)
-      fw[h][p >> 1][p & 1] = v;
-    else
-      fx[h][(p - 8) >> 1][p & 1] = v;
+    return v;
   };
-
-  constexpr int kCopies = kXCopies + kWCopies;
-  constexpr int kMfma = 4 * XF;  // of a half step
+  auto read_w = [&](int k, int f, int p, auto last) {
+    fw[f][p] = read_rows(k, p, TM + wn * 128 + f * 32, last);
+  };
+  auto read_x = [&](int k, int x, int p, auto last) {
+    fx[x][p] = read_rows(k, p, wm * 32 * XF + x * 32, last);
+  };
+  constexpr int kXA = XF / 2;  // token fragments of half A, and of half B
+  constexpr int kMfma = 8 * kXA;  // of a half
+  // MFMA i of a half whose first token fragment is x0: weight fragments one
+  // after the other, both channel halves of each
+  auto multiply = [&](int i, int x0) {
+    const int f = i / (2 * kXA), h = i / kXA % 2, x = x0 + i % kXA;
+    if (G == 32 && h == 1)
+      // the second half's scales are two bytes further
+      acc[f][x] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+          join(fw[f][2], fw[f][3]), join(fx[x][2], fx[x][3]), acc[f][x], 0, 0,
+          0, (int)sw[f], 2, (int)sx[x]);
+    else
+      acc[f][x] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+          join(fw[f][2 * h], fw[f][2 * h + 1]),
+          join(fx[x][2 * h], fx[x][2 * h + 1]), acc[f][x], 0, 0, 0,
+          (int)sw[f], 0, (int)sx[x]);
+    __builtin_amdgcn_sched_barrier(0);
+  };
   using Yes = std::true_type;
   using No = std::false_type;
 
   fetch_scales(0);
 #pragma unroll
-  for (int i = 0; i < kCopies; ++i) copy_piece(0, i, step_back(0));
-  put_scales(0);
-  landed_barrier();
-  if (nsteps > 1)
+  for (int c = 0; c < kCopiesA; ++c) copy_a(0, c, step_back(0));
 #pragma unroll
-    for (int i = 0; i < kCopies; ++i) copy_piece(1, i, step_back(1));
+  for (int c = 0; c < kCopiesB; ++c) copy_b(0, c, step_back(0));
+  put_scales(0);
+  landed_barrier<0, 0>();
+  if (nsteps > 1) {
+#pragma unroll
+    for (int c = 0; c < kCopiesA; ++c) copy_a(1, c, step_back(1));
+#pragma unroll
+    for (int c = 0; c < kCopiesB; ++c) copy_b(1, c, step_back(1));
+  }
   read_scales(0);
   use_scales();
 #pragma unroll
-  for (int p = 0; p < kPieces; ++p) read_piece(0, 0, p, Yes{});
+  for (int x = 0; x < kXA; ++x)
+#pragma unroll
+    for (int p = 0; p < 4; ++p) read_x(0, x, p, Yes{});
+#pragma unroll
+  for (int f = 0; f < 4; ++f)
+#pragma unroll
+    for (int p = 0; p < 4; ++p) read_w(0, f, p, Yes{});
+  __builtin_amdgcn_sched_barrier(0);
 
   // One step.  `more`: another one follows; `copy`: and one after that;
-  // `last`: this is, and `next_last`: the next one is, the last.  Reads and
-  // copies are dealt out between the MFMAs, so that neither LDS nor the
-  // memory pipe gets them in one burst while the matrix unit waits.
-  auto step = [&](int k, auto more, auto copy, auto last, auto next_last) {
+  // `last`: this is, and `next_last`: the next one is, the last.  The waits
+  // count the copies that may still be on their way: at barrier A all of the
+  // next step's, at barrier B those of its second token fragments and of the
+  // step after it.  At barrier A the four reads of weight fragment 3, always
+  // the last ones, may be too: its rows are overwritten after barrier B only.
+  auto step = [&](int k, auto more_, auto copy_, auto last, auto next_last) {
+    constexpr bool more = decltype(more_)::value;
+    constexpr bool copy = decltype(copy_)::value;
+    const uint32_t back = step_back(k + 2);
+    landed_barrier<more ? kCopiesA + kCopiesB : 0, 4>();
 #pragma unroll
     for (int i = 0; i < kMfma; ++i) {
+      if constexpr (copy) {
 #pragma unroll
-      for (int p = i * kPieces / kMfma; p < (i + 1) * kPieces / kMfma; ++p)
-        read_piece(k, 1, p, last);
-      const int f = i / XF, x = i % XF;
-      acc[f][x] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-          join(fw[0][f][0], fw[0][f][1]), join(fx[0][x][0], fx[0][x][1]),
-          acc[f][x], 0, 0, 0, (int)sw[f], 0, (int)sx[x]);
-      __builtin_amdgcn_sched_barrier(0);
+        for (int c = i * kCopiesA / kMfma; c < (i + 1) * kCopiesA / kMfma; ++c)
+          copy_a(k + 2, c, back);
+      }
+      if (i < 4) {
+#pragma unroll
+        for (int x = kXA; x < XF; ++x) read_x(k, x, i, last);
+      }
+      multiply(i, 0);
     }
-    landed_barrier();
-    if constexpr (decltype(copy)::value) {
+    if constexpr (more)
+      landed_barrier<copy ? kCopiesA + 2 * kXA : 2 * kXA, 0>();
+    if constexpr (copy) {
       // one chunk ahead: fetched in a chunk's first step, put down in its
-      // second, where the loads have landed
+      // second
       const int next = (k / kPer + 1) * kPer;
       if (k % kPer == 0 && next < nsteps) fetch_scales(k / kPer + 1);
       if (k % kPer == 1 && next < nsteps) put_scales(k / kPer + 1);
     }
-    if constexpr (decltype(more)::value) read_scales(k + 1);
-    const uint32_t back = step_back(k + 2);
+    if constexpr (more) read_scales(k + 1);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < kMfma; ++i) {
-      if constexpr (decltype(copy)::value) {
+      if constexpr (copy) {
 #pragma unroll
-        for (int p = i * kCopies / kMfma; p < (i + 1) * kCopies / kMfma; ++p)
-          copy_piece(k + 2, p, back);
+        for (int c = i * kCopiesB / kMfma; c < (i + 1) * kCopiesB / kMfma; ++c)
+          copy_b(k + 2, c, back);
       }
-      if constexpr (decltype(more)::value) {
+      if constexpr (more) {
+        // a weight fragment's registers take the next step's as soon as its
+        // MFMAs are issued
+        constexpr int kF = 2 * kXA;  // MFMAs of a weight fragment
+        if (i < kF) {
 #pragma unroll
-        for (int p = i * kPieces / kMfma; p < (i + 1) * kPieces / kMfma; ++p)
-          read_piece(k + 1, 0, p, next_last);
+          for (int p = i * 4 / kF; p < (i + 1) * 4 / kF; ++p)
+#pragma unroll
+            for (int x = 0; x < kXA; ++x) read_x(k + 1, x, p, next_last);
+        } else {
+#pragma unroll
+          for (int p = i % kF * 4 / kF; p < (i % kF + 1) * 4 / kF; ++p)
+            read_w(k + 1, i / kF - 1, p, next_last);
+        }
       }
-      const int f = i / XF, x = i % XF;
-      // the second half's scales are two bytes further where a step has four
-      acc[f][x] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-          join(fw[1][f][0], fw[1][f][1]), join(fx[1][x][0], fx[1][x][1]),
-          acc[f][x], 0, 0, 0, (int)sw[f], G == 128 ? 0 : 2, (int)sx[x]);
-      __builtin_amdgcn_sched_barrier(0);
+      multiply(i, kXA);
     }
-    if constexpr (decltype(more)::value) use_scales();
+    if constexpr (more) {
+      use_scales();
+#pragma unroll
+      for (int p = 0; p < 4; ++p) read_w(k + 1, 3, p, next_last);
+    }
+    __builtin_amdgcn_sched_barrier(0);
   };
   int k = 0;
   for (; k + 2 < nsteps; ++k) step(k, Yes{}, Yes{}, No{}, No{});
