@@ -320,7 +320,7 @@ constexpr int tile_lds_bytes() {
   return loop > end ? loop : end;
 }
 
-template <int G, int XF, int OUT>
+template <int G, int XF, int OUT, bool GATED>
 __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs a,
                                                              int32_t tiles_n) {
   constexpr int TM = 64 * XF;
@@ -332,8 +332,7 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs a,
   const ExpertRows er = expert_rows(a, t.e);
   const int rows = min(er.count - t.m0, TM);  // live rows of this tile
   const int64_t row0 = er.first + t.m0;
-  const bool gated = a.act == kActSiluMul;
-  const int n0 = t.n * (gated ? 128 : 256);
+  const int n0 = t.n * (GATED ? 128 : 256);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 1, wn = wave & 1;
@@ -344,7 +343,7 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs a,
 
   // weight row (within the expert's matrix) of local row lr of the tile
   auto weight_row = [&](int lr) {
-    if (!gated) return min(n0 + lr, a.N - 1);
+    if (!GATED) return min(n0 + lr, a.N - 1);
     const int c = min(n0 + (lr >> 7) * 64 + (lr & 63), a.NO - 1);
     return (lr & 64) ? a.NO + c : c;
   };
@@ -451,11 +450,11 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs a,
 #pragma unroll
     for (int j = 0; j < 8; ++j) d[j] = xs_next[j];
   };
-  const int up_block = (a.NO + n0) / 128;  // of a gated tile's factor rows
+  const int up_block = (a.NO + n0) / 128;  // of a GATED tile's factor rows
   for (int i = threadIdx.x; i < 3 * nws; i += 256) {
     const int b = i / nws;
     const int block = b == 0 ? n0 / 128
-                      : gated ? up_block + b - 1 : n0 / 128 + b;
+                      : GATED ? up_block + b - 1 : n0 / 128 + b;
     if (block < nwb)
       wscale[b * kMaxSteps + i % nws] =
           a.ws[((int64_t)t.e * nwb + block) * nws + i % nws];
@@ -464,7 +463,7 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs a,
 #pragma unroll
   for (int f = 0; f < 4; ++f) {
     const int block = weight_row(wn * 128 + f * 32 + r32) / 128;
-    wsoff[f] = (gated && f >= 2 ? block - up_block + 1 : block - n0 / 128) *
+    wsoff[f] = (GATED && f >= 2 ? block - up_block + 1 : block - n0 / 128) *
                kMaxSteps;
   }
   uint32_t sx[XF], sw[4], sx1[XF], sw1[4];  // of this step and the next one
@@ -633,10 +632,12 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs a,
   // channels of a row: gate and factor meet, a row is written in whole lines,
   // and a quantization group lies within a wavefront.
   float* stage = reinterpret_cast<float*>(lds);
-  const int out_lanes = gated ? 16 : 32;  // threads per row
-  const int oc = (int)threadIdx.x % out_lanes * 8;
+  constexpr int kOutLanes = GATED ? 16 : 32;  // threads per row
+  constexpr int kPerRound = 256 / kOutLanes;  // rows per round of the block
+  constexpr int kRounds = 128 / kPerRound;
+  const int orow = (int)threadIdx.x / kOutLanes;
+  const int oc = (int)threadIdx.x % kOutLanes * 8;
   const int col = n0 + oc;
-  const int per = 256 / out_lanes;  // rows per round of the block
   float b[8], bu[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) b[j] = bu[j] = 0.0f;
@@ -645,28 +646,35 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs a,
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       b[j] = br[min(col + j, a.NO - 1)];
-      if (gated) bu[j] = br[a.NO + min(col + j, a.NO - 1)];
+      if (GATED) bu[j] = br[a.NO + min(col + j, a.NO - 1)];
     }
   }
-  // where the gate of output oc stands in a staged row, and its factor
-  const int gate_at = gated ? (oc >> 6) * 128 + (oc & 63) : oc;
+  // where the gate of output oc stands in a staged row; its factor is 64 on
+  const int gate_at = GATED ? (oc >> 6) * 128 + (oc & 63) : oc;
+  // token (of the tile) of row i of pass p
+  auto token = [&](int p, int i) {
+    return (i >> 6) * 32 * XF + p * 64 + (i & 63);
+  };
+  constexpr int kPasses = XF / 2;
+  // A pass's residual is asked for a pass ahead, the first one's before its
+  // staging: the loads are in flight together and behind other work.
+  u32x4 res[2][kRounds];
+  auto ask = [&](int p) {
 #pragma unroll
-  for (int pass = 0; pass < XF / 2; ++pass) {
-    // token (of the tile) of staged row i
-    auto token = [&](int i) {
-      return (i >> 6) * 32 * XF + pass * 64 + (i & 63);
-    };
-    constexpr int kBatch = 4;
-    u32x4 res[2][kBatch];
-    auto ask = [&](u32x4 (&d)[kBatch], int i0) {
+    for (int i = 0; i < kRounds; ++i)
+      res[p & 1][i] = load_residual(
+          a, row0 + min(token(p, i * kPerRound + orow), rows - 1), col);
+  };
+  const bool has_res = OUT == kOutBf16 && a.res != nullptr;
+  if (has_res) {
+    ask(0);
+  } else {
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int tok = token(i0 + i * per + (int)threadIdx.x / out_lanes);
-        d[i] = load_residual(a, row0 + min(tok, rows - 1), col);
-      }
-    };
-    // the residual is asked for a batch ahead, first before the staging
-    if constexpr (OUT == kOutBf16) ask(res[0], 0);
+    for (int i = 0; i < kRounds; ++i)
+      res[0][i] = res[1][i] = u32x4{0, 0, 0, 0};
+  }
+#pragma unroll
+  for (int pass = 0; pass < kPasses; ++pass) {
     __syncthreads();
 #pragma unroll
     for (int f = 0; f < 4; ++f)
@@ -681,34 +689,24 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs a,
               v4f{v[4 * q4], v[4 * q4 + 1], v[4 * q4 + 2], v[4 * q4 + 3]};
         }
     __syncthreads();
-#pragma unroll 1
-    for (int i0 = 0; i0 < 128; i0 += 2 * kBatch * per) {
+    if (has_res && pass + 1 < kPasses) ask(pass + 1);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int ih = i0 + h * kBatch * per;
-        if constexpr (OUT == kOutBf16) {
-          if (ih + kBatch * per < 128) ask(res[1 - h], ih + kBatch * per);
-        }
+    for (int i = 0; i < kRounds; ++i) {
+      const int at = i * kPerRound + orow;
+      const int tok = token(pass, at);
+      const float* src = stage + at * kStageLd + gate_at;
+      float v[8];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int at = ih + i * per + (int)threadIdx.x / out_lanes;
-          const int tok = token(at);
-          const float* src = stage + at * kStageLd + gate_at;
-          float v[8];
+      for (int j = 0; j < 8; ++j) v[j] = src[j] + b[j];
+      if constexpr (GATED) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] = src[j] + b[j];
-          if (gated) {
+        for (int j = 0; j < 8; ++j) v[j] = silu(v[j]) * (src[64 + j] + bu[j]);
+      } else if (a.act == kActSilu) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              v[j] = silu(v[j]) * (src[64 + j] + bu[j]);
-          } else if (a.act == kActSilu) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = silu(v[j]);
-          }
-          store_channels<OUT>(a, row0 + min(tok, rows - 1), col,
-                              tok < rows && col < a.NO, v, res[h][i]);
-        }
+        for (int j = 0; j < 8; ++j) v[j] = silu(v[j]);
       }
+      store_channels<OUT>(a, row0 + min(tok, rows - 1), col,
+                          tok < rows && col < a.NO, v, res[pass & 1][i]);
     }
   }
 }
@@ -741,7 +739,8 @@ mxq_status launch_tile(const MatmulArgs& a, hipStream_t s) {
   const int64_t blocks = ceil_div(tm * tn, 8) * 8;
   if (blocks > INT32_MAX) return MXQ_ERR_UNSUPPORTED;
   constexpr int lds = tile_lds_bytes<XF>();
-  auto* k = &matmul_tile_kernel<G, XF, OUT>;
+  auto* k = a.act == kActSiluMul ? &matmul_tile_kernel<G, XF, OUT, true>
+                                 : &matmul_tile_kernel<G, XF, OUT, false>;
   if (hipFuncSetAttribute(reinterpret_cast<const void*>(k),
                           hipFuncAttributeMaxDynamicSharedMemorySize,
                           lds) != hipSuccess) {

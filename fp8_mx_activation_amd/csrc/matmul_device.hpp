@@ -54,18 +54,14 @@ __device__ __forceinline__ ExpertRows expert_rows(const MatmulArgs& a, int e) {
   return ExpertRows{first, (int32_t)n};
 }
 
-// x / (1 + exp(-x)).  exp(-x) is the hardware's power of two of -x log2(e),
-// with the part of that product that fp32 cannot hold put back as a factor
-// 1 + ln(2) * rest: its error is a few 2^-24 wherever it counts, and the
-// hardware's reciprocal adds one step.  Beyond 2^+-126 the power is used as
-// it is (0 or infinity included, so silu(inf) = inf).
+// x / (1 + exp(-x)) with the hardware's power of two and reciprocal.  The
+// product -x log2(e) is rounded once, so exp(-x) is off by a factor of at most
+// 1 + (|x| + 2) 2^-24; beyond fp32's range it is 0 or infinity, and the
+// quotient x or -0.
 __device__ __forceinline__ float silu(float x) {
-  constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
-  const float p = -x * kLog2e;
-  const float rest = fmaf(-x, kLog2e, -p);
-  const float e = __builtin_amdgcn_exp2f(p);
-  const float near = fmaf(e, rest * kLn2, e);
-  return x * __builtin_amdgcn_rcpf(1.0f + (fabsf(p) < 126.0f ? near : e));
+  constexpr float kLog2e = 1.44269504088896341f;
+  return x * __builtin_amdgcn_rcpf(1.0f +
+                                   __builtin_amdgcn_exp2f(-x * kLog2e));
 }
 
 // Power-of-two exponent of a group from the fp32 magnitude bits of its

@@ -193,12 +193,16 @@ def expert_matmul(q, scales, group, w, ws, offsets, counts, bias, act,
         run = [np.abs(v).reshape(v.shape[0], -1, 16).max(-1) for v in (x, m)]
         d = (H + 1) * 2.0 ** -23 * size + 2.0 ** -8 * (run[0] @ run[1].T)
         if act != "none":
-            # |silu'| < 1.1; exp, sum and quotient are off by a few steps
+            # |silu'| < 1.1.  exp(-x) of a product -x log2(e) rounded to fp32
+            # (half a step: 2^-24 |x| log2(e), times ln(2) in the power) is
+            # off by a factor 1 + |x| 2^-24, and so is the quotient at most;
+            # the power, sum, quotient and product add up to 2^-21
             gate = y[:, :cols] if act == "silu_mul" else y
             dg = d[:, :cols] if act == "silu_mul" else d
             with np.errstate(over="ignore"):
                 s = gate / (1 + np.exp(-gate))
-            ds = 1.1 * dg + 2.0 ** -21 * np.abs(s)
+            ds = 1.1 * dg + (2.0 ** -21 + 2.0 ** -24 * np.abs(gate)) * \
+                np.abs(s)
             if act == "silu_mul":
                 u, du = y[:, cols:], d[:, cols:]
                 y, d = s * u, ds * np.abs(u) + (np.abs(s) + ds) * du
