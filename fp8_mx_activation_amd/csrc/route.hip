@@ -9,7 +9,8 @@
 // One wavefront per token; lane i owns the PER consecutive experts from
 // i * PER, so a row is one vector load per lane, and the lowest lane that
 // holds the maximum also holds the lowest index.  Each of the K choices is
-// one wavefront maximum of ordered integer keys (DPP, no LDS memory).
+// one wavefront maximum of ordered integer keys (six v_max with DPP operands
+// for 32 bits, twice that for 64; no LDS memory).
 //
 // Choice values are computed and compared in 64 bits wherever they come out
 // of an exponential: near a tie two experts' values lie closer than fp32
@@ -22,6 +23,8 @@
 // Bound: a row of E logits is 0.5-4 KB, so even 8192 tokens are one or two
 // microseconds of HBM time; the kernel is bound by the K dependent
 // reductions of one wavefront.
+#include <type_traits>
+
 #include "mxq_device.hpp"
 #include "mxq_host.hpp"
 
@@ -47,28 +50,40 @@ __device__ __forceinline__ uint64_t dpp64(uint64_t old, uint64_t v) {
   return ((uint64_t)hi << 32) | lo;
 }
 
-__device__ __forceinline__ uint64_t lane63(uint64_t v) {
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), 63);
+// Each step combines a lane with one below it (rows of 16 lanes by shifts of
+// 1, 2, 4 and 8, then across rows), so lane 63 ends with the whole
+// wavefront's value.  A lane with no source takes 0, the lowest key: a step is
+// one v_max with a DPP operand.
+template <int CTRL>
+__device__ __forceinline__ uint32_t max_step(uint32_t v) {
+  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF,
+                                                      0xF, true));
+}
+
+__device__ __forceinline__ uint32_t wave_max_key(uint32_t v) {
+  v = max_step<0x111>(v);
+  v = max_step<0x112>(v);
+  v = max_step<0x114>(v);
+  v = max_step<0x118>(v);
+  v = max_step<0x142>(v);
+  v = max_step<0x143>(v);
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
+// A 64-bit key by halves: the low half decides among the lanes that hold the
+// largest high half.
+__device__ __forceinline__ uint64_t wave_max_key(uint64_t v) {
+  const uint32_t hi = wave_max_key((uint32_t)(v >> 32));
+  const uint32_t lo =
+      wave_max_key((uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
   return ((uint64_t)hi << 32) | lo;
 }
 
-// Each step combines a lane with one below it (rows of 16 lanes by shifts of
-// 1, 2, 4 and 8, then across rows), so lane 63 ends with the whole
-// wavefront's value.  A lane with no source keeps `old`.
-template <int CTRL, int ROWS>
-__device__ __forceinline__ uint64_t max_step(uint64_t v) {
-  return max(v, dpp64<CTRL, ROWS>(v, v));
-}
-
-__device__ __forceinline__ uint64_t wave_max64(uint64_t v) {
-  v = max_step<0x111, 0xF>(v);
-  v = max_step<0x112, 0xF>(v);
-  v = max_step<0x114, 0xF>(v);
-  v = max_step<0x118, 0xF>(v);
-  v = max_step<0x142, 0xA>(v);
-  v = max_step<0x143, 0xC>(v);
-  return lane63(v);
+__device__ __forceinline__ uint64_t from_lane(uint64_t v, int lane) {
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
+  const uint32_t hi =
+      (uint32_t)__builtin_amdgcn_readlane((int)(v >> 32), lane);
+  return ((uint64_t)hi << 32) | lo;
 }
 
 template <int CTRL, int ROWS>
@@ -84,7 +99,8 @@ __device__ __forceinline__ double wave_sum64(double v) {
   v = sum_step<0x118, 0xF>(v);
   v = sum_step<0x142, 0xA>(v);
   v = sum_step<0x143, 0xC>(v);
-  return __builtin_bit_cast(double, lane63(__builtin_bit_cast(uint64_t, v)));
+  return __builtin_bit_cast(double,
+                            from_lane(__builtin_bit_cast(uint64_t, v), 63));
 }
 
 // ------------------------------------------------------------ ordered keys
@@ -100,6 +116,31 @@ __device__ __forceinline__ uint64_t key_of(double v) {
 __device__ __forceinline__ double value_of(uint64_t k) {
   const uint64_t b = (k >> 63) ? k & ~(1ull << 63) : ~k;
   return __builtin_bit_cast(double, b);
+}
+
+__device__ __forceinline__ uint32_t key_of(float v) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, v + 0.0f);
+  const uint32_t k = (b >> 31) ? ~b : b | (1u << 31);
+  return v > -__builtin_inff() ? k : 0;
+}
+
+__device__ __forceinline__ float value_of(uint32_t k) {
+  const uint32_t b = (k >> 31) ? k & ~(1u << 31) : ~k;
+  return __builtin_bit_cast(float, b);
+}
+
+// The two largest keys of a group: (a1, a2) joined with (b1, b2).
+__device__ __forceinline__ void join_top2(uint64_t& a1, uint64_t& a2,
+                                          uint64_t b1, uint64_t b2) {
+  const uint64_t lesser = min(a1, b1);
+  a1 = max(a1, b1);
+  a2 = max(lesser, max(a2, b2));
+}
+
+// Joined with the lane that DPP control CTRL pairs this one with.
+template <int CTRL>
+__device__ __forceinline__ void join_paired(uint64_t& a1, uint64_t& a2) {
+  join_top2(a1, a2, dpp64<CTRL, 0xF>(0, a1), dpp64<CTRL, 0xF>(0, a2));
 }
 
 // --------------------------------------------------------------- row access
@@ -221,8 +262,10 @@ struct RouteArgs {
 
 constexpr int kMaxGroups = 64;
 
-template <int PER, bool BF16>
+// WIDE: 64-bit choice values; else the logits themselves are the choice.
+template <int PER, bool BF16, bool WIDE>
 __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
+  using Key = std::conditional_t<WIDE, uint64_t, uint32_t>;
   const int lane = threadIdx.x & 63;
   const int64_t t = (int64_t)blockIdx.x * (blockDim.x >> 6) +
                     __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -234,29 +277,19 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
   float l[PER];
   load_logits<PER, BF16>(row, E, e0, a.vec != 0, l);
 
-  // the row's maximum, for the softmax's exponentials
-  float top = -__builtin_inff();
-  double z = 0.0;
-  const bool plain = !a.sigmoid && a.bias == nullptr && a.groups == 1;
+  // a softmax's largest logit, and the sum of its exponentials where a single
+  // one depends on it
+  double top = 0.0, z = 1.0;
   if (!a.sigmoid) {
     float m = l[0];
 #pragma unroll
     for (int i = 1; i < PER; ++i) m = fmaxf(m, l[i]);
-    const uint64_t k = wave_max64(key_of((double)m));
-    top = k ? (float)value_of(k) : 0.0f;
+    const uint32_t k = wave_max_key(key_of(m));
+    top = k ? (double)value_of(k) : 0.0;
   }
 
-  uint64_t key[PER];
-  if (plain) {
-#pragma unroll
-    for (int i = 0; i < PER; ++i) key[i] = key_of((double)l[i]);
-    if (!a.renorm) {
-      double part = 0.0;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) part += exp((double)l[i] - (double)top);
-      z = wave_sum64(part);
-    }
-  } else {
+  Key key[PER];
+  if constexpr (WIDE) {
     double s[PER];
     if (a.sigmoid) {
 #pragma unroll
@@ -265,113 +298,132 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
       double part = 0.0;
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
-        s[i] = exp((double)l[i] - (double)top);
+        s[i] = exp((double)l[i] - top);
         part += s[i];
       }
       z = wave_sum64(part);
 #pragma unroll
       for (int i = 0; i < PER; ++i) s[i] = s[i] / z;
     }
+    if (a.bias != nullptr) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const bool live = l[i] > -__builtin_inff();
-      double c = s[i];
-      if (a.bias != nullptr && e0 + i < E) c += (double)a.bias[e0 + i];
-      key[i] = live ? key_of(c) : 0;
+      for (int i = 0; i < PER; ++i)
+        if (e0 + i < E) s[i] += (double)a.bias[e0 + i];
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      key[i] = l[i] > -__builtin_inff() ? key_of(s[i]) : 0;
+  } else {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) key[i] = key_of(l[i]);
+    if (!a.renorm) {
+      double part = 0.0;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) part += exp((double)l[i] - top);
+      z = wave_sum64(part);
     }
   }
 
-  if (a.groups > 1) {
-    // Group value: the sum of the group's two largest choice values.  A
-    // group without a live expert has none and is kept only when too few
-    // groups have one (nothing of it can be chosen either way).
-    const int gs = E / a.groups;
-    uint64_t mine = 0;  // lane g: the key of group g's value
-    for (int g = 0; g < a.groups; ++g) {
-      const int lo = g * gs, hi = lo + gs;
-      uint64_t m1 = 0;
+  if constexpr (WIDE) {
+    if (a.groups > 1) {
+      // Group value: the sum of the group's two largest choice values.  A
+      // group without a live expert has none and is never kept.
+      const int gs = E / a.groups;
+      const int lanes = gs / PER;  // of a group
+      uint64_t value = 0;          // key of the lane's group's value
+      int group = 0;
+      const bool aligned = lanes * PER == gs && lanes <= 16 &&
+                           (lanes & (lanes - 1)) == 0;
+      if (aligned) {
+        // a group is 1, 2, 4, 8 or 16 neighbouring lanes of a DPP row: joined
+        // pairwise (quad permutes, then mirrors of 8 and 16 lanes), all
+        // groups at once
+        uint64_t m1 = key[0], m2 = 0;
 #pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (e0 + i >= lo && e0 + i < hi) m1 = max(m1, key[i]);
-      const uint64_t first = wave_max64(m1);
-      uint64_t gk = 0;
-      if (first != 0) {
-        // the lowest lane that holds it drops its first copy
-        const bool owner =
-            lane == __ffsll((unsigned long long)__ballot(m1 == first)) - 1;
-        bool dropped = !owner;
-        uint64_t m2 = 0;
+        for (int i = 1; i < PER; ++i) join_top2(m1, m2, key[i], 0);
+        if (lanes >= 2) join_paired<0xB1>(m1, m2);
+        if (lanes >= 4) join_paired<0x4E>(m1, m2);
+        if (lanes >= 8) join_paired<0x141>(m1, m2);
+        if (lanes >= 16) join_paired<0x140>(m1, m2);
+        if (m1 != 0)
+          value = key_of(value_of(m1) + (m2 ? value_of(m2) : 0.0));
+        group = lane / max(lanes, 1);
+        // kept: fewer than top_groups others are better (an equal one with a
+        // lower index is)
+        int better = 0;
+        for (int g = 0; g < a.groups; ++g) {
+          const uint64_t v = from_lane(value, g * lanes);
+          better += v > value || (v == value && g < group);
+        }
+        const bool keep = better < a.top_groups && value != 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) key[i] = keep ? key[i] : 0;
+      } else {
+        uint64_t mine = 0;  // lane g: the key of group g's value
+        for (int g = 0; g < a.groups; ++g) {
+          const int lo = g * gs, hi = lo + gs;
+          uint64_t m1 = 0, m2 = 0;
+#pragma unroll
+          for (int i = 0; i < PER; ++i)
+            if (e0 + i >= lo && e0 + i < hi) join_top2(m1, m2, key[i], 0);
+          const uint64_t first = wave_max_key(m1);
+          if (first == 0) continue;
+          // the lowest lane that holds it offers its second instead
+          const int owner =
+              __ffsll((unsigned long long)__ballot(m1 == first)) - 1;
+          const uint64_t second = wave_max_key(lane == owner ? m2 : m1);
+          const uint64_t gk =
+              key_of(value_of(first) + (second ? value_of(second) : 0.0));
+          if (lane == g) mine = gk;
+        }
+        uint64_t kept = 0;  // bit g: group g may be chosen from
+        for (int n = 0; n < a.top_groups; ++n) {
+          const uint64_t best = wave_max_key(mine);
+          if (best == 0) break;
+          const int g =
+              __ffsll((unsigned long long)__ballot(mine == best)) - 1;
+          kept |= 1ull << g;
+          if (lane == g) mine = 0;
+        }
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-          if (e0 + i < lo || e0 + i >= hi) continue;
-          if (!dropped && key[i] == first)
-            dropped = true;
-          else
-            m2 = max(m2, key[i]);
+          const int g = min((e0 + i) / gs, kMaxGroups - 1);
+          if (!((kept >> g) & 1)) key[i] = 0;
         }
-        const uint64_t second = wave_max64(m2);
-        gk = key_of(value_of(first) + (second ? value_of(second) : 0.0));
       }
-      if (lane == g) mine = gk;
-    }
-    uint64_t kept = 0;  // bit g: group g may be chosen from
-    for (int n = 0; n < a.top_groups; ++n) {
-      const uint64_t best = wave_max64(mine);
-      if (best == 0) break;
-      const int g = __ffsll((unsigned long long)__ballot(mine == best)) - 1;
-      kept |= 1ull << g;
-      if (lane == g) mine = 0;
-    }
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int g = min((e0 + i) / gs, kMaxGroups - 1);
-      if (!((kept >> g) & 1)) key[i] = 0;
     }
   }
 
   // K choices; lane j keeps the j-th
   int my_id = -1;
-  float my_l = -__builtin_inff();
   for (int j = 0; j < a.K; ++j) {
-    uint64_t m = key[0];
+    Key m = key[0];
+    int at = 0;  // lowest of the lane's experts that holds m
 #pragma unroll
-    for (int i = 1; i < PER; ++i) m = max(m, key[i]);
-    const uint64_t best = wave_max64(m);
+    for (int i = 1; i < PER; ++i) {
+      at = key[i] > m ? i : at;
+      m = max(m, key[i]);
+    }
+    const Key best = wave_max_key(m);
     if (best == 0) break;  // nothing left: ids from here on stay -1
     const int from = __ffsll((unsigned long long)__ballot(m == best)) - 1;
-    int at = 0;
-    float lv = 0.0f;
-    bool found = false;
+    const int taken = __builtin_amdgcn_readlane(at, from);
+    if (lane == j) my_id = from * PER + taken;
+    const int mark = lane == from ? taken : -1;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      if (!found && key[i] == best) {
-        found = true;
-        at = i;
-        lv = l[i];
-        if (lane == from) key[i] = 0;
-      }
-    }
-    const int id = from * PER + __builtin_amdgcn_readlane(at, from);
-    const int lb =
-        __builtin_amdgcn_readlane(__builtin_bit_cast(int, lv), from);
-    if (lane == j) {
-      my_id = id;
-      my_l = __builtin_bit_cast(float, lb);
-    }
+    for (int i = 0; i < PER; ++i) key[i] = mark == i ? 0 : key[i];
   }
 
   double p = 0.0;
   if (my_id >= 0) {
-    if (a.sigmoid) {
-      p = sigmoid64(my_l);
-    } else {
-      p = exp((double)my_l - (double)top);
-      if (!a.renorm) p = p / z;
-    }
+    const float mine = logit_at<BF16>(row, my_id);
+    p = a.sigmoid ? sigmoid64(mine) : exp((double)mine - top);
   }
   if (a.renorm) {
     const double total = wave_sum64(p);
     p = total > 0.0 ? p / total : 0.0;
+  } else {
+    p = z > 0.0 ? p / z : 0.0;  // 0: no live expert
   }
   if (lane < a.K) {
     a.ids[t * a.K + lane] = my_id;
@@ -439,8 +491,8 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteBackArgs a) {
     }
     d = has ? ds * s * (1.0 - s) : 0.0;
   } else if (a.renorm) {
-    const uint64_t k = wave_max64(key_of((double)lj));
-    const double top = k ? value_of(k) : 0.0;
+    const uint32_t k = wave_max_key(key_of(lj));
+    const double top = k ? (double)value_of(k) : 0.0;
     const double x = has ? exp((double)lj - top) : 0.0;
     const double total = wave_sum64(x);
     const double q = total > 0.0 ? x / total : 0.0;
@@ -451,8 +503,8 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteBackArgs a) {
     float m = l[0];
 #pragma unroll
     for (int i = 1; i < PER; ++i) m = fmaxf(m, l[i]);
-    const uint64_t k = wave_max64(key_of((double)m));
-    const double top = k ? value_of(k) : 0.0;
+    const uint32_t k = wave_max_key(key_of(m));
+    const double top = k ? (double)value_of(k) : 0.0;
     double part = 0.0;
     double x[PER];
 #pragma unroll
@@ -470,12 +522,8 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteBackArgs a) {
     for (int i = 0; i < PER; ++i) full[i] = -x[i] * inv * dot;
     for (int j = 0; j < a.K; ++j) {
       const int idj = __builtin_amdgcn_readlane(id, j);
-      const uint64_t db = __builtin_bit_cast(uint64_t, d);
-      const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)db, j);
-      const uint32_t hi =
-          (uint32_t)__builtin_amdgcn_readlane((int)(db >> 32), j);
-      const double dj =
-          __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+      const double dj = __builtin_bit_cast(
+          double, from_lane(__builtin_bit_cast(uint64_t, d), j));
 #pragma unroll
       for (int i = 0; i < PER; ++i)
         if (idj == e0 + i) full[i] += dj;
@@ -506,7 +554,7 @@ inline bool row_vec(const void* p, int64_t ld, int64_t esz) {
   return aligned16(p) && (ld * esz) % 16 == 0;
 }
 
-template <bool BF16, typename F>
+template <typename F>
 void by_experts(int32_t E, F&& f) {
   if (E <= 64)
     f(std::integral_constant<int, 1>{});
@@ -553,16 +601,17 @@ extern "C" mxq_status moe_route(const void* logits, mxq_out_dtype dtype,
               topk_ids,   topk_weights};
   const unsigned blocks = (unsigned)ceil_div(T, waves);
   hipStream_t s = as_stream(stream);
-  if (dtype == MXQ_OUT_BF16)
-    by_experts<true>(E, [&](auto per) {
-      route_kernel<decltype(per)::value, true>
-          <<<blocks, waves * 64, 0, s>>>(a);
-    });
-  else
-    by_experts<false>(E, [&](auto per) {
-      route_kernel<decltype(per)::value, false>
-          <<<blocks, waves * 64, 0, s>>>(a);
-    });
+  // a softmax keeps the order of its logits
+  const bool wide = a.sigmoid || bias != nullptr || num_groups > 1;
+  by_experts(E, [&](auto per) {
+    constexpr int kPer = decltype(per)::value;
+    if (dtype == MXQ_OUT_BF16)
+      wide ? route_kernel<kPer, true, true><<<blocks, waves * 64, 0, s>>>(a)
+           : route_kernel<kPer, true, false><<<blocks, waves * 64, 0, s>>>(a);
+    else
+      wide ? route_kernel<kPer, false, true><<<blocks, waves * 64, 0, s>>>(a)
+           : route_kernel<kPer, false, false><<<blocks, waves * 64, 0, s>>>(a);
+  });
   return launch_status();
 }
 
@@ -590,15 +639,12 @@ extern "C" mxq_status moe_route_backward(
                   row_vec(grad_logits, ld_grad, esz), grad_logits, ld_grad};
   const unsigned blocks = (unsigned)ceil_div(T, waves);
   hipStream_t s = as_stream(stream);
-  if (dtype == MXQ_OUT_BF16)
-    by_experts<true>(E, [&](auto per) {
-      route_backward_kernel<decltype(per)::value, true>
-          <<<blocks, waves * 64, 0, s>>>(a);
-    });
-  else
-    by_experts<false>(E, [&](auto per) {
-      route_backward_kernel<decltype(per)::value, false>
-          <<<blocks, waves * 64, 0, s>>>(a);
-    });
+  by_experts(E, [&](auto per) {
+    constexpr int kPer = decltype(per)::value;
+    if (dtype == MXQ_OUT_BF16)
+      route_backward_kernel<kPer, true><<<blocks, waves * 64, 0, s>>>(a);
+    else
+      route_backward_kernel<kPer, false><<<blocks, waves * 64, 0, s>>>(a);
+  });
   return launch_status();
 }
