@@ -23,205 +23,7 @@ namespace {
 
 using namespace mxq;
 
-// ------------------------------------------------------------ few rows
-//
-// Weights are what few rows read: each is needed once per 16 MT rows, so it
-// goes from memory straight into the registers of the one wavefront that
-// multiplies it, with no LDS and no barrier.  A block owns 64 NG weight rows
-// of one expert and all rows of that expert; its wavefronts split the weight
-// rows in groups of 64 and the K axis in KS interleaved parts (neighbouring
-// 128-byte lines are in flight at once), joined in LDS at the end.  The weight
-// rows are the MFMA's A operand, the token rows its B operand, so a lane ends
-// up with four neighbouring output channels of one token.
-//
-// A 16x16x128 step: lane l = 16 g + r holds channels 16 g + [0, 16) and
-// 64 + 16 g + [0, 16) of row r; the scale of 32-channel block g of row r
-// comes from lane l.
-template <int MT>
-struct SmallStep {
-  v4i w[4][2];
-  v4i x[MT][2];
-  int sw[4];
-  int sx[MT];
-};
-
-__device__ __forceinline__ v8i join(const v4i& a, const v4i& b) {
-  return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-}
-
-template <int G, int MT, int NG, int KS, int OUT>
-__global__ __launch_bounds__(64 * NG * KS) void matmul_small_kernel(
-    MatmulArgs a, int32_t blocks_n) {
-  constexpr int NB = 64 * NG;
-  constexpr int LDT = NB + 4;  // floats per staged token
-  extern __shared__ __attribute__((aligned(16))) float part[];
-  const int e = blockIdx.x / blocks_n;
-  const ExpertRows er = expert_rows(a, e);
-  if (er.count == 0) return;
-  const bool gated = a.act == kActSiluMul;
-  const int nbo = gated ? NB / 2 : NB;
-  const int n0 = (int)(blockIdx.x % blocks_n) * nbo;
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int ng = wave / KS, ks = wave % KS;
-  const int r16 = lane & 15, g = lane >> 4;
-  const int H = a.H;
-  const int nsteps = (H + 127) / 128;
-
-  // weight row of the lane in each fragment, clamped to the matrix
-  const uint8_t* wrow[4];
-  const uint8_t* wsrow[4];
-#pragma unroll
-  for (int f = 0; f < 4; ++f) {
-    const int lr = ng * 64 + f * 16 + r16;
-    int n;
-    if (gated)
-      n = lr < nbo ? min(n0 + lr, a.NO - 1)
-                   : a.NO + min(n0 + lr - nbo, a.NO - 1);
-    else
-      n = min(n0 + lr, a.N - 1);
-    wrow[f] = a.w + ((int64_t)e * a.N + n) * H + 16 * g;
-    wsrow[f] = a.ws + ((int64_t)e * ((a.N + 127) / 128) + n / 128) * a.nbk;
-  }
-
-  for (int base = 0; base < er.count; base += 16 * MT) {
-    const uint8_t* xrow[MT];
-    const uint8_t* sxrow[MT];
-    v4f acc[4][MT];
-#pragma unroll
-    for (int x = 0; x < MT; ++x) {
-      const int64_t row =
-          er.first + min(base + x * 16 + r16, er.count - 1);
-      xrow[x] = a.q + row * a.ld_q + 16 * g;
-      sxrow[x] = a.s + row * a.ld_s;
-#pragma unroll
-      for (int f = 0; f < 4; ++f) acc[f][x] = v4f{0, 0, 0, 0};
-    }
-    auto load = [&](SmallStep<MT>& t, int step) {
-      const int k0 = step * 128;
-      // the last step may end inside the 128 channels (H % 32 == 0): what
-      // lies past H is zero, with a scale of one
-      const bool lo = k0 + 16 * g < H, hi = k0 + 64 + 16 * g < H;
-      const v4i zero{0, 0, 0, 0};
-#pragma unroll
-      for (int f = 0; f < 4; ++f) {
-        t.w[f][0] =
-            lo ? *reinterpret_cast<const v4i*>(wrow[f] + k0) : zero;
-        t.w[f][1] =
-            hi ? *reinterpret_cast<const v4i*>(wrow[f] + k0 + 64) : zero;
-        t.sw[f] = wsrow[f][step];
-      }
-#pragma unroll
-      for (int x = 0; x < MT; ++x) {
-        t.x[x][0] =
-            lo ? *reinterpret_cast<const v4i*>(xrow[x] + k0) : zero;
-        t.x[x][1] =
-            hi ? *reinterpret_cast<const v4i*>(xrow[x] + k0 + 64) : zero;
-        if constexpr (G == 128)
-          t.sx[x] = sxrow[x][step];
-        else
-          t.sx[x] = k0 + 32 * g < H ? sxrow[x][step * 4 + g] : 127;
-      }
-    };
-    auto multiply = [&](const SmallStep<MT>& t) {
-#pragma unroll
-      for (int x = 0; x < MT; ++x)
-#pragma unroll
-        for (int f = 0; f < 4; ++f)
-          acc[f][x] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-              join(t.w[f][0], t.w[f][1]), join(t.x[x][0], t.x[x][1]),
-              acc[f][x], 0, 0, 0, t.sw[f], 0, t.sx[x]);
-    };
-    if (ks < nsteps) {
-      SmallStep<MT> s0, s1;
-      load(s0, ks);
-      for (int step = ks; step < nsteps; step += 2 * KS) {
-        if (step + KS < nsteps) load(s1, step + KS);
-        multiply(s0);
-        if (step + KS >= nsteps) break;
-        if (step + 2 * KS < nsteps) load(s0, step + 2 * KS);
-        multiply(s1);
-      }
-    }
-
-    // join the K parts: part[ks][token][channel]
-#pragma unroll
-    for (int x = 0; x < MT; ++x)
-#pragma unroll
-      for (int f = 0; f < 4; ++f)
-        *reinterpret_cast<v4f*>(
-            part + ((int64_t)(ks * 16 * MT + x * 16 + r16)) * LDT + ng * 64 +
-            f * 16 + 4 * g) = acc[f][x];
-    __syncthreads();
-    const int lanes = nbo / 8;  // lanes per token
-    for (int i = threadIdx.x; i < 16 * MT * lanes; i += 64 * NG * KS) {
-      const int tok = i / lanes;
-      const int c = i % lanes * 8;
-      float v[8];
-      auto sum = [&](int col, float (&o)[8]) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = 0.0f;
-#pragma unroll
-        for (int p = 0; p < KS; ++p) {
-          const float* src = part + (int64_t)(p * 16 * MT + tok) * LDT + col;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) o[j] += src[j];
-        }
-      };
-      const int col = n0 + c;
-      const bool in = col < a.NO;
-      sum(c, v);
-      if (a.bias != nullptr)
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          v[j] += a.bias[(int64_t)e * a.N + min(col + j, a.NO - 1)];
-      if (gated) {
-        float u[8];
-        sum(nbo + c, u);
-        if (a.bias != nullptr)
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            u[j] += a.bias[(int64_t)e * a.N + a.NO + min(col + j, a.NO - 1)];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = silu(v[j]) * u[j];
-      } else if (a.act == kActSilu) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = silu(v[j]);
-      }
-      const bool live = in && base + tok < er.count;
-      const int64_t row = er.first + min(base + tok, er.count - 1);
-      u32x4 res{0, 0, 0, 0};
-      if constexpr (OUT == kOutBf16) res = load_residual(a, row, col);
-      store_channels<OUT>(a, row, col, live, v, res);
-    }
-    __syncthreads();
-  }
-}
-
-// ------------------------------------------------------------ many rows
-//
-// A block of four wavefronts, one per SIMD, owns TM = 64 XF token rows of one
-// expert by 256 weight rows; each wavefront multiplies 32 XF tokens by 128
-// weight rows in 32x32x64 steps (64 XF accumulators per lane).  K goes by in
-// steps of 128 channels, held in LDS twice: while one step is multiplied, the
-// next is on its way from memory straight into LDS.
-//
-// LDS rows are 128 bytes; 16-byte chunk c of row r sits at chunk
-// c ^ ((r >> 1) & 7): 16 neighbouring rows of a fragment read then touch all
-// 64 banks once.  The
-// copy into LDS is linear, hence the chunk order is turned on its global side.
-//
-// A step is multiplied in two halves, A with the first half of the wavefront's
-// token fragments, B with the second.  B's token fragments are read from LDS
-// during A; the next step's weight fragments and first token fragments during
-// B, each weight fragment into the registers that its last MFMA has just left.
-// So most of a step's buffer is free when A begins and the rest when B does,
-// and the copies of the step after the next are dealt out evenly over the
-// whole step, one or two steps before they are waited for.  Copied in one half
-// only, they ask for 64 bytes a cycle, all that a CU's L1 can bring.
-//
-// A gated tile takes 128 gate rows and the 128 factor rows of the same
-// outputs; a wavefront holds both for 64 outputs.
+// ------------------------------------------------------------ copies to LDS
 
 __device__ __forceinline__ v4i buffer_of(const void* base, uint32_t bytes) {
   const uint64_t p = reinterpret_cast<uint64_t>(base);
@@ -247,15 +49,280 @@ __device__ __forceinline__ void copy_to_lds(const v4i& buf, uint32_t lds,
       : "s"(lds), "v"(voff), "s"(buf), "s"(soff));
 }
 
-// All but the last VM loads and copies and the last LGKM LDS reads issued so
-// far have landed, in this wavefront and, after the barrier, in every
-// wavefront of the block.
+// Waits until all but the last VM loads and copies and the last LGKM LDS reads
+// that this wavefront has issued are done.
 template <int VM, int LGKM>
-__device__ __forceinline__ void landed_barrier() {
+__device__ __forceinline__ void wait_for() {
+  asm volatile("" ::: "memory");
   __builtin_amdgcn_s_waitcnt((VM & 15) | ((VM >> 4) << 14) | 0x70 |
                              (LGKM << 8));
+  asm volatile("" ::: "memory");
+}
+
+// The same for the whole block.
+template <int VM, int LGKM>
+__device__ __forceinline__ void landed_barrier() {
+  wait_for<VM, LGKM>();
   asm volatile("s_barrier" ::: "memory");
 }
+
+constexpr int kMaxSteps = MXQ_MAX_HIDDEN / 128;
+
+// 16-byte chunk c of an LDS row of 128 bytes sits at place c ^ ((row >> 1) & 7):
+// 16 neighbouring rows of a fragment read then touch all 64 banks once.  A
+// copy fills places in order, so the order is turned on its global side.
+__device__ __forceinline__ int place(int c, int row) {
+  return c ^ ((row >> 1) & 7);
+}
+
+__device__ __forceinline__ v8i join(const v4i& a, const v4i& b) {
+  return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
+
+// ------------------------------------------------------------ few rows
+//
+// With few rows an expert's weights are read once for all of them (16 at a
+// time), and the kernel is bound by that stream.  A block of four wavefronts
+// owns 64 NG weight rows of one expert and all rows of that expert; its wavefronts take
+// 64 weight rows each and, where NG < 4, split the K axis in 4 / NG
+// interleaved parts (neighbouring 128-byte lines are in flight at once),
+// joined in LDS at the end.
+//
+// Each wavefront keeps a ring of three steps of 128 channels of its own in
+// LDS, filled by copies that bring whole lines and need no registers: 20 KB
+// per wavefront are on their way while a step is multiplied, and no barrier
+// orders them.  (Loaded into registers, where a lane's 16 bytes make half
+// lines, one token through 8 of 32 experts of 4096 x 7168 took 64 us; 44.5 us
+// this way, 5.3 TB/s, the rate of a large copy.)  The weight rows are the MFMA's A operand, the token
+// rows its B operand: a lane ends up with four neighbouring output channels
+// of one token.
+//
+// A 16x16x128 step: lane l = 16 g + r holds channels 16 g + [0, 16) and
+// 64 + 16 g + [0, 16) of row r; the scale of 32-channel block g of row r
+// comes from lane l.
+constexpr int kRing = 3;                       // steps held per wavefront
+constexpr int kSmallStep = (64 + 16) * 128;    // bytes of one
+constexpr int kRingBytes = 4 * kRing * kSmallStep;
+
+inline int small_scale_ld(int groups) { return (groups + 3) / 4 * 4 + 4; }
+
+template <int G, int NG, int OUT>
+__global__ __launch_bounds__(256, 1) void matmul_small_kernel(
+    MatmulArgs a, int32_t blocks_n, int32_t ld_xs) {
+  constexpr int KS = 4 / NG;
+  constexpr int NB = 64 * NG;
+  constexpr int LDT = NB + 4;  // floats per staged token
+  constexpr int kCopies = 10;  // of a step: 64 weight rows, 16 token rows
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  const int e = blockIdx.x / blocks_n;
+  const ExpertRows er = expert_rows(a, e);
+  if (er.count == 0) return;
+  const bool gated = a.act == kActSiluMul;
+  const int nbo = gated ? NB / 2 : NB;
+  const int n0 = (int)(blockIdx.x % blocks_n) * nbo;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int ng = wave / KS, ks = wave % KS;
+  const int r16 = lane & 15, g = lane >> 4;
+  const int H = a.H;
+  const int nsteps = (H + 127) / 128;
+  const int mine = (nsteps - ks + KS - 1) / KS;  // steps of this wavefront
+  const int nws = a.nbk, nwb = (a.N + 127) / 128;
+  const int nxs = H / G;
+  uint8_t* ring = lds + wave * kRing * kSmallStep;
+  uint8_t* xscale = lds + kRingBytes;
+  uint8_t* wscale = xscale + 16 * ld_xs;
+  const uint32_t ring0 = (uint32_t)(uintptr_t)(
+      __attribute__((address_space(3))) uint8_t*)ring;
+
+  // weight row (within the expert's matrix) of local row lr of the block
+  auto weight_row = [&](int lr) {
+    if (!gated) return min(n0 + lr, a.N - 1);
+    return lr < nbo ? min(n0 + lr, a.NO - 1)
+                    : a.NO + min(n0 + lr - nbo, a.NO - 1);
+  };
+  // copy i brings rows 8 i + (l >> 3); odd copies' chunks differ by 4
+  const int chunk0 = place(lane & 7, lane >> 3);
+  uint32_t woff[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    woff[i] = (uint32_t)((weight_row(ng * 64 + 8 * i + (lane >> 3)) - n0) * H);
+  const v4i wbuf = buffer_of(a.w + ((int64_t)e * a.N + n0) * H,
+                             (uint32_t)((a.N - n0) * H));
+  // scale bytes of the (at most three) 128-row blocks of the weight rows
+  const int up_block = (a.NO + n0) / 128;
+  for (int i = threadIdx.x; i < 3 * nws; i += 256) {
+    const int b = i / nws;
+    const int block = b == 0 ? n0 / 128
+                      : gated ? up_block + b - 1 : n0 / 128 + b;
+    if (block < nwb)
+      wscale[b * kMaxSteps + i % nws] =
+          a.ws[((int64_t)e * nwb + block) * nws + i % nws];
+  }
+  int wsoff[4];
+#pragma unroll
+  for (int f = 0; f < 4; ++f) {
+    const int lr = ng * 64 + f * 16 + r16;
+    const int block = weight_row(lr) / 128;
+    wsoff[f] = (gated && lr >= nbo ? block - up_block + 1 : block - n0 / 128) *
+               kMaxSteps;
+  }
+
+  for (int base = 0; base < er.count; base += 16) {
+    const int rows = min(er.count - base, 16);
+    const int64_t row0 = er.first + base;
+    const v4i xbuf = buffer_of(a.q + row0 * a.ld_q,
+                               (uint32_t)((rows - 1) * a.ld_q + H));
+    uint32_t xoff[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      xoff[i] = (uint32_t)(min(8 * i + (lane >> 3), rows - 1) * (int)a.ld_q);
+    // In a last step that ends inside the 128 channels, chunks past H repeat
+    // chunk 0 of the step: in bounds, and cleared when they are read.
+    auto copy_step = [&](int i) {
+      const int k0 = (ks + i * KS) * 128;
+      const uint32_t at = ring0 + (uint32_t)(i % kRing) * kSmallStep;
+      const int c1 = chunk0 ^ 4;
+      const uint32_t o0 = k0 + 16 * chunk0 < H ? 16 * chunk0 : 0;
+      const uint32_t o1 = k0 + 16 * c1 < H ? 16 * c1 : 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        copy_to_lds(wbuf, at + j * 1024, woff[j] + (j & 1 ? o1 : o0), k0);
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        copy_to_lds(xbuf, at + 8192 + j * 1024, xoff[j] + (j & 1 ? o1 : o0),
+                    k0);
+    };
+    for (int i = threadIdx.x; i < 16 * nxs; i += 256) {
+      const int r = i / nxs;
+      xscale[r * ld_xs + i % nxs] =
+          a.s[(row0 + min(r, rows - 1)) * a.ld_s + i % nxs];
+    }
+#pragma unroll
+    for (int i = 0; i < kRing; ++i)
+      if (i < mine) copy_step(i);
+    landed_barrier<63, 0>();  // the scale bytes are down
+
+    v4f acc[4];
+#pragma unroll
+    for (int f = 0; f < 4; ++f) acc[f] = v4f{0, 0, 0, 0};
+
+    for (int i = 0; i < mine; ++i) {
+      // this step's copies have landed; later ones may be on their way
+      if (i + kRing <= mine)
+        wait_for<(kRing - 1) * kCopies, 15>();
+      else
+        wait_for<0, 15>();
+      const int step = ks + i * KS;
+      const uint8_t* at = ring + i % kRing * kSmallStep;
+      v4i w[4][2], x[2];
+      uint32_t sw[4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int c = 4 * h + g;
+#pragma unroll
+        for (int f = 0; f < 4; ++f)
+          w[f][h] = *reinterpret_cast<const v4i*>(
+              at + (f * 16 + r16) * 128 + place(c, r16) * 16);
+        x[h] = *reinterpret_cast<const v4i*>(at + 8192 + r16 * 128 +
+                                             place(c, r16) * 16);
+      }
+#pragma unroll
+      for (int f = 0; f < 4; ++f) sw[f] = wscale[wsoff[f] + step];
+      // a block past H has no scale: any finite one will do
+      const uint32_t sx =
+          xscale[r16 * ld_xs +
+                 (G == 128 ? step : min(4 * step + g, nxs - 1))];
+      wait_for<63, 0>();  // read: the ring's place may be filled again
+      if (i + kRing < mine) copy_step(i + kRing);
+      if (step * 128 + 128 > H) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (step * 128 + 64 * h + 16 * g < H) continue;
+#pragma unroll
+          for (int f = 0; f < 4; ++f) w[f][h] = v4i{0, 0, 0, 0};
+          x[h] = v4i{0, 0, 0, 0};
+        }
+      }
+#pragma unroll
+      for (int f = 0; f < 4; ++f)
+        acc[f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+            join(w[f][0], w[f][1]), join(x[0], x[1]), acc[f], 0, 0, 0,
+            (int)sw[f], 0, (int)sx);
+    }
+
+    // join the K parts: part[ks][token][channel], over the rings
+    __syncthreads();
+    float* part = reinterpret_cast<float*>(lds);
+#pragma unroll
+    for (int f = 0; f < 4; ++f)
+      *reinterpret_cast<v4f*>(part + (ks * 16 + r16) * LDT + ng * 64 +
+                              f * 16 + 4 * g) = acc[f];
+    __syncthreads();
+    const int lanes = nbo / 8;  // lanes per token
+    for (int i = threadIdx.x; i < 16 * lanes; i += 256) {
+      const int tok = i / lanes;
+      const int c = i % lanes * 8;
+      float v[8];
+      auto sum = [&](int col, float (&o)[8]) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = 0.0f;
+#pragma unroll
+        for (int p = 0; p < KS; ++p) {
+          const float* src = part + (p * 16 + tok) * LDT + col;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) o[j] += src[j];
+        }
+      };
+      const int col = n0 + c;
+      const bool in = col < a.NO;
+      sum(c, v);
+      if (a.bias != nullptr)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          v[j] += a.bias[(int64_t)e * a.N + min(col + j, a.NO - 1)];
+      if (gated) {
+        float u[8];
+        sum(nbo + c, u);
+        if (a.bias != nullptr)
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            u[j] += a.bias[(int64_t)e * a.N + a.NO + min(col + j, a.NO - 1)];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = silu(v[j]) * u[j];
+      } else if (a.act == kActSilu) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = silu(v[j]);
+      }
+      const bool live = in && tok < rows;
+      const int64_t row = row0 + min(tok, rows - 1);
+      u32x4 res{0, 0, 0, 0};
+      if constexpr (OUT == kOutBf16) res = load_residual(a, row, col);
+      store_channels<OUT>(a, row, col, live, v, res);
+    }
+    __syncthreads();
+  }
+}
+
+// ------------------------------------------------------------ many rows
+//
+// A block of four wavefronts, one per SIMD, owns TM = 64 XF token rows of one
+// expert by 256 weight rows; each wavefront multiplies 32 XF tokens by 128
+// weight rows in 32x32x64 steps (64 XF accumulators per lane).  K goes by in
+// steps of 128 channels, held in LDS twice: while one step is multiplied, the
+// next is on its way from memory straight into LDS.
+//
+// A step is multiplied in two halves, A with the first half of the wavefront's
+// token fragments, B with the second.  B's token fragments are read from LDS
+// during A; the next step's weight fragments and first token fragments during
+// B, each weight fragment into the registers that its last MFMA has just left.
+// So most of a step's buffer is free when A begins and the rest when B does,
+// and the copies of the step after the next are dealt out evenly over the
+// whole step, one or two steps before they are waited for.  Copied in one half
+// only, they ask for 64 bytes a cycle, all that a CU's L1 can bring.
+//
+// A gated tile takes 128 gate rows and the 128 factor rows of the same
+// outputs; a wavefront holds both for 64 outputs.
 
 // The tile a block works on.  Experts' tiles are numbered expert by expert,
 // from device data; every wavefront finds its block's by itself.  Runs of
@@ -310,7 +377,6 @@ __device__ __forceinline__ bool find_tile(const MatmulArgs& a, int tiles_n,
 
 constexpr int kStageLd = 260;  // floats per staged token (256 weight rows + pad)
 constexpr int kScaleLd = 36;   // bytes per row of a scale chunk (32 + pad)
-constexpr int kMaxSteps = MXQ_MAX_HIDDEN / 128;
 
 template <int XF>
 constexpr int tile_lds_bytes() {
@@ -351,7 +417,7 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs a,
   // Copies: 8 rows (1 KB) each, lane l fills place l & 7 of row l >> 3.  The
   // 64 rows of fragment f of both wavefront columns are two copies per
   // wavefront, and so are those of fragment x of both wavefront rows.
-  const int chunk = (lane & 7) ^ ((4 * wave + (lane >> 4)) & 7);
+  const int chunk = place(lane & 7, wave * 8 + (lane >> 3));
   const int crow = wave * 8 + (lane >> 3);
   uint32_t xoff[XF][2], woff[4][2];
   const int64_t wfirst = n0;
@@ -499,7 +565,7 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs a,
     const int c = p * 2 + g;
     v4i v = *reinterpret_cast<const v4i*>(
         lds + (k & 1) * kStage + first_row * 128 + r32 * 128 +
-        ((c ^ ((r32 >> 1) & 7)) * 16));
+        place(c, r32) * 16);
     if constexpr (decltype(last)::value)
       if (k * 128 + 16 * c >= H) v = v4i{0, 0, 0, 0};
     return v;
@@ -713,21 +779,24 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs a,
 
 // ------------------------------------------------------------ entry points
 
-template <int G, int MT, int NG, int KS, int OUT>
+template <int G, int NG, int OUT>
 mxq_status launch_small(const MatmulArgs& a, hipStream_t s) {
   const int nbo = a.act == kActSiluMul ? 32 * NG : 64 * NG;
   const int64_t bn = ceil_div(a.NO, nbo);
   if (bn * a.E > INT32_MAX) return MXQ_ERR_UNSUPPORTED;
-  const size_t lds = (size_t)KS * 16 * MT * (64 * NG + 4) * sizeof(float);
-  auto* k = &matmul_small_kernel<G, MT, NG, KS, OUT>;
-  if (lds > 65536 &&
-      hipFuncSetAttribute(reinterpret_cast<const void*>(k),
+  const int ld_xs = small_scale_ld(a.H / G);
+  const int lds = kRingBytes + 16 * ld_xs + 3 * kMaxSteps;
+  static_assert(kRingBytes >= 4 * 16 * (64 + 4) * 4 &&
+                    kRingBytes >= 16 * (256 + 4) * 4,
+                "the joined K parts fit the rings");
+  auto* k = &matmul_small_kernel<G, NG, OUT>;
+  if (hipFuncSetAttribute(reinterpret_cast<const void*>(k),
                           hipFuncAttributeMaxDynamicSharedMemorySize,
-                          (int)lds) != hipSuccess) {
+                          lds) != hipSuccess) {
     (void)hipGetLastError();
     return MXQ_ERR_HIP;
   }
-  k<<<(unsigned)(bn * a.E), 64 * NG * KS, lds, s>>>(a, (int32_t)bn);
+  k<<<(unsigned)(bn * a.E), 256, lds, s>>>(a, (int32_t)bn, ld_xs);
   return launch_status();
 }
 
@@ -751,18 +820,27 @@ mxq_status launch_tile(const MatmulArgs& a, hipStream_t s) {
   return launch_status();
 }
 
+// The kernel for `expected` rows in a busy expert.  Measured with top-8
+// routings over 32 experts whose fullest holds 2.6 times the mean, gate/up
+// (4096 x 7168, G = 128) and down (7168 x 2048, G = 32), us:
+//   mean rows        4         16        64        128       256       512
+//   few rows     152, 90   274, 122  765, 326
+//   128-row tile 161, 106  178, 112  231, 124  236, 158  386, 227  607, 394
+//   256-row tile 186, 126  201, 131  206, 144  285, 159  313, 209  507, 323
+// The weights alone take 177 and 89 us at 5.3 TB/s; gate/up with few rows
+// leaves experts without a row out.
 template <int G, int OUT>
 mxq_status launch(const MatmulArgs& a, int64_t expected, hipStream_t s) {
-  if (expected > 128) return launch_tile<G, 4, OUT>(a, s);
-  if (expected > 64) return launch_tile<G, 2, OUT>(a, s);
-  if constexpr (OUT == kOutG128) {
-    // a group of 128 outputs stays in one block: 128 weight rows, or 256
-    if (a.act == kActSiluMul) return launch_small<G, 1, 4, 2, OUT>(a, s);
-    return launch_small<G, 1, 2, 4, OUT>(a, s);
-  } else {
-    if (expected <= 16) return launch_small<G, 1, 1, 4, OUT>(a, s);
-    return launch_small<G, 4, 1, 4, OUT>(a, s);
-  }
+  if (expected > 160) return launch_tile<G, 4, OUT>(a, s);
+  if (expected > 12) return launch_tile<G, 2, OUT>(a, s);
+  // 256 weight rows per block once that makes a block for every CU: longer
+  // runs, so a block's start costs less (down, mean 8: 86 against 102 us);
+  // else 64, and the K axis is split.  A group of 128 outputs stays in one
+  // block: 128 weight rows at least, 256 when gated.
+  if (ceil_div(a.N, 256) * a.E >= 256 ||
+      (OUT == kOutG128 && a.act == kActSiluMul))
+    return launch_small<G, 4, OUT>(a, s);
+  return launch_small<G, OUT == kOutG128 ? 2 : 1, OUT>(a, s);
 }
 
 inline bool aligned8(const void* p) {
