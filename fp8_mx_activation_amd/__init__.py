@@ -158,16 +158,19 @@ def _stream(t: torch.Tensor) -> int:
     return torch.cuda.current_stream(t.device).cuda_stream
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _call(fn: str, t: torch.Tensor, *args) -> None:
     """Run entry point ``fn`` on the current stream of t's device, which need
     not be the current one; raises on an error status."""
-    f = getattr(lib(), fn)
-    dev = t.device.index
+    f = getattr(_lib or lib(), fn)
+    dev = t.get_device()
     if dev == torch.cuda.current_device():
-        st = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+        st = f(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            st = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+            st = f(*args, _raw_stream(dev))
     if st != MXQ_OK:
         raise MxqError(fn, st)
 
@@ -183,6 +186,9 @@ def _dev(t: torch.Tensor | None, name: str,
     """Every tensor handed to the library must live on the GPU (a host
     pointer would fault the kernel), on the device of the call's inputs."""
     if t is None:
+        return
+    d = t.get_device()
+    if d >= 0 and (like is None or d == like.get_device()):
         return
     if not t.is_cuda:
         raise ValueError("%s must be a GPU tensor" % name)
@@ -339,15 +345,16 @@ def _logits(logits: torch.Tensor, name: str = "logits") -> int:
     return _rows(logits, name, tuple(OUT_DTYPES))
 
 
-def _dense(t: torch.Tensor, name: str, dtype, shape, like: torch.Tensor):
-    """A contiguous tensor of exactly this dtype and shape, on the inputs'
-    device."""
-    _dev(t, name, like)
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or \
-            not t.is_contiguous():
+def _dense(t: torch.Tensor, name: str, dtype, shape: tuple,
+           like: torch.Tensor) -> int | None:
+    """Pointer of a contiguous tensor of exactly this dtype and shape, on the
+    inputs' device."""
+    if t.get_device() != like.get_device():
+        _dev(t, name, like)
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError("%s must be contiguous %s %s"
                          % (name, dtype, list(shape)))
-    return t
+    return t.data_ptr() or None
 
 
 def moe_route(logits: torch.Tensor, K: int, scoring: str = "softmax",
@@ -363,20 +370,18 @@ def moe_route(logits: torch.Tensor, K: int, scoring: str = "softmax",
     the weight 0."""
     ld = _logits(logits)
     T, E = logits.shape
-    if bias is not None:
-        _dense(bias, "bias", torch.float32, (E,), logits)
+    b = None if bias is None else _dense(bias, "bias", torch.float32, (E,),
+                                         logits)
     if ids is None:
         ids = torch.empty((T, K), dtype=torch.int32, device=logits.device)
-    else:
-        _dense(ids, "ids", torch.int32, (T, K), logits)
     if weights is None:
         weights = torch.empty((T, K), dtype=torch.float32,
                               device=logits.device)
-    else:
-        _dense(weights, "weights", torch.float32, (T, K), logits)
-    _call("moe_route", logits, _ptr(logits), OUT_DTYPES[logits.dtype], ld, T,
-          E, K, SCORE_FNS[scoring], _ptr(bias), num_groups, top_groups,
-          int(renormalize), weight_scale, _ptr(ids), _ptr(weights))
+    _call("moe_route", logits, logits.data_ptr(), OUT_DTYPES[logits.dtype],
+          ld, T, E, K, SCORE_FNS[scoring], b, num_groups, top_groups,
+          int(renormalize), weight_scale,
+          _dense(ids, "ids", torch.int32, (T, K), logits),
+          _dense(weights, "weights", torch.float32, (T, K), logits))
     return ids, weights
 
 
@@ -390,22 +395,20 @@ def moe_route_backward(grad_weights: torch.Tensor, logits: torch.Tensor,
     dtype."""
     ld = _logits(logits)
     T, E = logits.shape
-    _dev(topk_ids, "topk_ids", logits)
     if topk_ids.dim() != 2:
         raise ValueError("topk_ids must be int32 [T, K]")
     K = topk_ids.shape[1]
-    _dense(topk_ids, "topk_ids", torch.int32, (T, K), logits)
-    _dense(grad_weights, "grad_weights", torch.float32, (T, K), logits)
+    ids = _dense(topk_ids, "topk_ids", torch.int32, (T, K), logits)
+    g = _dense(grad_weights, "grad_weights", torch.float32, (T, K), logits)
     if grad_logits is None:
         grad_logits = torch.empty((T, E), dtype=logits.dtype,
                                   device=logits.device)
     _dev(grad_logits, "grad_logits", logits)
     ld_g = _rows(grad_logits, "grad_logits", (logits.dtype,))
     _at_least(grad_logits, "grad_logits", T, E)
-    _call("moe_route_backward", logits, _ptr(grad_weights), _ptr(logits),
-          OUT_DTYPES[logits.dtype], ld, _ptr(topk_ids), T, E, K,
-          SCORE_FNS[scoring], int(renormalize), weight_scale,
-          _ptr(grad_logits), ld_g)
+    _call("moe_route_backward", logits, g, logits.data_ptr(),
+          OUT_DTYPES[logits.dtype], ld, ids, T, E, K, SCORE_FNS[scoring],
+          int(renormalize), weight_scale, grad_logits.data_ptr(), ld_g)
     return grad_logits
 
 
@@ -864,16 +867,15 @@ def _matmul_inputs(q, scales, w, w_scales, expert_offsets, counts, fmt, act,
             not w_scales.is_contiguous():
         raise ValueError("w_scales must be contiguous uint8 %s"
                          % (list(blocks),))
-    _dense(expert_offsets, "expert_offsets", torch.int32, (E + 1,), q)
-    _dense(counts, "counts", torch.int32, (E,), q)
-    if bias is not None:
-        _dense(bias, "bias", torch.float32, (E, N), q)
+    off = _dense(expert_offsets, "expert_offsets", torch.int32, (E + 1,), q)
+    cnt = _dense(counts, "counts", torch.int32, (E,), q)
+    b = None if bias is None else _dense(bias, "bias", torch.float32, (E, N),
+                                         q)
     a = ACTIVATIONS[act]
     if expected_m is None:
         expected_m = -(-rows // E) if E else 0
     args = (_ptr(q), ld_q, _ptr(scales), ld_s, rows, code, _ptr(w),
-            _ptr(w_scales), E, N, H, _ptr(expert_offsets), _ptr(counts),
-            _ptr(bias), a)
+            _ptr(w_scales), E, N, H, off, cnt, b, a)
     return args, rows, N // 2 if act == "silu_mul" else N, expected_m
 
 
@@ -1016,7 +1018,7 @@ def moe_combine_backward(grad_out: torch.Tensor, y: torch.Tensor,
     num_rows = y.shape[0]
     if y.shape[1] != H:
         raise ValueError("y must be [num_rows, %d]" % H)
-    _dense(topk_weights, "topk_weights", torch.float32, (T, K), grad_out)
+    w = _dense(topk_weights, "topk_weights", torch.float32, (T, K), grad_out)
     if grad_y is None:
         grad_y = torch.empty((num_rows, H), dtype=torch.bfloat16,
                              device=y.device)
@@ -1026,13 +1028,11 @@ def moe_combine_backward(grad_out: torch.Tensor, y: torch.Tensor,
     if grad_weights is None:
         grad_weights = torch.empty((T, K), dtype=torch.float32,
                                    device=y.device)
-    else:
-        _dense(grad_weights, "grad_weights", torch.float32, (T, K), grad_out)
+    gw = _dense(grad_weights, "grad_weights", torch.float32, (T, K), grad_out)
     if T and K:
         _call("moe_combine_backward", grad_out, _ptr(grad_out),
               OUT_DTYPES[grad_out.dtype], ld_g, _ptr(y), ld_y, num_rows,
-              _ptr(src2dst), _ptr(topk_weights), T, K, H, _ptr(grad_y), ld_gy,
-              _ptr(grad_weights))
+              _ptr(src2dst), w, T, K, H, _ptr(grad_y), ld_gy, gw)
     return grad_y, grad_weights
 
 
