@@ -827,12 +827,22 @@ mxq_status launch_tile(const MatmulArgs& a, hipStream_t s) {
 //   few rows     152, 90   274, 122  765, 326
 //   128-row tile 161, 106  178, 112  231, 124  236, 158  386, 227  607, 394
 //   256-row tile 186, 126  201, 131  206, 144  285, 159  313, 209  507, 323
-// The weights alone take 177 and 89 us at 5.3 TB/s; gate/up with few rows
-// leaves experts without a row out.
+// (the weights alone take 177 and 89 us at 5.3 TB/s; gate/up with few rows
+// leaves experts without a row out).  A 128-row tile takes 0.6 of a 256-row
+// one's time, both one to a CU, so the smaller one is taken where that many
+// rounds of the 256 CUs are over sooner: 375 mean rows of 24 experts of 1432 x
+// 1376 take 43 against 58 us in two rounds either way, 750 take 80 against 63.
 template <int G, int OUT>
 mxq_status launch(const MatmulArgs& a, int64_t expected, hipStream_t s) {
-  if (expected > 160) return launch_tile<G, 4, OUT>(a, s);
-  if (expected > 12) return launch_tile<G, 2, OUT>(a, s);
+  constexpr int64_t kCus = 256;
+  if (expected > 12) {
+    const int64_t columns =
+        a.E * ceil_div(a.NO, a.act == kActSiluMul ? 128 : 256);
+    const int64_t rounds4 = ceil_div(columns * ceil_div(expected, 256), kCus);
+    const int64_t rounds2 = ceil_div(columns * ceil_div(expected, 128), kCus);
+    return rounds2 * 3 <= rounds4 * 5 ? launch_tile<G, 2, OUT>(a, s)
+                                      : launch_tile<G, 4, OUT>(a, s);
+  }
   // 256 weight rows per block once that makes a block for every CU: longer
   // runs, so a block's start costs less (down, mean 8: 86 against 102 us);
   // else 64, and the K axis is split.  A group of 128 outputs stays in one
@@ -858,6 +868,7 @@ mxq_status checked(const void* q, int64_t ld_q, const uint8_t* scales,
                    void* stream) {
   const int G = group_of(fmt);
   if (G == 0) return MXQ_ERR_UNSUPPORTED;
+  if (expected_m > INT32_MAX) expected_m = INT32_MAX;
   if (act != MXQ_ACT_NONE && act != MXQ_ACT_SILU && act != MXQ_ACT_SILU_MUL)
     return MXQ_ERR_UNSUPPORTED;
   if (E < 1 || E > MXQ_MAX_LOCAL_EXPERTS || N < 1 || H < 1 || H % G != 0 ||
