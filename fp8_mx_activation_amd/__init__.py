@@ -158,6 +158,9 @@ def _stream(t: torch.Tensor) -> int:
     return torch.cuda.current_stream(t.device).cuda_stream
 
 
+# the current device and the stream handle of a device, without building
+# Python objects for them (a microsecond of a call's six)
+_device = torch._C._cuda_getDevice
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
@@ -166,7 +169,7 @@ def _call(fn: str, t: torch.Tensor, *args) -> None:
     not be the current one; raises on an error status."""
     f = getattr(_lib or lib(), fn)
     dev = t.get_device()
-    if dev == torch.cuda.current_device():
+    if dev == _device():
         st = f(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
@@ -219,9 +222,11 @@ def _rows(t: torch.Tensor, name: str, dtypes) -> int:
         raise TypeError("%s: dtype %s not in %s" % (name, t.dtype, dtypes))
     if t.dim() != 2:
         raise ValueError("%s must be 2-D" % name)
-    if t.shape[1] > 1 and t.stride(1) != 1:
+    rows, cols = t.shape
+    ld, step = t.stride()
+    if cols > 1 and step != 1:
         raise ValueError("%s must have unit column stride" % name)
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], t.stride(0))
+    return ld if rows > 1 else max(cols, ld)
 
 
 _FP8 = (torch.uint8, torch.float8_e4m3fn)
@@ -342,7 +347,7 @@ SCORE_FNS = {"softmax": 0, "sigmoid": 1}
 
 def _logits(logits: torch.Tensor, name: str = "logits") -> int:
     _dev(logits, name)
-    return _rows(logits, name, tuple(OUT_DTYPES))
+    return _rows(logits, name, OUT_DTYPES)
 
 
 def _dense(t: torch.Tensor, name: str, dtype, shape: tuple,
@@ -985,7 +990,7 @@ def moe_scatter_rows_backward(grad_rows: torch.Tensor, src2dst: torch.Tensor,
     sum of its rows of ``grad_rows [num_rows, H]`` (bf16 or float32), in the
     rows' dtype unless ``out_dtype`` or ``out`` says otherwise."""
     _dev(grad_rows, "grad_rows")
-    ld = _rows(grad_rows, "grad_rows", tuple(OUT_DTYPES))
+    ld = _rows(grad_rows, "grad_rows", OUT_DTYPES)
     num_rows, H = grad_rows.shape
     K = _src2dst(src2dst, grad_rows, None)
     T = src2dst.shape[0]
@@ -993,7 +998,7 @@ def moe_scatter_rows_backward(grad_rows: torch.Tensor, src2dst: torch.Tensor,
         out = torch.empty((T, H), dtype=out_dtype or grad_rows.dtype,
                           device=grad_rows.device)
     _dev(out, "out", grad_rows)
-    ld_o = _rows(out, "out", tuple(OUT_DTYPES))
+    ld_o = _rows(out, "out", OUT_DTYPES)
     _at_least(out, "out", T, H)
     _call("moe_scatter_rows_backward", grad_rows, _ptr(grad_rows),
           OUT_DTYPES[grad_rows.dtype], ld, num_rows, _ptr(src2dst), T, K, H,
@@ -1010,7 +1015,7 @@ def moe_combine_backward(grad_out: torch.Tensor, y: torch.Tensor,
     float32 [T, K])``.  Rows of ``grad_y`` that are no destination keep the
     contents of a given ``grad_y``."""
     _dev(grad_out, "grad_out")
-    ld_g = _rows(grad_out, "grad_out", tuple(OUT_DTYPES))
+    ld_g = _rows(grad_out, "grad_out", OUT_DTYPES)
     T, H = grad_out.shape
     K = _src2dst(src2dst, grad_out, T)
     _dev(y, "y", grad_out)

@@ -344,6 +344,9 @@ __device__ __forceinline__ bool find_tile(const MatmulArgs& a, int tiles_n,
   for (int i = 0; i < per; ++i) {
     const int e = lane * per + i;
     if (e < a.E) mine += (expert_rows(a, e).count + TM - 1) / TM;
+    // regions that do not overlap hold 2^24 tiles at most; more, of offsets
+    // that no layout makes, must not overflow the sums
+    mine = min(mine, 1 << 24);
   }
   int upto = mine;  // row tiles of lanes up to this one
 #pragma unroll
