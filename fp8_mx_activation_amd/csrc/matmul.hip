@@ -83,19 +83,19 @@ __device__ __forceinline__ v8i join(const v4i& a, const v4i& b) {
 //
 // With few rows an expert's weights are read once for all of them (16 at a
 // time), and the kernel is bound by that stream.  A block of four wavefronts
-// owns 64 NG weight rows of one expert and all rows of that expert; its wavefronts take
-// 64 weight rows each and, where NG < 4, split the K axis in 4 / NG
-// interleaved parts (neighbouring 128-byte lines are in flight at once),
-// joined in LDS at the end.
+// owns 64 NG weight rows of one expert and all rows of that expert; its
+// wavefronts take 64 weight rows each and, where NG < 4, split the K axis in
+// 4 / NG interleaved parts (neighbouring 128-byte lines are in flight at
+// once), joined in LDS at the end.
 //
 // Each wavefront keeps a ring of three steps of 128 channels of its own in
 // LDS, filled by copies that bring whole lines and need no registers: 20 KB
 // per wavefront are on their way while a step is multiplied, and no barrier
 // orders them.  (Loaded into registers, where a lane's 16 bytes make half
 // lines, one token through 8 of 32 experts of 4096 x 7168 took 64 us; 44.5 us
-// this way, 5.3 TB/s, the rate of a large copy.)  The weight rows are the MFMA's A operand, the token
-// rows its B operand: a lane ends up with four neighbouring output channels
-// of one token.
+// this way, 5.3 TB/s, the rate of a large copy.)  The weight rows are the MFMA's A
+// operand, the token rows its B operand: a lane ends up with four neighbouring
+// output channels of one token.
 //
 // A 16x16x128 step: lane l = 16 g + r holds channels 16 g + [0, 16) and
 // 64 + 16 g + [0, 16) of row r; the scale of 32-channel block g of row r

@@ -22,7 +22,11 @@
 //
 // Bound: a row of E logits is 0.5-4 KB, so even 8192 tokens are one or two
 // microseconds of HBM time; the kernel is bound by the K dependent
-// reductions of one wavefront.
+// reductions of one wavefront.  Measured: one token of 256 experts in 8
+// groups, sigmoid with bias, top-8: 5.4 us (10.9 with 64-bit shuffles and the
+// groups joined one after another); 8192 tokens of 256 experts, softmax
+// top-8: 7.3-8.4 us (14.2 with 64-bit keys throughout); their gradient, 17 MB:
+// 6.3-7.2 us.  An empty kernel takes 2.1 us, a launch 4.2 us of host time.
 #include <type_traits>
 
 #include "mxq_device.hpp"
