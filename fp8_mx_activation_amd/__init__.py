@@ -1,5 +1,6 @@
 """MoE expert-dispatch preprocessing with fp8 e4m3 activations and
-power-of-two group scales, on MI355X (gfx950).
+power-of-two group scales, on MI355X (gfx950), with the router in front of
+it, the experts' products on its rows, and their gradients.
 
 Thin Python binding over ``libmxq.so`` (declared in ``include/mxq.h``).  The
 functions carry the C names; they check tensor dtypes, shapes and devices,
@@ -159,9 +160,10 @@ def _stream(t: torch.Tensor) -> int:
 
 
 # the current device and the stream handle of a device, without building
-# Python objects for them (a microsecond of a call's six)
-_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# Python objects for them (a microsecond of a call's six); a torch without
+# GPU support has neither, and no tensor that gets this far
+_device = getattr(torch._C, "_cuda_getDevice", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _call(fn: str, t: torch.Tensor, *args) -> None:

@@ -12,6 +12,8 @@
 // writes K.  All sums are in fp32, in a fixed order.  Measured at 8192 tokens,
 // top-8, hidden 7168, bf16: sort 176-180 us (5.9 TB/s, a large copy's rate),
 // combine 372-388 us (5.2-5.4 TB/s; its writes are half of the traffic).
+#include <algorithm>
+
 #include "mxq_device.hpp"
 #include "mxq_host.hpp"
 
@@ -95,12 +97,13 @@ __global__ __launch_bounds__(1024) void scatter_rows_backward_kernel(
     char* __restrict__ out, int64_t ld_out) {
   constexpr int kIn = F32_IN ? 4 : 2, kOut = F32_OUT ? 4 : 2;
   const int64_t t = blockIdx.x;
-  const int c_lo = (int)blockIdx.y * slice;
-  const int c_hi = min(H, c_lo + slice);
+  // unsigned: a slice's end and a block's stride past it stay below 2^32
+  const uint32_t c_lo = blockIdx.y * (uint32_t)slice;
+  const uint32_t c_hi = min((uint32_t)H, c_lo + (uint32_t)slice);
   const int lane = threadIdx.x & 63;
   const int32_t d_lane =
       K > 0 ? src2dst[t * K + min(lane, K - 1)] : -1;
-  for (int col = c_lo + (int)threadIdx.x * 8; col < c_hi;
+  for (uint32_t col = c_lo + threadIdx.x * 8; col < c_hi;
        col += blockDim.x * 8) {
     float acc[8];
 #pragma unroll
@@ -217,7 +220,8 @@ __global__ __launch_bounds__(kCombineBackThreads) void combine_backward_kernel(
 }
 
 // As in the combine: below this many tokens a row is dealt to blocks of
-// kBackSlice channels.
+// kBackSlice channels (more, where a grid's second dimension would pass
+// 65535).
 constexpr int64_t kBackSliceMaxTokens = 192;
 constexpr int32_t kBackSlice = 1024;
 
@@ -246,8 +250,10 @@ extern "C" mxq_status moe_scatter_rows_backward(
   if (!row_ok(grad_x, ld_x, H, on) || (K > 0 && src2dst == nullptr) ||
       (num_rows > 0 && !row_ok(grad_rows, ld_rows, H, in)))
     return MXQ_ERR_INVALID_ARGUMENT;
-  const int32_t slice =
-      T <= kBackSliceMaxTokens && H > kBackSlice ? kBackSlice : H;
+  int32_t slice = H;
+  if (T <= kBackSliceMaxTokens && H > kBackSlice)
+    slice = (int32_t)std::max<int64_t>(
+        kBackSlice, ceil_div(ceil_div(H, 65535), 8) * 8);
   const dim3 grid((unsigned)T, (unsigned)ceil_div(H, slice));
   const int threads = row_block_threads(slice, 8);
   hipStream_t s = as_stream(stream);

@@ -881,7 +881,9 @@ mxq_status checked(const void* q, int64_t ld_q, const uint8_t* scales,
   const int32_t NO = act == MXQ_ACT_SILU_MUL ? N / 2 : N;
   const int unit = OUT == kOutBf16 ? 4 : OUT == kOutG128 ? 128 : 32;
   if (NO % unit != 0) return MXQ_ERR_INVALID_ARGUMENT;
-  if (H > MXQ_MAX_HIDDEN || (int64_t)N * H > INT32_MAX)
+  // row counts are rounded up to whole tiles in 32 bits
+  if (H > MXQ_MAX_HIDDEN || (int64_t)N * H > INT32_MAX ||
+      num_rows > MXQ_MAX_MATMUL_ROWS)
     return MXQ_ERR_UNSUPPORTED;
   if (num_rows == 0) return MXQ_OK;
   if (q == nullptr || scales == nullptr || w == nullptr ||

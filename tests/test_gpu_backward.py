@@ -216,3 +216,33 @@ def test_refusals():
         mxq.moe_combine_backward(g, y, s, w, grad_y=y[:7])
     with pytest.raises(ValueError):
         mxq.moe_combine_backward(g, y, s, w.cpu())
+
+
+def test_rows_beyond_32_bit_offsets():
+    """Destinations past 2^32 bytes of the rows' start."""
+    T, K, H, rows = 40, 3, 8192, 300000
+    src = torch.arange(T * K, dtype=torch.int32).view(T, K)
+    far = (rows - T * K + src).to(DEV)
+    near = src.to(DEV)
+    y = randn(1, T * K, H).bfloat16().to(DEV)
+    big = torch.empty((rows, H), dtype=torch.bfloat16, device=DEV)
+    big[rows - T * K:] = y
+    g = randn(2, T, H).bfloat16().to(DEV)
+    w = randn(3, T, K).to(DEV)
+    say("rows beyond 32-bit offsets")
+    gy, gw = mxq.moe_combine_backward(g, y, near, w)
+    far_gy, far_gw = mxq.moe_combine_backward(g, big, far, w)
+    assert torch.equal(far_gw, gw)
+    assert torch.equal(far_gy[rows - T * K:], gy)
+    assert torch.equal(mxq.moe_scatter_rows_backward(big, far),
+                       mxq.moe_scatter_rows_backward(y, near))
+
+
+def test_sort_gradient_of_very_wide_rows():
+    """More channels than 65535 blocks of the usual size."""
+    H = 70000 * 1024 + 8
+    rows = (torch.arange(2 * H, device=DEV) % 251 - 125).bfloat16().view(2, H)
+    s = torch.tensor([[0, 1, -1]], dtype=torch.int32, device=DEV)
+    say("very wide rows")
+    out = mxq.moe_scatter_rows_backward(rows, s)
+    assert torch.equal(out[0], rows[0] + rows[1])  # whole numbers below 256

@@ -356,3 +356,31 @@ def test_refusals():
     # 64 gated columns hold no group of 128
     with pytest.raises(mxq.MxqError):
         call(quant=True, act="silu_mul")
+
+
+@pytest.mark.parametrize("hint", HINTS)
+def test_rows_far_apart(hint):
+    """Rows, scales, residual and output beyond 2^32 bytes of their starts:
+    the widest row strides the call takes."""
+    p = Problem(61, [20, 300], 128, 256, "ue8m0_g128", residual=True,
+                exact=True)
+    d = p.dev()
+    res = p.res.to(DEV)
+    plain = mxq.moe_expert_matmul(**d, residual=res, expected_m=hint)
+    rows, ld, at = 1400, 1 << 22, 1060  # expert 1 begins past 2^32 bytes
+    a, b = int(p.offsets[1]), int(p.counts[1])
+    src = torch.cat([torch.arange(20), torch.arange(a, a + b)]).to(DEV)
+    dst = torch.cat([torch.arange(20), torch.arange(at, at + b)]).to(DEV)
+
+    def far(t):
+        big = torch.empty((rows, ld // t.element_size()), dtype=t.dtype,
+                          device=DEV)[:, :t.shape[1]]
+        big[dst] = t[src]
+        return big
+
+    say("rows far apart", hint)
+    d["q"], d["scales"], res = far(d["q"]), far(d["scales"]), far(res)
+    d["expert_offsets"] = i32_to_dev([0, at, at + b])
+    out = far(torch.zeros_like(plain))
+    mxq.moe_expert_matmul(**d, residual=res, out=out, expected_m=hint)
+    assert torch.equal(out[dst], plain[src])

@@ -175,3 +175,14 @@ def test_expert_matmul_quant_validation(mxq):
                 dict(ldo=264), dict(ldo=240), dict(ldso=1),
                 dict(of=1, ldso=7)):
         assert call(**bad) == INVALID, bad
+
+
+def test_expert_matmul_refuses_row_counts_near_int32(mxq):
+    """Row counts are rounded up to whole tiles in 32 bits."""
+    def call(rows):
+        return mxq.lib().moe_expert_matmul(
+            FAKE, 256, FAKE, 2, rows, 0, FAKE, FAKE, 2, 256, 256, FAKE, FAKE,
+            None, 0, None, 0, 4, FAKE, 256, None)
+
+    assert call((1 << 31) - (1 << 16) + 1) == UNSUPPORTED
+    assert call((1 << 31) - 1) == UNSUPPORTED
