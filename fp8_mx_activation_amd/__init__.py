@@ -204,18 +204,20 @@ def _dev(t: torch.Tensor | None, name: str,
 
 def _at_least(t: torch.Tensor, name: str, rows: int, cols: int) -> None:
     """A 2-D buffer the kernels index up to [rows, cols)."""
-    if t.shape[0] < rows or t.shape[1] < cols:
+    shape = t.shape
+    if shape[0] < rows or shape[1] < cols:
         raise ValueError("%s must be at least [%d, %d], got %s"
                          % (name, rows, cols, tuple(t.shape)))
 
 
 def _src2dst(src2dst: torch.Tensor, like: torch.Tensor, T: int | None):
     _dev(src2dst, "src2dst", like)
-    if src2dst.dtype != torch.int32 or src2dst.dim() != 2 or \
-            (T is not None and src2dst.shape[0] != T) or \
+    shape = src2dst.shape
+    if src2dst.dtype != torch.int32 or len(shape) != 2 or \
+            (T is not None and shape[0] != T) or \
             not src2dst.is_contiguous():
         raise ValueError("src2dst must be contiguous int32 [T, K]")
-    return src2dst.shape[1]
+    return shape[1]
 
 
 def _rows(t: torch.Tensor, name: str, dtypes) -> int:
@@ -231,6 +233,7 @@ def _rows(t: torch.Tensor, name: str, dtypes) -> int:
     return ld if rows > 1 else max(cols, ld)
 
 
+_BF16 = (torch.bfloat16,)
 _FP8 = (torch.uint8, torch.float8_e4m3fn)
 _SCALE = (torch.uint8,) + ((torch.float8_e8m0fnu,)
                            if hasattr(torch, "float8_e8m0fnu") else ())
@@ -347,11 +350,6 @@ def mxq_mfma_scale_bytes(rows: int, H: int, tile_m: int = 32) -> int:
 SCORE_FNS = {"softmax": 0, "sigmoid": 1}
 
 
-def _logits(logits: torch.Tensor, name: str = "logits") -> int:
-    _dev(logits, name)
-    return _rows(logits, name, OUT_DTYPES)
-
-
 def _dense(t: torch.Tensor, name: str, dtype, shape: tuple,
            like: torch.Tensor) -> int | None:
     """Pointer of a contiguous tensor of exactly this dtype and shape, on the
@@ -362,6 +360,36 @@ def _dense(t: torch.Tensor, name: str, dtype, shape: tuple,
         raise ValueError("%s must be contiguous %s %s"
                          % (name, dtype, list(shape)))
     return t.data_ptr() or None
+
+
+def _matrix(t: torch.Tensor, name: str, dtypes,
+            like: torch.Tensor | None = None):
+    """What ``_dev``, ``_rows`` and ``_ptr`` check and give, with each
+    attribute read once: pointer (None if empty), rows, columns, row
+    stride."""
+    dev = t.get_device()
+    if dev < 0 or (like is not None and dev != like.get_device()):
+        _dev(t, name, like)
+    if t.dtype not in dtypes:
+        raise TypeError("%s: dtype %s not in %s" % (name, t.dtype, dtypes))
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError("%s must be 2-D" % name)
+    rows, cols = shape
+    ld, step = t.stride()
+    if cols > 1 and step != 1:
+        raise ValueError("%s must have unit column stride" % name)
+    return (t.data_ptr() or None, rows, cols,
+            ld if rows > 1 else max(cols, ld))
+
+
+def _output(t: torch.Tensor, name: str, dtypes, rows: int, cols: int,
+            like: torch.Tensor):
+    """Pointer and row stride of a caller's output of at least [rows, cols]."""
+    p, r, c, ld = _matrix(t, name, dtypes, like)
+    if r < rows or c < cols:
+        _at_least(t, name, rows, cols)
+    return p, ld
 
 
 def moe_route(logits: torch.Tensor, K: int, scoring: str = "softmax",
@@ -375,8 +403,7 @@ def moe_route(logits: torch.Tensor, K: int, scoring: str = "softmax",
     ``"softmax"`` or ``"sigmoid"``; ``bias`` (float32 [E]) takes part in the
     choice only.  Where fewer than K experts can be chosen the id is -1 and
     the weight 0."""
-    ld = _logits(logits)
-    T, E = logits.shape
+    p, T, E, ld = _matrix(logits, "logits", OUT_DTYPES)
     b = None if bias is None else _dense(bias, "bias", torch.float32, (E,),
                                          logits)
     if ids is None:
@@ -384,7 +411,7 @@ def moe_route(logits: torch.Tensor, K: int, scoring: str = "softmax",
     if weights is None:
         weights = torch.empty((T, K), dtype=torch.float32,
                               device=logits.device)
-    _call("moe_route", logits, logits.data_ptr(), OUT_DTYPES[logits.dtype],
+    _call("moe_route", logits, p, OUT_DTYPES[logits.dtype],
           ld, T, E, K, SCORE_FNS[scoring], b, num_groups, top_groups,
           int(renormalize), weight_scale,
           _dense(ids, "ids", torch.int32, (T, K), logits),
@@ -400,22 +427,21 @@ def moe_route_backward(grad_weights: torch.Tensor, logits: torch.Tensor,
     """Gradient of ``moe_route``'s weights to its logits, with the forward
     call's arguments and its ids: ``grad_logits [T, E]`` in the logits'
     dtype."""
-    ld = _logits(logits)
-    T, E = logits.shape
-    if topk_ids.dim() != 2:
+    p, T, E, ld = _matrix(logits, "logits", OUT_DTYPES)
+    shape = topk_ids.shape
+    if len(shape) != 2:
         raise ValueError("topk_ids must be int32 [T, K]")
-    K = topk_ids.shape[1]
+    K = shape[1]
     ids = _dense(topk_ids, "topk_ids", torch.int32, (T, K), logits)
     g = _dense(grad_weights, "grad_weights", torch.float32, (T, K), logits)
     if grad_logits is None:
         grad_logits = torch.empty((T, E), dtype=logits.dtype,
                                   device=logits.device)
-    _dev(grad_logits, "grad_logits", logits)
-    ld_g = _rows(grad_logits, "grad_logits", (logits.dtype,))
-    _at_least(grad_logits, "grad_logits", T, E)
-    _call("moe_route_backward", logits, g, logits.data_ptr(),
-          OUT_DTYPES[logits.dtype], ld, ids, T, E, K, SCORE_FNS[scoring],
-          int(renormalize), weight_scale, grad_logits.data_ptr(), ld_g)
+    out, ld_g = _output(grad_logits, "grad_logits", (logits.dtype,), T, E,
+                        logits)
+    _call("moe_route_backward", logits, g, p, OUT_DTYPES[logits.dtype], ld,
+          ids, T, E, K, SCORE_FNS[scoring], int(renormalize), weight_scale,
+          out, ld_g)
     return grad_logits
 
 
@@ -856,21 +882,18 @@ def _matmul_inputs(q, scales, w, w_scales, expert_offsets, counts, fmt, act,
                    bias, expected_m):
     """Checked inputs of the experts' products: the C call's leading
     arguments and the shape (rows, output columns)."""
-    _dev(q, "q")
-    _dev(scales, "scales", q)
     code, G = SCALE_FORMATS[fmt]
-    ld_q = _rows(q, "q", _FP8)
-    ld_s = _rows(scales, "scales", _SCALE)
-    rows, H = q.shape
-    _at_least(scales, "scales", rows, H // G)
+    q_p, rows, H, ld_q = _matrix(q, "q", _FP8)
+    s_p, ld_s = _output(scales, "scales", _SCALE, rows, H // G, q)
     _dev(w, "w", q)
-    if w.dtype not in _FP8 or w.dim() != 3 or w.shape[2] != H or \
+    shape = w.shape
+    if w.dtype not in _FP8 or len(shape) != 3 or shape[2] != H or \
             not w.is_contiguous():
         raise ValueError("w must be contiguous fp8 [E, N, %d]" % H)
-    E, N, _ = w.shape
+    E, N, _ = shape
     _dev(w_scales, "w_scales", q)
     blocks = (E, -(-N // 128), -(-H // 128))
-    if w_scales.dtype not in _SCALE or tuple(w_scales.shape) != blocks or \
+    if w_scales.dtype not in _SCALE or w_scales.shape != blocks or \
             not w_scales.is_contiguous():
         raise ValueError("w_scales must be contiguous uint8 %s"
                          % (list(blocks),))
@@ -881,8 +904,8 @@ def _matmul_inputs(q, scales, w, w_scales, expert_offsets, counts, fmt, act,
     a = ACTIVATIONS[act]
     if expected_m is None:
         expected_m = -(-rows // E) if E else 0
-    args = (_ptr(q), ld_q, _ptr(scales), ld_s, rows, code, _ptr(w),
-            _ptr(w_scales), E, N, H, off, cnt, b, a)
+    args = (q_p, ld_q, s_p, ld_s, rows, code, w.data_ptr() or None,
+            w_scales.data_ptr() or None, E, N, H, off, cnt, b, a)
     return args, rows, N // 2 if act == "silu_mul" else N, expected_m
 
 
@@ -905,18 +928,13 @@ def moe_expert_matmul(q: torch.Tensor, scales: torch.Tensor, w: torch.Tensor,
     args, rows, cols, m = _matmul_inputs(q, scales, w, w_scales,
                                          expert_offsets, counts, fmt, act,
                                          bias, expected_m)
-    ld_r = 0
+    res, ld_r = None, 0
     if residual is not None:
-        _dev(residual, "residual", q)
-        ld_r = _rows(residual, "residual", (torch.bfloat16,))
-        _at_least(residual, "residual", rows, cols)
+        res, ld_r = _output(residual, "residual", _BF16, rows, cols, q)
     if out is None:
         out = torch.empty((rows, cols), dtype=torch.bfloat16, device=q.device)
-    _dev(out, "out", q)
-    ld_o = _rows(out, "out", (torch.bfloat16,))
-    _at_least(out, "out", rows, cols)
-    _call("moe_expert_matmul", q, *args, _ptr(residual), ld_r, m, _ptr(out),
-          ld_o)
+    o, ld_o = _output(out, "out", _BF16, rows, cols, q)
+    _call("moe_expert_matmul", q, *args, res, ld_r, m, o, ld_o)
     return out
 
 
@@ -942,14 +960,9 @@ def moe_expert_matmul_quant(q: torch.Tensor, scales: torch.Tensor,
     if scales_out is None:
         scales_out = torch.empty((rows, cols // G), dtype=torch.uint8,
                                  device=q.device)
-    _dev(q_out, "q_out", q)
-    _dev(scales_out, "scales_out", q)
-    ld_o = _rows(q_out, "q_out", _FP8)
-    ld_so = _rows(scales_out, "scales_out", _SCALE)
-    _at_least(q_out, "q_out", rows, cols)
-    _at_least(scales_out, "scales_out", rows, cols // G)
-    _call("moe_expert_matmul_quant", q, *args, m, code, _ptr(q_out), ld_o,
-          _ptr(scales_out), ld_so)
+    o, ld_o = _output(q_out, "q_out", _FP8, rows, cols, q)
+    so, ld_so = _output(scales_out, "scales_out", _SCALE, rows, cols // G, q)
+    _call("moe_expert_matmul_quant", q, *args, m, code, o, ld_o, so, ld_so)
     return q_out, scales_out
 
 
@@ -991,20 +1004,17 @@ def moe_scatter_rows_backward(grad_rows: torch.Tensor, src2dst: torch.Tensor,
     """Gradient of the expert sort: ``out [T, H]``, for every token the fp32
     sum of its rows of ``grad_rows [num_rows, H]`` (bf16 or float32), in the
     rows' dtype unless ``out_dtype`` or ``out`` says otherwise."""
-    _dev(grad_rows, "grad_rows")
-    ld = _rows(grad_rows, "grad_rows", OUT_DTYPES)
-    num_rows, H = grad_rows.shape
+    g, num_rows, H, ld = _matrix(grad_rows, "grad_rows", OUT_DTYPES)
     K = _src2dst(src2dst, grad_rows, None)
     T = src2dst.shape[0]
     if out is None:
         out = torch.empty((T, H), dtype=out_dtype or grad_rows.dtype,
                           device=grad_rows.device)
-    _dev(out, "out", grad_rows)
-    ld_o = _rows(out, "out", OUT_DTYPES)
-    _at_least(out, "out", T, H)
-    _call("moe_scatter_rows_backward", grad_rows, _ptr(grad_rows),
-          OUT_DTYPES[grad_rows.dtype], ld, num_rows, _ptr(src2dst), T, K, H,
-          _ptr(out), ld_o, OUT_DTYPES[out.dtype])
+    o, ld_o = _output(out, "out", OUT_DTYPES, T, H, grad_rows)
+    _call("moe_scatter_rows_backward", grad_rows, g,
+          OUT_DTYPES[grad_rows.dtype], ld, num_rows,
+          src2dst.data_ptr() or None, T, K, H, o, ld_o,
+          OUT_DTYPES[out.dtype])
     return out
 
 
@@ -1016,30 +1026,24 @@ def moe_combine_backward(grad_out: torch.Tensor, y: torch.Tensor,
     [T, H]`` (bf16 or float32): ``(grad_y bf16 [num_rows, H], grad_weights
     float32 [T, K])``.  Rows of ``grad_y`` that are no destination keep the
     contents of a given ``grad_y``."""
-    _dev(grad_out, "grad_out")
-    ld_g = _rows(grad_out, "grad_out", OUT_DTYPES)
-    T, H = grad_out.shape
+    g, T, H, ld_g = _matrix(grad_out, "grad_out", OUT_DTYPES)
     K = _src2dst(src2dst, grad_out, T)
-    _dev(y, "y", grad_out)
-    ld_y = _rows(y, "y", (torch.bfloat16,))
-    num_rows = y.shape[0]
-    if y.shape[1] != H:
+    y_p, num_rows, cols, ld_y = _matrix(y, "y", _BF16, grad_out)
+    if cols != H:
         raise ValueError("y must be [num_rows, %d]" % H)
     w = _dense(topk_weights, "topk_weights", torch.float32, (T, K), grad_out)
     if grad_y is None:
         grad_y = torch.empty((num_rows, H), dtype=torch.bfloat16,
                              device=y.device)
-    _dev(grad_y, "grad_y", grad_out)
-    ld_gy = _rows(grad_y, "grad_y", (torch.bfloat16,))
-    _at_least(grad_y, "grad_y", num_rows, H)
+    gy, ld_gy = _output(grad_y, "grad_y", _BF16, num_rows, H, grad_out)
     if grad_weights is None:
         grad_weights = torch.empty((T, K), dtype=torch.float32,
                                    device=y.device)
     gw = _dense(grad_weights, "grad_weights", torch.float32, (T, K), grad_out)
     if T and K:
-        _call("moe_combine_backward", grad_out, _ptr(grad_out),
-              OUT_DTYPES[grad_out.dtype], ld_g, _ptr(y), ld_y, num_rows,
-              _ptr(src2dst), w, T, K, H, _ptr(grad_y), ld_gy, gw)
+        _call("moe_combine_backward", grad_out, g,
+              OUT_DTYPES[grad_out.dtype], ld_g, y_p, ld_y, num_rows,
+              src2dst.data_ptr(), w, T, K, H, gy, ld_gy, gw)
     return grad_y, grad_weights
 
 
