@@ -132,12 +132,17 @@ __global__ __launch_bounds__(1024) void scatter_rows_backward_kernel(
   }
 }
 
-// One block per token.  The token's gradient row is staged in LDS once, then
-// each wavefront takes assignments j = wave, wave + waves, ...: it reads row
-// d of y, adds up the product with the staged row and writes row d of dy on
-// the same pass, so y and dy are touched once and the dot product needs one
-// wavefront reduction per assignment and no barrier.
-constexpr int kCombineBackThreads = 512;
+// One block of eight wavefronts per token.  The token's gradient row is staged
+// in LDS once, then each wavefront takes one of the assignments that have a
+// row, and the eighth after it: it reads row d of y, adds up the product with
+// the staged row and writes row d of dy on the same pass, so y and dy are
+// touched once and the dot product needs one wavefront reduction per
+// assignment and no barrier.  Where fewer than five assignments have a row
+// (an expert-parallel rank's share), two, four or eight wavefronts take
+// vectors of a row in turn and join their sums in LDS; a token without any
+// is done before its gradient is read.
+constexpr int kCombineBackWaves = 8;
+constexpr int kCombineBackThreads = 64 * kCombineBackWaves;
 
 __device__ __forceinline__ float wave_sum(float v) {
 #pragma unroll
@@ -153,36 +158,43 @@ __global__ __launch_bounds__(kCombineBackThreads) void combine_backward_kernel(
     uint16_t* __restrict__ dy, int64_t ld_dy, float* __restrict__ dw) {
   constexpr int kG = F32_G ? 4 : 2;
   extern __shared__ __attribute__((aligned(16))) char staged[];
+  __shared__ float joined[kCombineBackWaves];
   const int64_t t = blockIdx.x;
   const int lane = threadIdx.x & 63;
-  const int wave = threadIdx.x >> 6;
-  const int waves = blockDim.x >> 6;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int jl = min(lane, K - 1);
   const int32_t d_lane = src2dst[t * K + jl];
   const int32_t w_lane = NEED_Y ? __float_as_int(w[t * K + jl]) : 0;
+  const bool has = lane < K && d_lane >= 0 && d_lane < num_rows;
+  const uint64_t rows = __ballot(has);
+  if (NEED_W && wave == 0 && lane < K && !has) dw[t * K + lane] = 0.0f;
+  if (rows == 0) return;
   const char* gr = g + t * ld_g * kG;
   for (int c = threadIdx.x * 16; c < H * kG; c += blockDim.x * 16)
     *reinterpret_cast<u32x4*>(staged + c) = load16(gr + c);
   __syncthreads();
-  for (int j = wave; j < K; j += waves) {
+  const int n = __popcll(rows);
+  const int share = n == 1 ? 8 : n == 2 ? 4 : n <= 4 ? 2 : 1;  // of a row
+  const int part = wave & (share - 1);
+  uint64_t left = rows;
+  for (int i = wave / share; i > 0; --i) left &= left - 1;
+  while (left != 0) {
+    const int j = __ffsll((unsigned long long)left) - 1;
     const int64_t d = __builtin_amdgcn_readlane(d_lane, j);
-    if (d < 0 || d >= num_rows) {
-      if (NEED_W && lane == 0) dw[t * K + j] = 0.0f;
-      continue;
-    }
     const float wj = __int_as_float(__builtin_amdgcn_readlane(w_lane, j));
-    float part[8];
+    float sum[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) part[i] = 0.0f;
+    for (int i = 0; i < 8; ++i) sum[i] = 0.0f;
     const char* yr = reinterpret_cast<const char*>(y + d * ld_y);
     char* dyr = reinterpret_cast<char*>(dy + d * ld_dy);
     // four vectors of 512 channels in flight per wavefront
-    for (int c0 = lane * 8; c0 < H; c0 += 4 * 512) {
+    const int step = share * 512;
+    for (int c0 = part * 512 + lane * 8; c0 < H; c0 += 4 * step) {
       Ch8<false> v[4];
       if constexpr (NEED_W) {
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const int c = c0 + u * 512;
+          const int c = c0 + u * step;
           if (c < H)
             v[u].load_nt(yr + c * 2);
           else
@@ -191,7 +203,7 @@ __global__ __launch_bounds__(kCombineBackThreads) void combine_backward_kernel(
       }
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        const int c = c0 + u * 512;
+        const int c = c0 + u * step;
         if (c >= H) continue;
         Ch8<F32_G> gv;
         gv.load(staged + c * kG);
@@ -201,7 +213,7 @@ __global__ __launch_bounds__(kCombineBackThreads) void combine_backward_kernel(
           float yf[8];
           v[u].get(yf);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) part[i] = fmaf(gf[i], yf[i], part[i]);
+          for (int i = 0; i < 8; ++i) sum[i] = fmaf(gf[i], yf[i], sum[i]);
         }
         if constexpr (NEED_Y) {
           float o[8];
@@ -212,9 +224,29 @@ __global__ __launch_bounds__(kCombineBackThreads) void combine_backward_kernel(
       }
     }
     if constexpr (NEED_W) {
-      const float s = wave_sum(((part[0] + part[1]) + (part[2] + part[3])) +
-                               ((part[4] + part[5]) + (part[6] + part[7])));
-      if (lane == 0) dw[t * K + j] = s;
+      const float s = wave_sum(((sum[0] + sum[1]) + (sum[2] + sum[3])) +
+                               ((sum[4] + sum[5]) + (sum[6] + sum[7])));
+      if (lane == 0) {
+        if (share == 1)
+          dw[t * K + j] = s;
+        else
+          joined[wave] = s;
+      }
+    }
+    if (share > 1) break;  // a row per group of wavefronts
+#pragma unroll
+    for (int i = 0; i < kCombineBackWaves; ++i) left &= left - 1;
+  }
+  if constexpr (NEED_W) {
+    if (share == 1) return;
+    __syncthreads();
+    if (left != 0 && part == 0 && lane == 0) {
+      float s = joined[wave] + joined[wave + 1];
+      if (share >= 4) s += joined[wave + 2] + joined[wave + 3];
+      if (share == 8)
+        s += (joined[wave + 4] + joined[wave + 5]) +
+             (joined[wave + 6] + joined[wave + 7]);
+      dw[t * K + __ffsll((unsigned long long)left) - 1] = s;
     }
   }
 }
@@ -306,8 +338,8 @@ extern "C" mxq_status moe_combine_backward(
     auto* k = &combine_backward_kernel<decltype(f32)::value,
                                        decltype(ny)::value,
                                        decltype(nw)::value>;
-    // a row of more than 64 KB needs the kernel's LDS limit raised first
-    if (lds > 65536 &&
+    // more than 64 KB, with the joined sums, needs the kernel's limit raised
+    if (lds + kCombineBackWaves * sizeof(float) > 65536 &&
         hipFuncSetAttribute(reinterpret_cast<const void*>(k),
                             hipFuncAttributeMaxDynamicSharedMemorySize,
                             (int)lds) != hipSuccess) {

@@ -246,3 +246,41 @@ def test_sort_gradient_of_very_wide_rows():
     say("very wide rows")
     out = mxq.moe_scatter_rows_backward(rows, s)
     assert torch.equal(out[0], rows[0] + rows[1])  # whole numbers below 256
+
+
+@pytest.mark.parametrize("H,tg", [(8, "f32"), (520, "bf16"), (1528, "f32"),
+                                  (7168, "bf16"), (16384, "f32")])
+def test_combine_backward_by_rows_here(H, tg):
+    """Tokens with none to all of nine assignments here: the shares of a row
+    that wavefronts take.  The bound is test_combine_backward's: with p
+    vectors of 512 channels a row's sum has at most p fused steps and joins
+    of shares, and nine joins within a wavefront."""
+    T, K = 80, 9
+    rng = np.random.default_rng(H)
+    s = np.full((T, K), -1, np.int32)
+    rows = rng.permutation(T * K)
+    at = 0
+    for t in range(T):
+        here = rng.permutation(K)[:t % (K + 1)]
+        s[t, here] = rows[at:at + len(here)]
+        at += len(here)
+    g = randn(1, T, H).to(TYPES[tg])
+    y = randn(2, T * K, H).bfloat16()
+    w = randn(3, T, K)
+    say("combine_backward by rows here", H, tg)
+    src = torch.from_numpy(s).to(DEV)
+    fill = torch.full((T * K, H), 7.0, dtype=torch.bfloat16, device=DEV)
+    got_w = torch.full((T, K), 7.0, device=DEV)
+    got_y, _ = mxq.moe_combine_backward(g.to(DEV), y.to(DEV), src, w.to(DEV),
+                                        grad_y=fill, grad_weights=got_w)
+    want_y, want_w = ref.combine_backward(
+        g.double().numpy(), y.double().numpy(), s, w.numpy(),
+        np.full((T * K, H), 7.0))
+    _, size = ref.combine_backward(
+        g.double().abs().numpy(), y.double().abs().numpy(), s, w.numpy(),
+        np.zeros((T * K, H)))
+    np.testing.assert_allclose(got_y.cpu().double().numpy(), want_y,
+                               rtol=2.0 ** -8 + 2.0 ** -23, atol=1e-40)
+    err = np.abs(host(got_w).astype(np.float64) - want_w)
+    assert (err <= (H / 512 + 10) * 2.0 ** -24 * size).all()
+    assert (host(got_w)[s < 0] == 0).all()
