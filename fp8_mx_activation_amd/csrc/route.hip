@@ -12,21 +12,22 @@
 // one wavefront maximum of ordered integer keys (six v_max with DPP operands
 // for 32 bits, twice that for 64; no LDS memory).
 //
-// Choice values are computed and compared in 64 bits wherever they come out
-// of an exponential: near a tie two experts' values lie closer than fp32
-// rounding, and the choice would then hang on the rounding of exp.  A softmax
-// without bias or groups keeps the order of its logits, so there the fp32
-// logits themselves are the keys and no exponential is taken for the choice.
-// The weights are computed in 64 bits (at most K exponentials per token, one
-// per lane) and rounded once to fp32.
+// Choice values are those of 64 bits wherever they come out of an exponential:
+// near a tie two experts' values lie closer than fp32 rounding, and the choice
+// would then hang on the rounding of exp.  They are first taken in 32 bits with
+// a bound on their error, which decides all but a token in a few hundred; such
+// a token is done again in 64 bits.  A softmax without bias or groups keeps the
+// order of its logits, so there the fp32 logits themselves are the keys and no
+// exponential is taken for the choice.  The weights are computed in 64 bits (at
+// most K exponentials per token, one per lane) and rounded once to fp32.
 //
 // Bound: a row of E logits is 0.5-4 KB, so even 8192 tokens are one or two
-// microseconds of HBM time; the kernel is bound by the K dependent
-// reductions of one wavefront.  Measured: one token of 256 experts in 8
-// groups, sigmoid with bias, top-8: 5.4 us (10.9 with 64-bit shuffles and the
-// groups joined one after another); 8192 tokens of 256 experts, softmax
-// top-8: 7.3-8.4 us (14.2 with 64-bit keys throughout); their gradient, 17 MB:
-// 6.3-7.2 us.  An empty kernel takes 2.1 us, a launch 4.2 us of host time.
+// microseconds of HBM time; the kernel is bound by the K dependent reductions
+// of one wavefront (some 65 instructions each).  Measured in a replayed graph,
+// launches included, 256 experts, top-8: softmax 3.3 us for one token, 7.4 for
+// 8192, 41 for 65536; sigmoid with bias and 4 of 8 groups 5.0, 13-15 and 72 us
+// (5.5, 15.4 and 96 with 64-bit values throughout); their gradients 2.5, 6 and
+// 31 us (134 MB).  An empty kernel takes 2.1 us, a launch 4.2 us of host time.
 #include <type_traits>
 
 #include "mxq_device.hpp"
@@ -107,6 +108,21 @@ __device__ __forceinline__ double wave_sum64(double v) {
                             from_lane(__builtin_bit_cast(uint64_t, v), 63));
 }
 
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float sum_step(float v) {
+  return v + __uint_as_float(dpp32<CTRL, ROWS>(0, __float_as_uint(v)));
+}
+
+__device__ __forceinline__ float wave_sum32(float v) {
+  v = sum_step<0x111, 0xF>(v);
+  v = sum_step<0x112, 0xF>(v);
+  v = sum_step<0x114, 0xF>(v);
+  v = sum_step<0x118, 0xF>(v);
+  v = sum_step<0x142, 0xA>(v);
+  v = sum_step<0x143, 0xC>(v);
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+
 // ------------------------------------------------------------ ordered keys
 
 // Integer whose unsigned order is the order of the value.  Key 0 stands for
@@ -134,9 +150,9 @@ __device__ __forceinline__ float value_of(uint32_t k) {
 }
 
 // The two largest keys of a group: (a1, a2) joined with (b1, b2).
-__device__ __forceinline__ void join_top2(uint64_t& a1, uint64_t& a2,
-                                          uint64_t b1, uint64_t b2) {
-  const uint64_t lesser = min(a1, b1);
+template <typename Key>
+__device__ __forceinline__ void join_top2(Key& a1, Key& a2, Key b1, Key b2) {
+  const Key lesser = min(a1, b1);
   a1 = max(a1, b1);
   a2 = max(lesser, max(a2, b2));
 }
@@ -147,14 +163,28 @@ __device__ __forceinline__ void join_paired(uint64_t& a1, uint64_t& a2) {
   join_top2(a1, a2, dpp64<CTRL, 0xF>(0, a1), dpp64<CTRL, 0xF>(0, a2));
 }
 
+template <int CTRL>
+__device__ __forceinline__ void join_paired(uint32_t& a1, uint32_t& a2) {
+  join_top2(a1, a2, dpp32<CTRL, 0xF>(0, a1), dpp32<CTRL, 0xF>(0, a2));
+}
+
+// The same over a group of 1, 2, 4, 8 or 16 neighbouring lanes of a DPP row:
+// pairwise (quad permutes, then mirrors of 8 and 16 lanes), all groups at
+// once.
+template <typename Key>
+__device__ __forceinline__ void join_group(int lanes, Key& m1, Key& m2) {
+  if (lanes >= 2) join_paired<0xB1>(m1, m2);
+  if (lanes >= 4) join_paired<0x4E>(m1, m2);
+  if (lanes >= 8) join_paired<0x141>(m1, m2);
+  if (lanes >= 16) join_paired<0x140>(m1, m2);
+}
+
 // --------------------------------------------------------------- row access
 
-// The lane's PER logits from e0 on; -inf (never chosen, score 0) past E and
-// for NaN; +inf counts as the largest finite value.
+// The lane's PER values from e0 on, -inf past E.
 template <int PER, bool BF16>
-__device__ __forceinline__ void load_logits(const void* row, int E, int e0,
-                                            bool vec, float (&l)[PER]) {
-  float raw[PER];
+__device__ __forceinline__ void load_row(const void* row, int E, int e0,
+                                         bool vec, float (&raw)[PER]) {
 #pragma unroll
   for (int i = 0; i < PER; ++i) raw[i] = -__builtin_inff();
   if constexpr (BF16) {
@@ -190,9 +220,17 @@ __device__ __forceinline__ void load_logits(const void* row, int E, int e0,
         if (e0 + i < E) raw[i] = p[e0 + i];
     }
   }
+}
+
+// Logits: -inf (never chosen, score 0) for NaN too; +inf counts as the largest
+// finite value.
+template <int PER, bool BF16>
+__device__ __forceinline__ void load_logits(const void* row, int E, int e0,
+                                            bool vec, float (&l)[PER]) {
+  load_row<PER, BF16>(row, E, e0, vec, l);
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const float v = raw[i];
+    const float v = l[i];
     l[i] = v != v ? -__builtin_inff() : (v > kFltMax ? kFltMax : v);
   }
 }
@@ -259,17 +297,160 @@ struct RouteArgs {
   int32_t groups, top_groups;
   int32_t renorm;
   float scale;
-  int32_t vec;  // rows start on 16 bytes
+  int32_t vec, vec_bias;  // rows (the bias) start on 16 bytes
   int32_t* ids;
   float* weights;
 };
 
 constexpr int kMaxGroups = 64;
 
+// Takes the largest of the wavefront's keys (equal ones by lowest index): its
+// key, 0 if none is left, and its expert in `id`.
+template <int PER, typename Key>
+__device__ __forceinline__ Key take_largest(int lane, Key (&key)[PER],
+                                            int& id) {
+  Key m = key[0];
+  int at = 0;  // lowest of the lane's experts that holds m
+#pragma unroll
+  for (int i = 1; i < PER; ++i) {
+    at = key[i] > m ? i : at;
+    m = max(m, key[i]);
+  }
+  const Key best = wave_max_key(m);
+  if (best == 0) return best;
+  const int from = __ffsll((unsigned long long)__ballot(m == best)) - 1;
+  const int taken = __builtin_amdgcn_readlane(at, from);
+  id = from * PER + taken;
+  const int mark = lane == from ? taken : -1;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) key[i] = mark == i ? 0 : key[i];
+  return best;
+}
+
+// K choices; lane j keeps the j-th.  Ids stay -1 once nothing is left.
+template <int PER, typename Key>
+__device__ __forceinline__ void choose(int lane, int K, Key (&key)[PER],
+                                       int& my_id) {
+  for (int j = 0; j < K; ++j) {
+    int id = -1;
+    if (take_largest<PER>(lane, key, id) == 0) break;
+    if (lane == j) my_id = id;
+  }
+}
+
+// A group of gs experts is 1, 2, 4, 8 or 16 whole neighbouring lanes.
+__device__ __forceinline__ bool whole_lanes(int gs, int per) {
+  const int lanes = gs / per;
+  return lanes * per == gs && lanes <= 16 && (lanes & (lanes - 1)) == 0;
+}
+
+// The choice in 32 bits, where it is certain to be that of the 64-bit values:
+// false if two values that decide it lie too close (a token in a few hundred;
+// it then goes by 64 bits).  With u = 2^-24:
+//   - a sigmoid is off by less than 4 u (3 u of its own from the sum and the
+//     reciprocal, and s (1 - s) times the power's 2 u (|l| + 1)), a softmax by
+//     less than 53 u (1 u, and s times 46 u of the sum over the row and 5 u);
+//     adding the bias, u |c| more.  Two values that differ by 2^-20 max(1, |c|)
+//     for the sigmoid, 2^-17 max(1, |c|) for the softmax, are in order;
+//   - a group's value, of two values of at most 16 each, is off by less than
+//     256 u: two that differ by 2^-15 are in order;
+//   - without a bias the choice within the groups goes by the logits.  Logits
+//     that differ by 2^-40 or more (any two beyond 2^-16 do) have scores that
+//     differ in 64 bits too, but for sigmoids close to one (l > 16) and what
+//     comes near 64 bits' smallest (exp(-700)).
+// Where a set is cut off (the groups, the K-th choice) the next one is
+// compared too.
+template <int PER>
+__device__ __forceinline__ bool choose_in_32_bits(const RouteArgs& a, int lane,
+                                                  const float (&l)[PER],
+                                                  const float (&bias)[PER],
+                                                  float top, int& my_id) {
+  constexpr float kLog2e = 1.44269504088896341f;
+  const float inf = __builtin_inff();
+  const bool biased = a.bias != nullptr;
+  uint32_t key[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) key[i] = key_of(l[i]);
+  if (biased || a.groups > 1) {
+    float c[PER];
+    if (a.sigmoid) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        c[i] = __builtin_amdgcn_rcpf(
+            1.0f + __builtin_amdgcn_exp2f(-l[i] * kLog2e));
+    } else {
+      float part = 0.0f;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        c[i] = __builtin_amdgcn_exp2f((l[i] - top) * kLog2e);
+        part += c[i];
+      }
+      const float r = __builtin_amdgcn_rcpf(wave_sum32(part));
+#pragma unroll
+      for (int i = 0; i < PER; ++i) c[i] *= r;
+    }
+    if (biased) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) c[i] += bias[i];
+    }
+    uint32_t ck[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) ck[i] = l[i] > -inf ? key_of(c[i]) : 0;
+    bool keep = true;
+    if (a.groups > 1) {
+      const int lanes = a.E / a.groups / PER;
+      uint32_t m1 = ck[0], m2 = 0;
+#pragma unroll
+      for (int i = 1; i < PER; ++i) join_top2<uint32_t>(m1, m2, ck[i], 0);
+      join_group(lanes, m1, m2);
+      const float v1 = m1 ? value_of(m1) : 0.0f;
+      const float v2 = m2 ? value_of(m2) : 0.0f;
+      const float value = m1 ? v1 + v2 : -inf;
+      // a group's lanes compare it with one other group each
+      const int shift = __popc(lanes - 1);  // lanes is a power of two
+      const int group = lane >> shift, in = lane & (lanes - 1);
+      bool close = !(fabsf(v1) <= 16.0f && fabsf(v2) <= 16.0f);
+      int better = 0;
+      for (int g0 = 0; g0 < a.groups; g0 += lanes) {
+        const int g = g0 + in;
+        const float v = __shfl(value, g << shift);
+        const bool other = g < a.groups && g != group && v > -inf;
+        close |= other && !(fabsf(v - value) > 0x1p-15f);
+        const uint64_t above = __ballot(other && v > value);
+        better += __popcll(above >> (group << shift) & ((1ull << lanes) - 1));
+      }
+      if (__ballot(close) != 0) return false;
+      keep = better < a.top_groups && m1 != 0;
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) key[i] = !keep ? 0 : biased ? ck[i] : key[i];
+  }
+
+  bool sure = true;
+  float last = kFltMax;
+  const float rel = a.sigmoid ? 0x1p-20f : 0x1p-17f;
+  const float low = a.sigmoid ? -700.0f : top - 700.0f;
+  const float high = a.sigmoid ? 16.0f : kFltMax;
+  for (int j = 0; j <= a.K; ++j) {
+    int id = -1;
+    const uint32_t best = take_largest<PER>(lane, key, id);
+    if (best == 0) break;  // nothing left: ids from here on stay -1
+    const float v = value_of(best);
+    const float d = last - v;
+    if (biased)
+      sure &= d > rel * fmaxf(1.0f, fabsf(last));
+    else
+      sure &= (d > 0x1p-40f || (d == 0.0f && (j < a.K || fabsf(v) >= 0x1p-16f))) &&
+              (j == a.K || (v >= low && v <= high));
+    if (lane == j && j < a.K) my_id = id;
+    last = v;
+  }
+  return sure;
+}
+
 // WIDE: 64-bit choice values; else the logits themselves are the choice.
 template <int PER, bool BF16, bool WIDE>
 __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
-  using Key = std::conditional_t<WIDE, uint64_t, uint32_t>;
   const int lane = threadIdx.x & 63;
   const int64_t t = (int64_t)blockIdx.x * (blockDim.x >> 6) +
                     __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -280,6 +461,9 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
                     t * a.ld * (BF16 ? 2 : 4);
   float l[PER];
   load_logits<PER, BF16>(row, E, e0, a.vec != 0, l);
+  float bias[PER];
+  if (WIDE && a.bias != nullptr)
+    load_row<PER, false>(a.bias, E, e0, a.vec_bias != 0, bias);
 
   // a softmax's largest logit, and the sum of its exponentials where a single
   // one depends on it
@@ -292,130 +476,114 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
     top = k ? (double)value_of(k) : 0.0;
   }
 
-  Key key[PER];
+  int my_id = -1;  // lane j: the j-th choice
+  bool chosen = false;
   if constexpr (WIDE) {
-    double s[PER];
-    if (a.sigmoid) {
+    const int gs = E / a.groups;
+    if (a.groups == 1 || whole_lanes(gs, PER))
+      chosen = choose_in_32_bits<PER>(a, lane, l, bias, (float)top, my_id);
+    if (!chosen) {
+      my_id = -1;
+      double s[PER];
+      if (a.sigmoid) {
 #pragma unroll
-      for (int i = 0; i < PER; ++i) s[i] = sigmoid64(l[i]);
-    } else {
-      double part = 0.0;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        s[i] = exp((double)l[i] - top);
-        part += s[i];
-      }
-      z = wave_sum64(part);
-#pragma unroll
-      for (int i = 0; i < PER; ++i) s[i] = s[i] / z;
-    }
-    if (a.bias != nullptr) {
-#pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (e0 + i < E) s[i] += (double)a.bias[e0 + i];
-    }
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-      key[i] = l[i] > -__builtin_inff() ? key_of(s[i]) : 0;
-  } else {
-#pragma unroll
-    for (int i = 0; i < PER; ++i) key[i] = key_of(l[i]);
-    if (!a.renorm) {
-      double part = 0.0;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) part += exp((double)l[i] - top);
-      z = wave_sum64(part);
-    }
-  }
-
-  if constexpr (WIDE) {
-    if (a.groups > 1) {
-      // Group value: the sum of the group's two largest choice values.  A
-      // group without a live expert has none and is never kept.
-      const int gs = E / a.groups;
-      const int lanes = gs / PER;  // of a group
-      uint64_t value = 0;          // key of the lane's group's value
-      int group = 0;
-      const bool aligned = lanes * PER == gs && lanes <= 16 &&
-                           (lanes & (lanes - 1)) == 0;
-      if (aligned) {
-        // a group is 1, 2, 4, 8 or 16 neighbouring lanes of a DPP row: joined
-        // pairwise (quad permutes, then mirrors of 8 and 16 lanes), all
-        // groups at once
-        uint64_t m1 = key[0], m2 = 0;
-#pragma unroll
-        for (int i = 1; i < PER; ++i) join_top2(m1, m2, key[i], 0);
-        if (lanes >= 2) join_paired<0xB1>(m1, m2);
-        if (lanes >= 4) join_paired<0x4E>(m1, m2);
-        if (lanes >= 8) join_paired<0x141>(m1, m2);
-        if (lanes >= 16) join_paired<0x140>(m1, m2);
-        if (m1 != 0)
-          value = key_of(value_of(m1) + (m2 ? value_of(m2) : 0.0));
-        group = lane / max(lanes, 1);
-        // kept: fewer than top_groups others are better (an equal one with a
-        // lower index is)
-        int better = 0;
-        for (int g = 0; g < a.groups; ++g) {
-          const uint64_t v = from_lane(value, g * lanes);
-          better += v > value || (v == value && g < group);
-        }
-        const bool keep = better < a.top_groups && value != 0;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) key[i] = keep ? key[i] : 0;
+        for (int i = 0; i < PER; ++i) s[i] = sigmoid64(l[i]);
       } else {
-        uint64_t mine = 0;  // lane g: the key of group g's value
-        for (int g = 0; g < a.groups; ++g) {
-          const int lo = g * gs, hi = lo + gs;
-          uint64_t m1 = 0, m2 = 0;
-#pragma unroll
-          for (int i = 0; i < PER; ++i)
-            if (e0 + i >= lo && e0 + i < hi) join_top2(m1, m2, key[i], 0);
-          const uint64_t first = wave_max_key(m1);
-          if (first == 0) continue;
-          // the lowest lane that holds it offers its second instead
-          const int owner =
-              __ffsll((unsigned long long)__ballot(m1 == first)) - 1;
-          const uint64_t second = wave_max_key(lane == owner ? m2 : m1);
-          const uint64_t gk =
-              key_of(value_of(first) + (second ? value_of(second) : 0.0));
-          if (lane == g) mine = gk;
-        }
-        uint64_t kept = 0;  // bit g: group g may be chosen from
-        for (int n = 0; n < a.top_groups; ++n) {
-          const uint64_t best = wave_max_key(mine);
-          if (best == 0) break;
-          const int g =
-              __ffsll((unsigned long long)__ballot(mine == best)) - 1;
-          kept |= 1ull << g;
-          if (lane == g) mine = 0;
-        }
+        double part = 0.0;
 #pragma unroll
         for (int i = 0; i < PER; ++i) {
-          const int g = min((e0 + i) / gs, kMaxGroups - 1);
-          if (!((kept >> g) & 1)) key[i] = 0;
+          s[i] = exp((double)l[i] - top);
+          part += s[i];
+        }
+        z = wave_sum64(part);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) s[i] = s[i] / z;
+      }
+      if (a.bias != nullptr) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) s[i] += (double)bias[i];
+      }
+      uint64_t key[PER];
+#pragma unroll
+      for (int i = 0; i < PER; ++i)
+        key[i] = l[i] > -__builtin_inff() ? key_of(s[i]) : 0;
+      if (a.groups > 1) {
+        // Group value: the sum of the group's two largest choice values.  A
+        // group without a live expert has none and is never kept.
+        const int gs = E / a.groups;
+        const int lanes = gs / PER;  // of a group
+        uint64_t value = 0;          // key of the lane's group's value
+        int group = 0;
+        const bool aligned = lanes * PER == gs && lanes <= 16 &&
+                             (lanes & (lanes - 1)) == 0;
+        if (aligned) {
+          uint64_t m1 = key[0], m2 = 0;
+#pragma unroll
+          for (int i = 1; i < PER; ++i) join_top2<uint64_t>(m1, m2, key[i], 0);
+          join_group(lanes, m1, m2);
+          if (m1 != 0)
+            value = key_of(value_of(m1) + (m2 ? value_of(m2) : 0.0));
+          group = lane / max(lanes, 1);
+          // kept: fewer than top_groups others are better (an equal one with a
+          // lower index is)
+          int better = 0;
+          for (int g = 0; g < a.groups; ++g) {
+            const uint64_t v = from_lane(value, g * lanes);
+            better += v > value || (v == value && g < group);
+          }
+          const bool keep = better < a.top_groups && value != 0;
+#pragma unroll
+          for (int i = 0; i < PER; ++i) key[i] = keep ? key[i] : 0;
+        } else {
+          uint64_t mine = 0;  // lane g: the key of group g's value
+          for (int g = 0; g < a.groups; ++g) {
+            const int lo = g * gs, hi = lo + gs;
+            uint64_t m1 = 0, m2 = 0;
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+              if (e0 + i >= lo && e0 + i < hi)
+                join_top2<uint64_t>(m1, m2, key[i], 0);
+            const uint64_t first = wave_max_key(m1);
+            if (first == 0) continue;
+            // the lowest lane that holds it offers its second instead
+            const int owner =
+                __ffsll((unsigned long long)__ballot(m1 == first)) - 1;
+            const uint64_t second = wave_max_key(lane == owner ? m2 : m1);
+            const uint64_t gk =
+                key_of(value_of(first) + (second ? value_of(second) : 0.0));
+            if (lane == g) mine = gk;
+          }
+          uint64_t kept = 0;  // bit g: group g may be chosen from
+          for (int n = 0; n < a.top_groups; ++n) {
+            const uint64_t best = wave_max_key(mine);
+            if (best == 0) break;
+            const int g =
+                __ffsll((unsigned long long)__ballot(mine == best)) - 1;
+            kept |= 1ull << g;
+            if (lane == g) mine = 0;
+          }
+#pragma unroll
+          for (int i = 0; i < PER; ++i) {
+            const int g = min((e0 + i) / gs, kMaxGroups - 1);
+            if (!((kept >> g) & 1)) key[i] = 0;
+          }
         }
       }
+      choose<PER>(lane, a.K, key, my_id);
     }
+  } else {
+    uint32_t key[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) key[i] = key_of(l[i]);
+    choose<PER>(lane, a.K, key, my_id);
+    chosen = true;
   }
-
-  // K choices; lane j keeps the j-th
-  int my_id = -1;
-  for (int j = 0; j < a.K; ++j) {
-    Key m = key[0];
-    int at = 0;  // lowest of the lane's experts that holds m
+  // a softmax's own score takes the sum over the row
+  if (chosen && !a.sigmoid && !a.renorm) {
+    double part = 0.0;
 #pragma unroll
-    for (int i = 1; i < PER; ++i) {
-      at = key[i] > m ? i : at;
-      m = max(m, key[i]);
-    }
-    const Key best = wave_max_key(m);
-    if (best == 0) break;  // nothing left: ids from here on stay -1
-    const int from = __ffsll((unsigned long long)__ballot(m == best)) - 1;
-    const int taken = __builtin_amdgcn_readlane(at, from);
-    if (lane == j) my_id = from * PER + taken;
-    const int mark = lane == from ? taken : -1;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) key[i] = mark == i ? 0 : key[i];
+    for (int i = 0; i < PER; ++i) part += exp((double)l[i] - top);
+    z = wave_sum64(part);
   }
 
   double p = 0.0;
@@ -602,6 +770,7 @@ extern "C" mxq_status moe_route(const void* logits, mxq_out_dtype dtype,
               bias,       num_groups, top_groups,
               renormalize != 0, weight_scale,
               row_vec(logits, ld_logits, dtype == MXQ_OUT_BF16 ? 2 : 4),
+              aligned16(bias),
               topk_ids,   topk_weights};
   const unsigned blocks = (unsigned)ceil_div(T, waves);
   hipStream_t s = as_stream(stream);

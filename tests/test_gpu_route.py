@@ -124,6 +124,69 @@ def test_near_ties_go_by_64_bits():
         assert host(ids)[:, 0].tolist() == [40 + t for t in range(8)]
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,G,g,K", [(256, 8, 4, 8), (256, 1, 1, 8),
+                                     (96, 6, 2, 9), (1024, 16, 3, 5),
+                                     (40, 40, 7, 7)])
+def test_values_close_together(E, G, g, K, scoring, dtype):
+    """Choice values, group sums and cut-offs that 32 bits cannot tell apart
+    among others that they can, with and without a bias; saturated scores.
+
+    A 64-bit value takes an exponential (one unit, 2^-52 of it), a sum, a
+    quotient and the bias's sum (2^-53 each), a softmax's sum over the row
+    1024 positive terms: 2^-42 of the value at most, two of them in a group's
+    value.  What differs by less may go either way."""
+    rng = np.random.default_rng(E + G)
+    T = 96
+    spread = 10.0 ** rng.uniform(-9, 0, (T, 1))
+    centre = rng.choice([0.0, 0.0, 1.5, -3.0, 12.0, 20.0, 40.0, -720.0],
+                        (T, 1))
+    l = centre + spread * rng.standard_normal((T, E))
+    l[:16] = 1e-8 * rng.integers(-3, 4, (16, E))
+    l[16:24, ::3] = -np.inf
+    l = torch.from_numpy(l.astype(np.float32)).to(TYPES[dtype])
+    ties = np.where(rng.random(E) < 0.5, 0.25, -1.0)
+    for bias in (None, ties, 2.0 ** -23 * rng.integers(0, 9, E),
+                 rng.standard_normal(E), 30 * rng.standard_normal(E)):
+        b = None if bias is None else bias.astype(np.float32)
+        say("route close", E, G, g, K, scoring, dtype, b is None)
+        ids, w = mxq.moe_route(
+            l.to(DEV), K, scoring=scoring,
+            bias=None if b is None else torch.from_numpy(b).to(DEV),
+            num_groups=G, top_groups=g)
+        ids, w = host(ids), host(w)
+        L = ref.clean_logits(as64(l))
+        for t in range(T):
+            s = ref.scores(L[t], scoring)
+            c = s + (0 if b is None else b.astype(np.float64))
+            tol = 2.0 ** -40 * max(1.0, np.abs(c).max())
+            live = L[t] > -np.inf
+            c = np.where(live, c, -np.inf)
+            two = -np.sort(-c.reshape(G, -1), axis=1)[:, :2]
+            value = np.where(two > -np.inf, two, 0).sum(1)
+            value[two[:, 0] == -np.inf] = -np.inf
+            group = np.arange(E) // (E // G)
+            better = (value[None] > value[:, None] + tol).sum(1)
+            at_least = (value[None] >= value[:, None] - tol).sum(1) - 1
+            may = live & (better[group] < g)       # in a group that may be kept
+            must = live & (at_least[group] < g)    # in one that is kept
+            got = ids[t][ids[t] >= 0]
+            assert len(set(got.tolist())) == len(got) and may[got].all()
+            assert (ids[t][len(got):] == -1).all()
+            assert len(got) == K or must.sum() <= len(got)
+            assert (c[got][:-1] >= c[got][1:] - tol).all()
+            rest = must.copy()
+            rest[got] = False
+            if len(got):
+                assert not (c[rest] > c[got].min() + tol).any(), t
+            if b is None and G == 1 and scoring == "softmax":
+                assert (L[t][got][:-1] >= L[t][got][1:]).all()
+            p = s[got] / s[got].sum() if s[got].sum() > 0 else 0 * s[got]
+            np.testing.assert_allclose(w[t][:len(got)], p, rtol=2.0 ** -23,
+                                       atol=2.0 ** -149)
+
+
 def test_strided_logits_and_given_outputs():
     rng = np.random.default_rng(9)
     for dtype, pad in (("f32", 3), ("bf16", 1), ("f32", 4), ("bf16", 8)):
