@@ -24,8 +24,9 @@
 // Bound: a row of E logits is 0.5-4 KB, so even 8192 tokens are one or two
 // microseconds of HBM time; the kernel is bound by the K dependent reductions
 // of one wavefront (some 65 instructions each).  Measured in a replayed graph,
-// launches included, 256 experts, top-8: softmax 3.3 us for one token, 7.4 for
-// 8192, 41 for 65536; sigmoid with bias and 4 of 8 groups 5.0, 13-15 and 72 us
+// launches included, 256 experts, top-8: softmax of bf16 logits 2.9 us for one
+// token, 6.7 for 8192, 36 for 65536 (3.3, 7.4 and 41 with whole 32-bit keys, as
+// for fp32); sigmoid with bias and 4 of 8 groups 5.0, 13-15 and 72 us
 // (5.5, 15.4 and 96 with 64-bit values throughout); their gradients 2.5, 6 and
 // 31 us (134 MB).  An empty kernel takes 2.1 us, a launch 4.2 us of host time.
 #include <type_traits>
@@ -338,6 +339,31 @@ __device__ __forceinline__ void choose(int lane, int K, Key (&key)[PER],
   }
 }
 
+// The same for bf16 logits, whose keys have 16 bits to spare: with the expert
+// in them (the lower index the larger), the largest key says whose it is and
+// is no one else's.  Rounding up keeps the order of the 16 bits, and the
+// largest finite fp32 value, which stands for infinity, above bf16's.
+template <int PER>
+__device__ __forceinline__ void choose_packed(int lane, int K,
+                                              uint32_t (&key)[PER],
+                                              int& my_id) {
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+    key[i] = key[i] == 0 ? 0
+                         : ((key[i] + 0xFFFFu) & 0xFFFF0000u) |
+                               (0xFFFFu - (uint32_t)(lane * PER + i));
+  for (int j = 0; j < K; ++j) {
+    uint32_t m = key[0];
+#pragma unroll
+    for (int i = 1; i < PER; ++i) m = max(m, key[i]);
+    const uint32_t best = wave_max_key(m);
+    if (best == 0) break;
+    if (lane == j) my_id = (int)(0xFFFFu - (best & 0xFFFFu));
+#pragma unroll
+    for (int i = 0; i < PER; ++i) key[i] = key[i] == best ? 0 : key[i];
+  }
+}
+
 // A group of gs experts is 1, 2, 4, 8 or 16 whole neighbouring lanes.
 __device__ __forceinline__ bool whole_lanes(int gs, int per) {
   const int lanes = gs / per;
@@ -575,7 +601,10 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
     uint32_t key[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) key[i] = key_of(l[i]);
-    choose<PER>(lane, a.K, key, my_id);
+    if constexpr (BF16)
+      choose_packed<PER>(lane, a.K, key, my_id);
+    else
+      choose<PER>(lane, a.K, key, my_id);
     chosen = true;
   }
   // a softmax's own score takes the sum over the row

@@ -316,3 +316,18 @@ def test_route_refusals():
                                grad_logits=l.bfloat16())
     i, w = mxq.moe_route(l[:0], 4)
     assert tuple(i.shape) == (0, 4) and tuple(w.shape) == (0, 4)
+
+
+@pytest.mark.parametrize("E", [1, 5, 64, 200, 256, 1000, 1024])
+def test_every_bf16_value(E):
+    """All bf16 bit patterns as logits, NaNs and infinities among them, each
+    beside others drawn at random and its own repetition."""
+    rng = np.random.default_rng(E)
+    bits = rng.permutation(65536).astype(np.uint16)
+    pad = (-len(bits)) % E
+    bits = np.concatenate([bits, bits[:pad]]).reshape(-1, E)
+    bits = bits[rng.permutation(len(bits))[:512]]
+    bits[:, E // 2:] = bits[:, :E - E // 2]
+    l = torch.from_numpy(bits.view(np.int16).copy()).view(torch.bfloat16)
+    check(rng, l, min(E, 9), "bf16", "bf16 values")
+    check(rng, l, min(E, 9), "bf16", "bf16 values", renorm=False)
