@@ -649,12 +649,12 @@ struct RouteBackArgs {
 };
 
 // With q_j the chosen scores over their sum: renormalized weights give
-// ds_j = scale / sum * (g_j - sum_i q_i g_i), others ds_j = scale * g_j.
-// Sigmoid scores: dl_j = ds_j s_j (1 - s_j), with 1 - s_j = exp(-l_j) s_j, for
+// s_j ds_j = scale * q_j * (g_j - sum_i q_i g_i), others scale * s_j * g_j.
+// Sigmoid scores: dl_j = s_j ds_j (1 - s_j), with 1 - s_j = exp(-l_j) s_j, for
 // the difference leaves nothing of it near one.  Softmax scores: the
-// renormalized form depends on the chosen logits alone, dl_j = scale * q_j *
-// (g_j - sum_i q_i g_i); the other reads the whole row, dl_e = scale * p_e *
-// (g_e [e chosen] - sum_j p_j g_j).  In 64 bits, rounded once.
+// renormalized form depends on the chosen logits alone, dl_j = s_j ds_j; the
+// other reads the whole row, dl_e = scale * p_e * (g_e [e chosen] -
+// sum_j p_j g_j).  In 64 bits, rounded once.
 template <int PER, bool BF16>
 __global__ __launch_bounds__(256) void route_backward_kernel(RouteBackArgs a) {
   const int lane = threadIdx.x & 63;
@@ -687,13 +687,14 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteBackArgs a) {
     const double x = exp(-(double)lj);  // infinite below -709.8: s is 0
     const double s = has ? 1.0 / (1.0 + x) : 0.0;
     const double rest = s > 0.0 ? x * s : 1.0;  // 1 - s
-    double ds = (double)a.scale * g;
+    double ds = (double)a.scale * s * g;
     if (a.renorm) {
+      // s over the sum, whose reciprocal may be beyond 64 bits
       const double total = wave_sum64(s);
-      const double inv = total > 0.0 ? 1.0 / total : 0.0;
-      ds = (double)a.scale * inv * (g - wave_sum64(s * inv * g));
+      const double q = total > 0.0 ? s / total : 0.0;
+      ds = (double)a.scale * q * (g - wave_sum64(q * g));
     }
-    d = has ? ds * s * rest : 0.0;
+    d = has ? ds * rest : 0.0;
   } else if (a.renorm) {
     const uint32_t k = wave_max_key(key_of(lj));
     const double top = k ? (double)value_of(k) : 0.0;

@@ -142,7 +142,8 @@ size_t requant_workspace_bytes(int64_t T, int32_t H);
  *   topk_weights  fp32 [T, K]: weight_scale * s, divided by the sum of the
  *                 chosen s if renormalize != 0 (0 if that sum is 0 in fp64:
  *                 a softmax whose chosen logits all lie more than 745 below
- *                 the row's largest).
+ *                 the row's largest, sigmoids of logits below -709.8, where
+ *                 exp(-l) is beyond fp64).
  * Choice values are s_e (+ bias_e) in fp64; without bias and groups a softmax
  * chooses by the logits, whose order it keeps.  An expert whose logit or
  * choice value is -inf or NaN is never chosen: where fewer than K are left
@@ -165,7 +166,8 @@ mxq_status moe_route(const void* logits, mxq_out_dtype dtype,
  *                 row are written.  Ids outside [0, E) add nothing; an id
  *                 that occurs twice in a row adds up.
  * A renormalized softmax's weights depend on the chosen logits alone; their
- * gradient is that quotient's, also where the forward's sum is 0.
+ * gradient is that quotient's, also where the forward's sum is 0 (a
+ * sigmoid's gradient is 0 there).
  * grad_logits must not overlap logits. */
 mxq_status moe_route_backward(const float* grad_weights, const void* logits,
                               mxq_out_dtype dtype, int64_t ld_logits,

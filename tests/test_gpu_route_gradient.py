@@ -99,3 +99,17 @@ def test_saturated_sigmoid(dtype):
     g = torch.from_numpy(rng.standard_normal((171, 3))).float()
     say("saturated sigmoid", dtype)
     check(l, ids_of(rng, 171, 6, 3), g, "sigmoid", False, 1.5, dtype)
+
+
+@pytest.mark.parametrize("K", [1, 2, 8])
+def test_sigmoids_near_nothing(K):
+    """Scores whose sum is so small that its reciprocal is beyond 64 bits:
+    the weights, and their gradients, are of ordinary size."""
+    rng = np.random.default_rng(2)
+    l = torch.from_numpy(-709.7 + rng.uniform(0, 3, (40, 16))).float()
+    l[:8] = -709.75
+    l[8:16] = -600
+    g = torch.from_numpy(rng.standard_normal((40, K))).float()
+    g[0] = 1
+    say("sigmoids near nothing", K)
+    check(l, ids_of(rng, 40, 16, K), g, "sigmoid", True, 2.5)
