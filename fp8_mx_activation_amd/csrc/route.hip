@@ -648,13 +648,25 @@ struct RouteBackArgs {
   int64_t ld_out;
 };
 
+// The value v of the lowest lane that holds the wavefront's largest l.
+__device__ __forceinline__ double of_largest(float l, double v) {
+  const uint32_t k = key_of(l);
+  const int lane =
+      __ffsll((unsigned long long)__ballot(k == wave_max_key(k))) - 1;
+  return __builtin_bit_cast(double,
+                            from_lane(__builtin_bit_cast(uint64_t, v), lane));
+}
+
 // With q_j the chosen scores over their sum: renormalized weights give
 // s_j ds_j = scale * q_j * (g_j - sum_i q_i g_i), others scale * s_j * g_j.
 // Sigmoid scores: dl_j = s_j ds_j (1 - s_j), with 1 - s_j = exp(-l_j) s_j, for
 // the difference leaves nothing of it near one.  Softmax scores: the
 // renormalized form depends on the chosen logits alone, dl_j = s_j ds_j; the
-// other reads the whole row, dl_e = scale * p_e * (g_e [e chosen] -
-// sum_j p_j g_j).  In 64 bits, rounded once.
+// other reads the whole row, dl_e = scale * p_e * (G_e - sum_i p_i G_i), G_e
+// the sum of an expert's g_j (0 unless chosen).  The scores add up to one, so
+// gradients may be taken against any one: against the largest score's, the
+// sum is of what the others add and keeps its bits however little that is.
+// In 64 bits, rounded to fp32 and from there to bf16.
 template <int PER, bool BF16>
 __global__ __launch_bounds__(256) void route_backward_kernel(RouteBackArgs a) {
   const int lane = threadIdx.x & 63;
@@ -692,7 +704,8 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteBackArgs a) {
       // s over the sum, whose reciprocal may be beyond 64 bits
       const double total = wave_sum64(s);
       const double q = total > 0.0 ? s / total : 0.0;
-      ds = (double)a.scale * q * (g - wave_sum64(q * g));
+      const double dg = g - of_largest(lj, g);
+      ds = (double)a.scale * q * (dg - wave_sum64(q * dg));
     }
     d = has ? ds * rest : 0.0;
   } else if (a.renorm) {
@@ -701,7 +714,8 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteBackArgs a) {
     const double x = has ? exp((double)lj - top) : 0.0;
     const double total = wave_sum64(x);
     const double q = total > 0.0 ? x / total : 0.0;
-    d = (double)a.scale * q * (g - wave_sum64(q * g));
+    const double dg = g - of_largest(lj, g);
+    d = (double)a.scale * q * (dg - wave_sum64(q * dg));
   } else {
     float l[PER];
     load_logits<PER, BF16>(row, E, e0, a.vec_in != 0, l);
@@ -719,22 +733,31 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteBackArgs a) {
     }
     const double z = wave_sum64(part);
     const double inv = z > 0.0 ? 1.0 / z : 0.0;
-    const double pj = has ? exp((double)lj - top) * inv : 0.0;
-    d = (double)a.scale * pj * g;
-    const double dot = wave_sum64(pj * g) * (double)a.scale;
-    double full[PER];
+    double G[PER];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) full[i] = -x[i] * inv * dot;
+    for (int i = 0; i < PER; ++i) G[i] = 0.0;
     for (int j = 0; j < a.K; ++j) {
       const int idj = __builtin_amdgcn_readlane(id, j);
-      const double dj = __builtin_bit_cast(
-          double, from_lane(__builtin_bit_cast(uint64_t, d), j));
+      const double gj = __builtin_bit_cast(
+          double, from_lane(__builtin_bit_cast(uint64_t, g), j));
 #pragma unroll
       for (int i = 0; i < PER; ++i)
-        if (idj == e0 + i) full[i] += dj;
+        if (idj == e0 + i) G[i] += gj;
     }
+    double mine = G[0];  // of an expert with the lane's largest logit
 #pragma unroll
-    for (int i = 0; i < PER; ++i) res[i] = (float)full[i];
+    for (int i = 1; i < PER; ++i) mine = l[i] == m ? G[i] : mine;
+    const double largest = of_largest(m, mine);
+    double dot = 0.0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      G[i] -= largest;
+      dot += x[i] * G[i];
+    }
+    dot = wave_sum64(dot) * inv;
+#pragma unroll
+    for (int i = 0; i < PER; ++i)
+      res[i] = (float)((double)a.scale * (x[i] * inv) * (G[i] - dot));
     store_row<PER, BF16>(out, E, e0, a.vec_out != 0, res);
     return;
   }

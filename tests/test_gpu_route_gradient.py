@@ -24,6 +24,9 @@ from gpu_util import DEV, say
 pytestmark = pytest.mark.gpu
 
 HALF = {torch.float32: 2.0 ** -24, torch.bfloat16: 2.0 ** -8}
+# subnormals lie 2^-149 apart in fp32 and 2^-133 in bf16 (2^-126 / 2^7), whose
+# half step is 2^-134; fp32's whole step covers the rounding before bf16's
+SMALL = {torch.float32: 2.0 ** -149, torch.bfloat16: 2.0 ** -134 + 2.0 ** -149}
 
 
 def exact(g, l, ids, scoring, renorm, scale):
@@ -79,7 +82,7 @@ def check(l, ids, g, scoring, renorm, scale, dtype=torch.float32):
     want, size = exact(g.numpy(), l.double().numpy(), ids.numpy(), scoring,
                        renorm, scale)
     off = np.abs(got - want)
-    lim = HALF[dtype] * 1.001 * np.abs(want) + 2.0 ** -42 * size + 2.0 ** -149
+    lim = HALF[dtype] * 1.001 * np.abs(want) + 2.0 ** -42 * size + SMALL[dtype]
     assert (off <= lim).all(), (np.argwhere(~(off <= lim))[:4].tolist(),
                                 got[~(off <= lim)][:4],
                                 want[~(off <= lim)][:4])
@@ -113,3 +116,26 @@ def test_sigmoids_near_nothing(K):
     g[0] = 1
     say("sigmoids near nothing", K)
     check(l, ids_of(rng, 40, 16, K), g, "sigmoid", True, 2.5)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("scoring,renorm", [("softmax", True),
+                                            ("softmax", False),
+                                            ("sigmoid", True)])
+def test_one_score_far_above_the_others(scoring, renorm, dtype):
+    """Its gradient is what the others leave of one; the others' hang on the
+    difference to its gradient, which may be small or nothing."""
+    rng = np.random.default_rng(3)
+    T, E, K = 90, 12, 5
+    l = torch.from_numpy(rng.standard_normal((T, E)) - 40).float()
+    ids = ids_of(rng, T, E, K)
+    top = rng.integers(0, K, T)
+    for t in range(T):
+        e = ids[t, top[t]] if t % 3 else E - 1  # chosen, or maybe not
+        l[t, e] = -40 + t
+    g = torch.from_numpy(rng.standard_normal((T, K))).float()
+    g[::4] = g[::4, :1]                          # all equal
+    g[1::4] = g[1::4, :1] * (1 + 2.0 ** -20 * torch.from_numpy(
+        rng.standard_normal((len(g[1::4]), K))).float())
+    say("one score far above", scoring, renorm, dtype)
+    check(l, ids, g, scoring, renorm, 2.5, dtype)
