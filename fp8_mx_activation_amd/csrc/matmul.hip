@@ -38,7 +38,11 @@ __device__ __forceinline__ v4i buffer_of(const void* base, uint32_t bytes) {
 // 16 bytes per lane from `buf` at voff + soff into LDS at lds + 16 * lane.
 // The lane's address registers are the only operands: nothing is returned to
 // registers, so there is no result to wait for but the vmcnt before the next
-// barrier.
+// barrier.  The clobbers keep LDS accesses, and what the compiler may hold in
+// m0, on their side of the copy (it warns that m0 is a register it never
+// allocates; it does write it for instructions of its own).
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void copy_to_lds(const v4i& buf, uint32_t lds,
                                             uint32_t voff, uint32_t soff) {
   asm volatile(
@@ -46,8 +50,10 @@ __device__ __forceinline__ void copy_to_lds(const v4i& buf, uint32_t lds,
       "s_nop 0\n\t"
       "buffer_load_dwordx4 %1, %2, %3 offen lds"
       :
-      : "s"(lds), "v"(voff), "s"(buf), "s"(soff));
+      : "s"(lds), "v"(voff), "s"(buf), "s"(soff)
+      : "m0", "memory");
 }
+#pragma clang diagnostic pop
 
 // Waits until all but the last VM loads and copies and the last LGKM LDS reads
 // that this wavefront has issued are done.
