@@ -288,15 +288,19 @@ extern "C" mxq_status moe_scatter_rows_backward(
   if (T <= kBackSliceMaxTokens && H > kBackSlice)
     slice = (int32_t)std::max<int64_t>(
         kBackSlice, ceil_div(ceil_div(H, 65535), 8) * 8);
-  const dim3 grid((unsigned)T, (unsigned)ceil_div(H, slice));
   const int threads = row_block_threads(slice, 8);
+  const int64_t most = max_blocks(threads);  // tokens of a launch
   hipStream_t s = as_stream(stream);
   const char* r = static_cast<const char*>(grad_rows);
   char* o = static_cast<char*>(grad_x);
   auto go = [&](auto fin, auto fout) {
-    scatter_rows_backward_kernel<decltype(fin)::value, decltype(fout)::value>
-        <<<grid, threads, 0, s>>>(r, ld_rows, num_rows, src2dst, K, H, slice,
-                                  o, ld_x);
+    for (int64_t t = 0; t < T; t += most)
+      scatter_rows_backward_kernel<decltype(fin)::value,
+                                   decltype(fout)::value>
+          <<<dim3((unsigned)std::min(most, T - t),
+                  (unsigned)ceil_div(H, slice)),
+             threads, 0, s>>>(r, ld_rows, num_rows, src2dst + t * K, K, H,
+                              slice, o + t * ld_x * on, ld_x);
   };
   using Y = std::true_type;
   using N = std::false_type;
@@ -348,11 +352,14 @@ extern "C" mxq_status moe_combine_backward(
       (void)hipGetLastError();
       return MXQ_ERR_HIP;
     }
-    k<<<(unsigned)T, kCombineBackThreads, lds, s>>>(
-        static_cast<const char*>(grad_out), ld_g,
-        static_cast<const uint16_t*>(y_bf16), ld_y, num_rows, src2dst,
-        topk_weights, K, H, static_cast<uint16_t*>(grad_y_bf16), ld_gy,
-        grad_weights);
+    const int64_t most = max_blocks(kCombineBackThreads);  // of a launch
+    for (int64_t t = 0; t < T; t += most)
+      k<<<(unsigned)std::min(most, T - t), kCombineBackThreads, lds, s>>>(
+          static_cast<const char*>(grad_out) + t * ld_g * esz, ld_g,
+          static_cast<const uint16_t*>(y_bf16), ld_y, num_rows,
+          src2dst + t * K, need_y ? topk_weights + t * K : nullptr, K, H,
+          static_cast<uint16_t*>(grad_y_bf16), ld_gy,
+          need_w ? grad_weights + t * K : nullptr);
     return launch_status();
   };
   using Y = std::true_type;

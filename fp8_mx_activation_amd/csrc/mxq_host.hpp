@@ -32,6 +32,11 @@ inline int group_of(mxq_scale_fmt fmt) {
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// Blocks of `threads` that one launch holds along an axis.  The runtime counts
+// an axis in threads, in 32 bits: a longer one wraps without an error, and the
+// blocks past it never run.
+inline int64_t max_blocks(int threads) { return (int64_t)UINT32_MAX / threads; }
+
 // Threads per block for a row split in chunks of `per_lane` channels: a
 // whole number of 64-lane wavefronts, at most 1024.
 inline int row_block_threads(int64_t H, int per_lane) {

@@ -29,6 +29,7 @@
 // for fp32); sigmoid with bias and 4 of 8 groups 5.0, 13-15 and 72 us
 // (5.5, 15.4 and 96 with 64-bit values throughout); their gradients 2.5, 6 and
 // 31 us (134 MB).  An empty kernel takes 2.1 us, a launch 4.2 us of host time.
+#include <algorithm>
 #include <type_traits>
 
 #include "mxq_device.hpp"
@@ -778,6 +779,16 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteBackArgs a) {
 // that one, so that every token has a CU of its own.
 inline int route_waves(int64_t T) { return T > 256 ? 4 : 1; }
 
+// Calls f(first token, tokens, blocks) for every launch that T tokens take.
+template <typename F>
+void by_launches(int64_t T, int waves, F&& f) {
+  const int64_t most = max_blocks(waves * 64) * waves;
+  for (int64_t t = 0; t < T; t += most) {
+    const int64_t n = std::min(most, T - t);
+    f(t, n, (unsigned)ceil_div(n, waves));
+  }
+}
+
 inline bool row_vec(const void* p, int64_t ld, int64_t esz) {
   return aligned16(p) && (ld * esz) % 16 == 0;
 }
@@ -820,26 +831,34 @@ extern "C" mxq_status moe_route(const void* logits, mxq_out_dtype dtype,
   if (logits == nullptr || topk_ids == nullptr || topk_weights == nullptr ||
       ld_logits < E)
     return MXQ_ERR_INVALID_ARGUMENT;
+  const int64_t esz = dtype == MXQ_OUT_BF16 ? 2 : 4;
   const int waves = route_waves(T);
   RouteArgs a{logits,     ld_logits,  T,
               E,          K,          score == MXQ_SCORE_SIGMOID,
               bias,       num_groups, top_groups,
               renormalize != 0, weight_scale,
-              row_vec(logits, ld_logits, dtype == MXQ_OUT_BF16 ? 2 : 4),
+              row_vec(logits, ld_logits, esz),
               aligned16(bias),
               topk_ids,   topk_weights};
-  const unsigned blocks = (unsigned)ceil_div(T, waves);
   hipStream_t s = as_stream(stream);
   // a softmax keeps the order of its logits
   const bool wide = a.sigmoid || bias != nullptr || num_groups > 1;
-  by_experts(E, [&](auto per) {
-    constexpr int kPer = decltype(per)::value;
-    if (dtype == MXQ_OUT_BF16)
-      wide ? route_kernel<kPer, true, true><<<blocks, waves * 64, 0, s>>>(a)
-           : route_kernel<kPer, true, false><<<blocks, waves * 64, 0, s>>>(a);
-    else
-      wide ? route_kernel<kPer, false, true><<<blocks, waves * 64, 0, s>>>(a)
-           : route_kernel<kPer, false, false><<<blocks, waves * 64, 0, s>>>(a);
+  by_launches(T, waves, [&](int64_t t, int64_t n, unsigned blocks) {
+    a.logits = static_cast<const char*>(logits) + t * ld_logits * esz;
+    a.T = n;
+    a.ids = topk_ids + t * K;
+    a.weights = topk_weights + t * K;
+    by_experts(E, [&](auto per) {
+      constexpr int kPer = decltype(per)::value;
+      if (dtype == MXQ_OUT_BF16)
+        wide ? route_kernel<kPer, true, true><<<blocks, waves * 64, 0, s>>>(a)
+             : route_kernel<kPer, true, false>
+                   <<<blocks, waves * 64, 0, s>>>(a);
+      else
+        wide ? route_kernel<kPer, false, true><<<blocks, waves * 64, 0, s>>>(a)
+             : route_kernel<kPer, false, false>
+                   <<<blocks, waves * 64, 0, s>>>(a);
+    });
   });
   return launch_status();
 }
@@ -866,14 +885,20 @@ extern "C" mxq_status moe_route_backward(
                   score == MXQ_SCORE_SIGMOID, renormalize != 0, weight_scale,
                   row_vec(logits, ld_logits, esz),
                   row_vec(grad_logits, ld_grad, esz), grad_logits, ld_grad};
-  const unsigned blocks = (unsigned)ceil_div(T, waves);
   hipStream_t s = as_stream(stream);
-  by_experts(E, [&](auto per) {
-    constexpr int kPer = decltype(per)::value;
-    if (dtype == MXQ_OUT_BF16)
-      route_backward_kernel<kPer, true><<<blocks, waves * 64, 0, s>>>(a);
-    else
-      route_backward_kernel<kPer, false><<<blocks, waves * 64, 0, s>>>(a);
+  by_launches(T, waves, [&](int64_t t, int64_t n, unsigned blocks) {
+    a.grad = grad_weights + t * K;
+    a.logits = static_cast<const char*>(logits) + t * ld_logits * esz;
+    a.ids = topk_ids + t * K;
+    a.T = n;
+    a.out = static_cast<char*>(grad_logits) + t * ld_grad * esz;
+    by_experts(E, [&](auto per) {
+      constexpr int kPer = decltype(per)::value;
+      if (dtype == MXQ_OUT_BF16)
+        route_backward_kernel<kPer, true><<<blocks, waves * 64, 0, s>>>(a);
+      else
+        route_backward_kernel<kPer, false><<<blocks, waves * 64, 0, s>>>(a);
+    });
   });
   return launch_status();
 }
