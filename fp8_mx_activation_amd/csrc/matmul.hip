@@ -792,7 +792,7 @@ template <int G, int NG, int OUT>
 mxq_status launch_small(const MatmulArgs& a, hipStream_t s) {
   const int nbo = a.act == kActSiluMul ? 32 * NG : 64 * NG;
   const int64_t bn = ceil_div(a.NO, nbo);
-  if (bn * a.E > INT32_MAX) return MXQ_ERR_UNSUPPORTED;
+  if (bn * a.E > max_blocks(256)) return MXQ_ERR_UNSUPPORTED;
   const int ld_xs = small_scale_ld(a.H / G);
   const int lds = kRingBytes + 16 * ld_xs + 3 * kMaxSteps;
   static_assert(kRingBytes >= 4 * 16 * (64 + 4) * 4 &&
@@ -815,7 +815,7 @@ mxq_status launch_tile(const MatmulArgs& a, hipStream_t s) {
   // every expert ends in at most one partial row tile
   const int64_t tm = a.num_rows / (64 * XF) + a.E;
   const int64_t blocks = ceil_div(tm * tn, 8) * 8;
-  if (blocks > INT32_MAX) return MXQ_ERR_UNSUPPORTED;
+  if (blocks > max_blocks(256)) return MXQ_ERR_UNSUPPORTED;
   constexpr int lds = tile_lds_bytes<XF>();
   auto* k = a.act == kActSiluMul ? &matmul_tile_kernel<G, XF, OUT, true>
                                  : &matmul_tile_kernel<G, XF, OUT, false>;

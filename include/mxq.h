@@ -27,7 +27,9 @@
  *     failed check returns MXQ_ERR_INVALID_ARGUMENT (or MXQ_ERR_UNSUPPORTED
  *     for a format or size the library does not implement, MXQ_ERR_WORKSPACE
  *     for a short workspace) and enqueues nothing.  MXQ_ERR_HIP means a kernel
- *     launch was rejected by the runtime.
+ *     launch was rejected by the runtime.  One launch holds 2^32 - 1 threads;
+ *     the router and the gradients take several where they need more, an
+ *     experts' product that does is MXQ_ERR_UNSUPPORTED.
  *   - Launch geometry depends only on the host arguments, never on device
  *     data, so every call can be captured in a hipGraph and replayed.
  *   - Row offsets are 64-bit internally; row indices stored in int32 arrays
