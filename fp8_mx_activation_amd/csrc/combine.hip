@@ -134,6 +134,7 @@ extern "C" mxq_status moe_combine(const void* y_bf16, int64_t ld_y,
                             : H;
   const dim3 grid((unsigned)T, (unsigned)ceil_div(H, slice));
   const int threads = row_block_threads(slice, 8);
+  if (T > max_blocks(threads)) return MXQ_ERR_UNSUPPORTED;
   hipStream_t s = as_stream(stream);
   const uint16_t* y = static_cast<const uint16_t*>(y_bf16);
   if (out_dtype == MXQ_OUT_F32)

@@ -110,6 +110,7 @@ extern "C" mxq_status mxq_gather_read16(const void* rows, int64_t ld,
       (num_rows > 0 && row_bytes > 0 && (rows == nullptr || !aligned16(rows))))
     return MXQ_ERR_INVALID_ARGUMENT;
   const int threads = row_block_threads(row_bytes > 0 ? row_bytes : 16, 16);
+  if (groups > max_blocks(threads)) return MXQ_ERR_UNSUPPORTED;
   gather_read16_kernel<<<(unsigned)groups, threads, 0, as_stream(stream)>>>(
       static_cast<const uint8_t*>(rows), ld, num_rows, idx, group, row_bytes,
       sink);
@@ -125,6 +126,7 @@ extern "C" mxq_status mxq_fill_rows16(void* dst, int64_t ld, int64_t rows,
   if (rows == 0 || row_bytes == 0) return MXQ_OK;
   if (dst == nullptr || !aligned16(dst)) return MXQ_ERR_INVALID_ARGUMENT;
   const int threads = row_block_threads(row_bytes, 16);
+  if (rows > max_blocks(threads)) return MXQ_ERR_UNSUPPORTED;
   fill_rows16_kernel<<<(unsigned)rows, threads, 0, as_stream(stream)>>>(
       static_cast<uint8_t*>(dst), ld, row_bytes, pattern);
   return launch_status();

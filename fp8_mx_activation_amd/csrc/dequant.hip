@@ -283,6 +283,7 @@ extern "C" mxq_status upscale_fp8_to_bf16(const void* q_fp8, int64_t ld_q,
       !aligned16(q_fp8) || !aligned16(out_bf16))
     return MXQ_ERR_INVALID_ARGUMENT;
   const int threads = row_block_threads(H, 16);
+  if (num_rows > max_blocks(threads)) return MXQ_ERR_UNSUPPORTED;
   hipStream_t s = as_stream(stream);
   const uint8_t* q = static_cast<const uint8_t*>(q_fp8);
   uint16_t* o = static_cast<uint16_t*>(out_bf16);
@@ -322,7 +323,7 @@ extern "C" mxq_status requant_weight_block_ue8m0(
     return MXQ_ERR_INVALID_ARGUMENT;
   const int64_t ntk = ceil_div(K, kWTileK);
   const int64_t blocks = (int64_t)num_matrices * nbn * ntk;
-  if (blocks > INT32_MAX) return MXQ_ERR_INVALID_ARGUMENT;
+  if (blocks > max_blocks(kWTileK)) return MXQ_ERR_UNSUPPORTED;
   weight_requant_kernel<kWTileK><<<(unsigned)blocks, kWTileK, 0,
                                    as_stream(stream)>>>(
       static_cast<const uint8_t*>(q_fp8), ld, matrix_stride, s_inv, s_ld,

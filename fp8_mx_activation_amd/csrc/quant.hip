@@ -424,6 +424,8 @@ mxq_status scatter_quant_impl(const void* x_bf16, int64_t ld_x, int64_t T,
   // 1024 threads: at most two tokens in flight per CU, which keeps the
   // number of concurrent destination-row write streams low.
   const int threads = 1024;
+  const int64_t most = max_blocks(threads);
+  if (T > (place == kMfma ? most / 8 * 8 : most)) return MXQ_ERR_UNSUPPORTED;
   const size_t lds = (size_t)H + (size_t)(H / G);
   hipStream_t s = as_stream(stream);
   const uint16_t* x = static_cast<const uint16_t*>(x_bf16);

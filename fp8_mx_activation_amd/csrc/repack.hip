@@ -546,6 +546,7 @@ extern "C" mxq_status moe_scatter_rows(
          (xs_row_stride | xs_col_stride | os_row_stride | os_col_stride) % 4))
       return MXQ_ERR_INVALID_ARGUMENT;
   }
+  if (T > max_blocks(kRowsThreads)) return MXQ_ERR_UNSUPPORTED;
   const size_t lds = (size_t)(row_bytes < kRowsChunk ? row_bytes : kRowsChunk);
   scatter_rows_kernel<<<(unsigned)T, kRowsThreads, lds, as_stream(stream)>>>(
       static_cast<const uint8_t*>(x), ld_x, row_bytes,

@@ -28,8 +28,8 @@
  *     for a format or size the library does not implement, MXQ_ERR_WORKSPACE
  *     for a short workspace) and enqueues nothing.  MXQ_ERR_HIP means a kernel
  *     launch was rejected by the runtime.  One launch holds 2^32 - 1 threads;
- *     the router and the gradients take several where they need more, an
- *     experts' product that does is MXQ_ERR_UNSUPPORTED.
+ *     the router and the gradients take several where they need more, any
+ *     other call that does is MXQ_ERR_UNSUPPORTED.
  *   - Launch geometry depends only on the host arguments, never on device
  *     data, so every call can be captured in a hipGraph and replayed.
  *   - Row offsets are 64-bit internally; row indices stored in int32 arrays
