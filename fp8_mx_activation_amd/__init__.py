@@ -1021,29 +1021,45 @@ def moe_scatter_rows_backward(grad_rows: torch.Tensor, src2dst: torch.Tensor,
 def moe_combine_backward(grad_out: torch.Tensor, y: torch.Tensor,
                          src2dst: torch.Tensor, topk_weights: torch.Tensor,
                          grad_y: torch.Tensor | None = None,
-                         grad_weights: torch.Tensor | None = None):
+                         grad_weights: torch.Tensor | None = None,
+                         need_grad_y: bool = True,
+                         need_grad_weights: bool = True):
     """Gradient of ``moe_combine(y, src2dst, topk_weights)`` for ``grad_out
     [T, H]`` (bf16 or float32): ``(grad_y bf16 [num_rows, H], grad_weights
     float32 [T, K])``.  Rows of ``grad_y`` that are no destination keep the
-    contents of a given ``grad_y``."""
+    contents of a given ``grad_y``.  A gradient that is not needed is None
+    and costs nothing: without ``grad_weights`` the rows of ``y`` are not
+    read, without ``grad_y`` none are written."""
+    if not (need_grad_y or need_grad_weights):
+        raise ValueError("need_grad_y or need_grad_weights must be set")
+    if (grad_y is not None and not need_grad_y) or \
+            (grad_weights is not None and not need_grad_weights):
+        raise ValueError("an output is given for a gradient not needed")
     g, T, H, ld_g = _matrix(grad_out, "grad_out", OUT_DTYPES)
     K = _src2dst(src2dst, grad_out, T)
     y_p, num_rows, cols, ld_y = _matrix(y, "y", _BF16, grad_out)
     if cols != H:
         raise ValueError("y must be [num_rows, %d]" % H)
     w = _dense(topk_weights, "topk_weights", torch.float32, (T, K), grad_out)
-    if grad_y is None:
-        grad_y = torch.empty((num_rows, H), dtype=torch.bfloat16,
-                             device=y.device)
-    gy, ld_gy = _output(grad_y, "grad_y", _BF16, num_rows, H, grad_out)
-    if grad_weights is None:
-        grad_weights = torch.empty((T, K), dtype=torch.float32,
-                                   device=y.device)
-    gw = _dense(grad_weights, "grad_weights", torch.float32, (T, K), grad_out)
-    if T and K:
+    gy, ld_gy, gw = None, 0, None
+    if need_grad_y:
+        if grad_y is None:
+            grad_y = torch.empty((num_rows, H), dtype=torch.bfloat16,
+                                 device=y.device)
+        gy, ld_gy = _output(grad_y, "grad_y", _BF16, num_rows, H, grad_out)
+    if need_grad_weights:
+        if grad_weights is None:
+            grad_weights = torch.empty((T, K), dtype=torch.float32,
+                                       device=y.device)
+        gw = _dense(grad_weights, "grad_weights", torch.float32, (T, K),
+                    grad_out)
+    # rows of grad_y alone have nothing to do where there are none
+    if T and K and (need_grad_weights or num_rows):
         _call("moe_combine_backward", grad_out, g,
-              OUT_DTYPES[grad_out.dtype], ld_g, y_p, ld_y, num_rows,
-              src2dst.data_ptr(), w, T, K, H, gy, ld_gy, gw)
+              OUT_DTYPES[grad_out.dtype], ld_g,
+              y_p if need_grad_weights else None, ld_y, num_rows,
+              src2dst.data_ptr(), w if need_grad_y else None, T, K, H, gy,
+              ld_gy, gw)
     return grad_y, grad_weights
 
 
