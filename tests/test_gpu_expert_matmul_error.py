@@ -103,8 +103,9 @@ def test_error_of_normal_rows(act, fmt):
             "bound %.2e" % (E.norm() / y.norm()).item())
         assert (off.abs() <= 8 * E + step).all()
         assert off.norm() <= E.norm() + step.norm()
-        # the figure that the documents state
-        assert rel <= 3e-4
+        # measured 1.5e-5 (gated 2.2e-5) for every kernel and format; equal
+        # calls give equal bytes
+        assert rel <= 3e-5
         # half a step of bf16 and 8 E without the residual
         out = mxq.moe_expert_matmul(**d, act=act, expected_m=hint).double()
         assert ((out - y).abs() <= 2.0 ** -8 * (y.abs() + 8 * E) +
