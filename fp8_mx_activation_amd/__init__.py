@@ -924,7 +924,10 @@ def moe_expert_matmul(q: torch.Tensor, scales: torch.Tensor, w: torch.Tensor,
     slab); ``bias`` is float32 [E, N], ``residual`` bf16 rows added after the
     activation.  Rows that hold no assignment keep the contents of a given
     ``out``.  ``expected_m``, the rows a busy expert is expected to hold,
-    picks the kernel's shape; by default num_rows / E."""
+    picks the kernel's shape.  The default, num_rows / E, counts a compact
+    layout's padding and a slab's whole capacity: give T * K / experts where
+    that is few (one token through 8 of 32 experts takes 52 us with it, 62
+    without)."""
     args, rows, cols, m = _matmul_inputs(q, scales, w, w_scales,
                                          expert_offsets, counts, fmt, act,
                                          bias, expected_m)

@@ -55,9 +55,10 @@ __device__ __forceinline__ ExpertRows expert_rows(const MatmulArgs& a, int e) {
 }
 
 // x / (1 + exp(-x)) with the hardware's power of two and reciprocal.  The
-// product -x log2(e) is rounded once, so exp(-x) is off by a factor of at most
-// 1 + (|x| + 2) 2^-24; beyond fp32's range it is 0 or infinity, and the
-// quotient x or -0.
+// product -x log2(e) is rounded once and the constant is 0.22 * 2^-24 of itself
+// off, so exp(-x) is off by a factor of at most 1 + (1.22 |x| + 2) 2^-24.  A
+// reciprocal below 2^-126 is 0, and so is the quotient from -87.4 down (where
+// it is above -2^-119).
 __device__ __forceinline__ float silu(float x) {
   constexpr float kLog2e = 1.44269504088896341f;
   return x * __builtin_amdgcn_rcpf(1.0f +

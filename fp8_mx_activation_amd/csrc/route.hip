@@ -15,20 +15,23 @@
 // Choice values are those of 64 bits wherever they come out of an exponential:
 // near a tie two experts' values lie closer than fp32 rounding, and the choice
 // would then hang on the rounding of exp.  They are first taken in 32 bits with
-// a bound on their error, which decides all but a token in a few hundred; such
-// a token is done again in 64 bits.  A softmax without bias or groups keeps the
-// order of its logits, so there the fp32 logits themselves are the keys and no
-// exponential is taken for the choice.  The weights are computed in 64 bits (at
-// most K exponentials per token, one per lane) and rounded once to fp32.
+// a bound on their error; a token that the bound does not decide (how many do
+// not hangs on the values, see choose_in_32_bits) is done again in 64 bits.  A
+// softmax without bias or groups keeps the order of its logits, so there the
+// fp32 logits themselves are the keys and no exponential is taken for the
+// choice.  The weights are computed in 64 bits (at most K exponentials per
+// token, one per lane) and rounded once to fp32.
 //
 // Bound: a row of E logits is 0.5-4 KB, so even 8192 tokens are one or two
 // microseconds of HBM time; the kernel is bound by the K dependent reductions
 // of one wavefront (some 65 instructions each).  Measured in a replayed graph,
 // launches included, 256 experts, top-8: softmax of bf16 logits 2.9 us for one
-// token, 6.7 for 8192, 36 for 65536 (3.3, 7.4 and 41 with whole 32-bit keys, as
-// for fp32); sigmoid with bias and 4 of 8 groups 5.0, 13-15 and 72 us
-// (5.5, 15.4 and 96 with 64-bit values throughout); their gradients 2.5, 6 and
-// 31 us (134 MB).  An empty kernel takes 2.1 us, a launch 4.2 us of host time.
+// token, 6.6 for 8192, 36 for 65536 (3.3, 7.4 and 41 with whole 32-bit keys, as
+// for fp32); sigmoid with bias and 4 of 8 groups 5.0, 13-15 and 72-75 us
+// (5.5, 15.4 and 96 with 64-bit values throughout); gradients of renormalized
+// weights or sigmoids 2.5, 6.1-6.6 and 32-33 us (fp32: 134 MB), of a plain
+// softmax over the whole row 3.0, 8.9-9.3 and 52-54 us.  An empty kernel takes
+// 2.1 us, a launch 4.2 us of host time.
 #include <algorithm>
 #include <type_traits>
 
@@ -372,8 +375,8 @@ __device__ __forceinline__ bool whole_lanes(int gs, int per) {
 }
 
 // The choice in 32 bits, where it is certain to be that of the 64-bit values:
-// false if two values that decide it lie too close (a token in a few hundred;
-// it then goes by 64 bits).  With u = 2^-24:
+// false if two values that decide it lie too close, and the token goes by 64
+// bits.  With u = 2^-24:
 //   - a sigmoid is off by less than 4 u (3 u of its own from the sum and the
 //     reciprocal, and s (1 - s) times the power's 2 u (|l| + 1)), a softmax by
 //     less than 53 u (1 u, and s times 46 u of the sum over the row and 5 u);
@@ -387,6 +390,15 @@ __device__ __forceinline__ bool whole_lanes(int gs, int per) {
 //     comes near 64 bits' smallest (exp(-700)).
 // Where a set is cut off (the groups, the K-th choice) the next one is
 // compared too.
+//
+// Tokens that go by 64 bits, by this rule over drawn rows of 256 experts, top-8:
+// sigmoid of normal logits of deviation 2 with a bias of deviation 0.3 and 4 of
+// 8 groups 0.15 %, with a bias of 0.01 1.3 %, without a bias 1.3 %; softmax of
+// the same logits with a bias of 0.3 0.05 %, of 0.001 1.3 %.  The margins do not
+// shrink with the scores, so flat rows mostly go by 64 bits (softmax of logits
+// of deviation 0.5 with a bias of 0.001: 13 %, 512 experts and top-10 35 %), and
+// so do saturated ones (sigmoid of logits of deviation 6 with a bias: nearly
+// all, for the largest scores round to one).
 template <int PER>
 __device__ __forceinline__ bool choose_in_32_bits(const RouteArgs& a, int lane,
                                                   const float (&l)[PER],

@@ -92,7 +92,7 @@ typedef enum { MXQ_OUT_BF16 = 0, MXQ_OUT_F32 = 1 } mxq_out_dtype;
 
 /* Activation of the experts' products.  MXQ_ACT_SILU_MUL takes the first
  * half of the N outputs as gate, the second as factor: silu(a[n]) *
- * a[N/2 + n], N/2 columns; silu(x) = x / (1 + exp(-x)). */
+ * a[N/2 + n], N/2 columns; silu(x) = x / (1 + exp(-x)), 0 below -87.4. */
 typedef enum {
   MXQ_ACT_NONE = 0,
   MXQ_ACT_SILU = 1,
@@ -467,9 +467,11 @@ mxq_status requant_per_token_to_per_tensor(
  *   residual        bf16 [num_rows, ld_r] or NULL; may be out itself (same
  *                   stride).
  *   expected_m      rows a busy expert is expected to hold (a host guess,
- *                   such as T * K / experts); it picks the kernel's shape.
- *                   Any value gives a right result; a different shape may
- *                   add in another order.
+ *                   such as T * K / experts); it picks the kernel's shape,
+ *                   that for few rows up to 12.  Any value gives a right
+ *                   result; a different shape may add in another order.  Too
+ *                   large a guess costs up to two fifths, too small a one
+ *                   3 times at 64 rows and more beyond.
  *   out             bf16 [num_rows, ld_out], N columns (N/2 for
  *                   MXQ_ACT_SILU_MUL), a multiple of 4.  Rows that are not
  *                   live are not written.
@@ -478,7 +480,7 @@ mxq_status requant_per_token_to_per_tensor(
  * num_rows <= MXQ_MAX_MATMUL_ROWS, ld_q and ld_s <= MXQ_MAX_MATMUL_LD, else
  * MXQ_ERR_UNSUPPORTED.  Sums are fp32, but for the matrix unit's own
  * 32-product groups, in which it drops what lies more than 13 bits below the
- * group's largest product.  Scale byte 255 and e4m3 NaN bytes in a live row
+ * group's largest product (sums of normal values keep 16 bits).  Scale byte 255 and e4m3 NaN bytes in a live row
  * or its expert's weights give NaN in what they enter. */
 mxq_status moe_expert_matmul(const void* q_fp8, int64_t ld_q,
                              const uint8_t* scales, int64_t ld_s,
