@@ -533,6 +533,9 @@ mxq_status live_args_ok(const void* x_bf16, int64_t ld_x,
   if (ld_x < H || ld_q < H) return MXQ_ERR_INVALID_ARGUMENT;
   if (!rows_ok_bf16(x_bf16, ld_x) || !rows_ok_u8(q_fp8, ld_q))
     return MXQ_ERR_INVALID_ARGUMENT;
+  // the row kernel has a block per segment at least
+  if (num_segments > max_blocks(row_block_threads(H, 16)))
+    return MXQ_ERR_UNSUPPORTED;
   *rows = n;
   return MXQ_OK;
 }

@@ -54,3 +54,9 @@ def test_weight_requant(lib):
         FAKE, 16, 16, FAKE, 1, 1, n, 1, 16, 128, 128, FAKE, FAKE, 1, 1,
         None) == UNSUPPORTED
 
+
+def test_live_rows_segments(lib):
+    """Above 1024 segments each has a block of its own."""
+    n, H = 1 << 22, 16384
+    assert lib.mx_quant_live_rows(FAKE, H, n, 1, FAKE, H, 1, FAKE, H, FAKE,
+                                  H // 32, None) == UNSUPPORTED
