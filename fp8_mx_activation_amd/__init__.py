@@ -1,6 +1,7 @@
 """MoE expert-dispatch preprocessing with fp8 e4m3 activations and
 power-of-two group scales, on MI355X (gfx950), with the router in front of
-it, the experts' products on its rows, and their gradients.
+it, its balance loss, the experts' products on its rows, and their gradients;
+rows and weights in microscaled 4-bit floats too.
 
 Thin Python binding over ``libmxq.so`` (declared in ``include/mxq.h``).  The
 functions carry the C names; they check tensor dtypes, shapes and devices,
@@ -11,7 +12,9 @@ call raises.
 
 Byte formats: fp8 payloads are ``torch.uint8`` tensors holding OCP e4m3fn
 bytes (``.view(torch.float8_e4m3fn)`` reinterprets them); a scale byte b
-means 2^(b - 127) (``.view(torch.float8_e8m0fnu)``).
+means 2^(b - 127) (``.view(torch.float8_e8m0fnu)``).  MXFP4 payloads are
+``torch.uint8`` too, two e2m1 codes to a byte, the lower channel in the lower
+half.
 """
 from __future__ import annotations
 
@@ -35,7 +38,11 @@ __all__ = [
     "mxq_gather_read16", "mxq_fill_rows16", "SCORE_FNS", "moe_route",
     "moe_route_backward", "moe_scatter_rows_backward",
     "moe_combine_backward", "ACTIVATIONS", "moe_expert_matmul",
-    "moe_expert_matmul_quant",
+    "moe_expert_matmul_quant", "moe_balance_loss_workspace_bytes",
+    "moe_balance_loss", "moe_balance_loss_backward", "MX_FORMATS",
+    "mxfp4_quant_rows", "moe_scatter_quant_mxfp4", "mxfp4_to_e4m3",
+    "upscale_mxfp4_to_bf16", "moe_expert_matmul_mxfp4",
+    "moe_expert_matmul_mxfp4_quant",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -47,6 +54,8 @@ MXQ_ERR_SCRATCH_LIMIT = 6
 LAYOUT_NOALLOC_SCRATCH_BYTES = 1 << 20
 LAYOUT_KINDS = {"compact": 0, "masked": 1}
 SCALE_FORMATS = {"ue8m0_g128": (0, 128), "e8m0_g32": (1, 32)}
+# rows of 32-channel scales: format, channels in a byte of payload
+MX_FORMATS = {"mxfp4": (2, 2), "e8m0_g32": (1, 1)}
 SCALE_RULES = {"no_clip": 0, "ocp_floor": 1}
 SCALE_LAYOUTS = ("rows", "packed_mn", "mfma32", "mfma16")
 OUT_DTYPES = {torch.bfloat16: 0, torch.float32: 1}
@@ -119,6 +128,26 @@ _SIGNATURES = {
     "moe_expert_matmul_quant": (_i32, [_p, _i64, _p, _i64, _i64, _i32, _p, _p,
                                        _i32, _i32, _i32, _p, _p, _p, _i32,
                                        _i64, _i32, _p, _i64, _p, _i64, _p]),
+    "moe_balance_loss_workspace_bytes": (_sz, [_i64, _i32, _i32]),
+    "moe_balance_loss": (_i32, [_p, _i32, _i64, _p, _i64, _i32, _i32, _i32, _p,
+                                _p, _i32, _p, _p, _p, _p, _p, _sz, _p]),
+    "moe_balance_loss_backward": (_i32, [_p, _p, _p, _i32, _i64, _p, _i64,
+                                         _i32, _i32, _p, _p, _i32, _p, _i64,
+                                         _p, _i64, _p]),
+    "mxfp4_quant_rows": (_i32, [_p, _i32, _i64, _i64, _i32, _i32, _p, _i64,
+                                _p, _i64, _p]),
+    "moe_scatter_quant_mxfp4": (_i32, [_p, _i64, _i64, _i32, _p, _i32, _i32,
+                                       _p, _i64, _p, _i64, _i64, _p]),
+    "mxfp4_to_e4m3": (_i32, [_p, _i64, _i64, _i32, _p, _i64, _p]),
+    "upscale_mxfp4_to_bf16": (_i32, [_p, _i64, _p, _i64, _i64, _i32, _p, _i64,
+                                     _p]),
+    "moe_expert_matmul_mxfp4": (_i32, [_p, _i64, _p, _i64, _i64, _i32, _p, _p,
+                                       _i64, _i32, _i32, _i32, _p, _p, _p,
+                                       _i32, _p, _i64, _i64, _p, _i64, _p]),
+    "moe_expert_matmul_mxfp4_quant": (_i32, [_p, _i64, _p, _i64, _i64, _i32,
+                                             _p, _p, _i64, _i32, _i32, _i32,
+                                             _p, _p, _p, _i32, _i64, _i32, _p,
+                                             _i64, _p, _i64, _p]),
     "mxq_status_string": (ctypes.c_char_p, [_i32]),
     "mxq_abi_version": (_i32, []),
 }
@@ -442,6 +471,118 @@ def moe_route_backward(grad_weights: torch.Tensor, logits: torch.Tensor,
     _call("moe_route_backward", logits, g, p, OUT_DTYPES[logits.dtype], ld,
           ids, T, E, K, SCORE_FNS[scoring], int(renormalize), weight_scale,
           out, ld_g)
+    return grad_logits
+
+
+def moe_balance_loss_workspace_bytes(T: int, E: int, S: int) -> int:
+    return int(lib().moe_balance_loss_workspace_bytes(T, E, S))
+
+
+def _sequences(seq_offsets, seq_lens, like):
+    """Pointers of the sequences' offsets and lengths, and their number."""
+    off = lens = None
+    S = 1
+    if seq_offsets is not None:
+        if seq_offsets.dim() != 1 or seq_offsets.shape[0] < 2:
+            raise ValueError("seq_offsets must be int32 [S + 1]")
+        S = seq_offsets.shape[0] - 1
+        off = _dense(seq_offsets, "seq_offsets", torch.int32, (S + 1,), like)
+    if seq_lens is not None:
+        lens = _dense(seq_lens, "seq_lens", torch.int32, (S,), like)
+    return off, lens, S
+
+
+def moe_balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor,
+                     scoring: str = "softmax",
+                     seq_offsets: torch.Tensor | None = None,
+                     seq_lens: torch.Tensor | None = None,
+                     z_loss: bool = False, out: dict | None = None,
+                     workspace: torch.Tensor | None = None) -> dict:
+    """Balance loss of a routing ``topk_ids [T, K]`` with its ``logits
+    [T, E]`` (bf16 or float32), for each of S sequences (see
+    ``moe_balance_loss`` in mxq.h): a dict with ``loss`` float32 [S],
+    ``counts`` int32 [S, E] (choices of every expert), ``probs`` float32
+    [S, E] (mean shares) and, with ``z_loss=True``, ``z_loss`` float32 [S].
+    ``seq_offsets`` (int32 [S + 1]) are the sequences' first tokens, S = 1
+    without; ``seq_lens`` (int32 [S]) how many of each are no padding.
+    ``out`` may hold preallocated tensors under the same keys."""
+    p, T, E, ld = _matrix(logits, "logits", OUT_DTYPES)
+    shape = topk_ids.shape
+    if len(shape) != 2:
+        raise ValueError("topk_ids must be int32 [T, K]")
+    K = shape[1]
+    ids = _dense(topk_ids, "topk_ids", torch.int32, (T, K), logits)
+    off, lens, S = _sequences(seq_offsets, seq_lens, logits)
+    res, ptr = {}, {}
+    given = out or {}
+    for key, dtype, size in (("loss", torch.float32, (S,)),
+                             ("counts", torch.int32, (S, E)),
+                             ("probs", torch.float32, (S, E)),
+                             ("z_loss", torch.float32, (S,))):
+        if key == "z_loss" and not z_loss:
+            continue
+        t = given.get(key)
+        if t is None:
+            t = torch.empty(size, dtype=dtype, device=logits.device)
+        ptr[key] = _dense(t, "out[%r]" % key, dtype, size, logits)
+        res[key] = t
+    need = lib().moe_balance_loss_workspace_bytes(T, E, S)
+    if workspace is None:
+        ws, size = None, 0
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8,
+                                    device=logits.device)
+            ws, size = workspace.data_ptr(), need
+    else:
+        _dev(workspace, "workspace", logits)
+        if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous uint8 tensor")
+        ws, size = workspace.data_ptr() or None, workspace.numel()
+    _call("moe_balance_loss", logits, p, OUT_DTYPES[logits.dtype], ld, ids, T,
+          E, K, SCORE_FNS[scoring], off, lens, S, ptr["loss"],
+          ptr.get("z_loss"), ptr["counts"], ptr["probs"], ws, size)
+    return res
+
+
+def moe_balance_loss_backward(grad_loss: torch.Tensor | None,
+                              logits: torch.Tensor,
+                              counts: torch.Tensor | None,
+                              scoring: str = "softmax",
+                              seq_offsets: torch.Tensor | None = None,
+                              seq_lens: torch.Tensor | None = None,
+                              grad_z: torch.Tensor | None = None,
+                              add: torch.Tensor | None = None,
+                              grad_logits: torch.Tensor | None = None
+                              ) -> torch.Tensor:
+    """Gradient of ``moe_balance_loss`` to its logits, the counts held fixed:
+    ``grad_logits [T, E]`` in the logits' dtype, for ``grad_loss`` and
+    ``grad_z`` (float32 [S], either may be None).  ``counts`` are the forward
+    call's, or sums of them over several ranks.  ``add [T, E]``, such as the
+    router's own gradient, is added before the result is rounded; it may be
+    ``grad_logits`` itself."""
+    p, T, E, ld = _matrix(logits, "logits", OUT_DTYPES)
+    dtype = (logits.dtype,)
+    off, lens, S = _sequences(seq_offsets, seq_lens, logits)
+    g = None if grad_loss is None else _dense(
+        grad_loss, "grad_loss", torch.float32, (S,), logits)
+    gz = None if grad_z is None else _dense(
+        grad_z, "grad_z", torch.float32, (S,), logits)
+    if grad_loss is None and grad_z is None:
+        raise ValueError("grad_loss or grad_z must be given")
+    c = None if counts is None else _dense(counts, "counts", torch.int32,
+                                           (S, E), logits)
+    a, ld_a = None, 0
+    if add is not None:
+        a, rows, cols, ld_a = _matrix(add, "add", dtype, logits)
+        if (rows, cols) != (T, E):
+            raise ValueError("add must be [%d, %d]" % (T, E))
+    if grad_logits is None:
+        grad_logits = torch.empty((T, E), dtype=logits.dtype,
+                                  device=logits.device)
+    out, ld_g = _output(grad_logits, "grad_logits", dtype, T, E, logits)
+    _call("moe_balance_loss_backward", logits, g, gz, p,
+          OUT_DTYPES[logits.dtype], ld, c, T, E, SCORE_FNS[scoring], off,
+          lens, S, a, ld_a, out, ld_g)
     return grad_logits
 
 
@@ -966,6 +1107,197 @@ def moe_expert_matmul_quant(q: torch.Tensor, scales: torch.Tensor,
     o, ld_o = _output(q_out, "q_out", _FP8, rows, cols, q)
     so, ld_so = _output(scales_out, "scales_out", _SCALE, rows, cols // G, q)
     _call("moe_expert_matmul_quant", q, *args, m, code, o, ld_o, so, ld_so)
+    return q_out, scales_out
+
+
+# ------------------------------------------- microscaled 4-bit floats
+
+_BYTES = (torch.uint8,) + ((torch.float4_e2m1fn_x2,)
+                           if hasattr(torch, "float4_e2m1fn_x2") else ())
+
+
+def _flat_rows(t: torch.Tensor, name: str) -> torch.Tensor:
+    """Weights [E, N, C] as rows [E * N, C] of the same memory."""
+    if t.dim() != 3:
+        return t
+    try:
+        return t.view(t.shape[0] * t.shape[1], t.shape[2])
+    except RuntimeError:
+        raise ValueError("the matrices of %s must follow one another"
+                         % name) from None
+
+
+def mxfp4_quant_rows(x: torch.Tensor, rule: str = "no_clip",
+                     q: torch.Tensor | None = None,
+                     scales: torch.Tensor | None = None):
+    """Rows of ``x`` ([rows, H] or weights [E, N, H], bf16 or float32) to
+    MXFP4: ``(q [..., H/2] uint8, scales [..., H/32] uint8)``, H a multiple of
+    32.  ``rule`` is ``"no_clip"`` or ``"ocp_floor"`` (see
+    ``mxfp4_quant_rows`` in mxq.h).  Rows of scales allocated here start on 16
+    bytes (a view of a padded buffer where H/32 is no multiple of 16), as
+    ``moe_expert_matmul_mxfp4`` takes them."""
+    lead = x.shape[:-1]
+    p, rows, H, ld = _matrix(_flat_rows(x, "x"), "x", OUT_DTYPES)
+    if q is None:
+        q = torch.empty(lead + (H // 2,), dtype=torch.uint8, device=x.device)
+    if scales is None:
+        scales = _empty_rows_u8(rows, H // 32, x.device)
+        if len(lead) == 2:
+            scales = scales.unflatten(0, lead)
+    o, ld_q = _output(_flat_rows(q, "q"), "q", _BYTES, rows, H // 2, x)
+    so, ld_s = _output(_flat_rows(scales, "scales"), "scales", _SCALE, rows,
+                       H // 32, x)
+    _call("mxfp4_quant_rows", x, p, OUT_DTYPES[x.dtype], ld, rows, H,
+          SCALE_RULES[rule], o, ld_q, so, ld_s)
+    return q, scales
+
+
+def moe_scatter_quant_mxfp4(x: torch.Tensor, src2dst: torch.Tensor,
+                            num_rows: int, rule: str = "no_clip",
+                            q: torch.Tensor | None = None,
+                            scales: torch.Tensor | None = None):
+    """``moe_scatter_quant`` with MXFP4 rows: ``(q [num_rows, H/2] uint8,
+    scales [num_rows, H/32] uint8)``; rows that are no destination keep the
+    contents of a given ``q`` / ``scales``."""
+    p, T, H, ld = _matrix(x, "x", _BF16)
+    K = _src2dst(src2dst, x, T)
+    if q is None:
+        q = torch.empty((num_rows, H // 2), dtype=torch.uint8, device=x.device)
+    if scales is None:
+        scales = torch.empty((num_rows, H // 32), dtype=torch.uint8,
+                             device=x.device)
+    o, ld_q = _output(q, "q", _BYTES, num_rows, H // 2, x)
+    so, ld_s = _output(scales, "scales", _SCALE, num_rows, H // 32, x)
+    _call("moe_scatter_quant_mxfp4", x, p, ld, T, H,
+          src2dst.data_ptr() or None, K, SCALE_RULES[rule], o, ld_q, so, ld_s,
+          num_rows)
+    return q, scales
+
+
+def mxfp4_to_e4m3(q: torch.Tensor, out: torch.Tensor | None = None
+                  ) -> torch.Tensor:
+    """MXFP4 payloads ``q [rows, H/2]`` as e4m3 bytes ``out [rows, H]`` of
+    the same values: with the same scales, rows of ``"e8m0_g32"``."""
+    p, rows, cols, ld = _matrix(q, "q", _BYTES)
+    if out is None:
+        out = torch.empty((rows, 2 * cols), dtype=torch.uint8, device=q.device)
+    o, ld_o = _output(out, "out", _FP8, rows, 2 * cols, q)
+    _call("mxfp4_to_e4m3", q, p, ld, rows, 2 * cols, o, ld_o)
+    return out
+
+
+def upscale_mxfp4_to_bf16(q: torch.Tensor, scales: torch.Tensor,
+                          num_rows: int | None = None,
+                          out: torch.Tensor | None = None) -> torch.Tensor:
+    """MXFP4 rows to bf16 ``out [rows, H]`` for the first ``num_rows`` rows;
+    the others keep the contents of a given ``out``."""
+    p, rows, cols, ld = _matrix(q, "q", _BYTES)
+    n = rows if num_rows is None else int(num_rows)
+    if not 0 <= n <= rows:
+        raise ValueError("num_rows out of range")
+    H = 2 * cols
+    s, ld_s = _output(scales, "scales", _SCALE, n, H // 32, q)
+    if out is None:
+        out = torch.empty((rows, H), dtype=torch.bfloat16, device=q.device)
+    o, ld_o = _output(out, "out", _BF16, n, H, q)
+    _call("upscale_mxfp4_to_bf16", q, p, ld, s, ld_s, n, H, o, ld_o)
+    return out
+
+
+def _matmul4_inputs(q, scales, w, w_scales, expert_offsets, counts, fmt, act,
+                    bias, expected_m):
+    """``_matmul_inputs`` for weights in MXFP4."""
+    code, per_byte = MX_FORMATS[fmt]
+    q_p, rows, cols, ld_q = _matrix(q, "q", _BYTES if per_byte == 2 else _FP8)
+    H = cols * per_byte
+    s_p, ld_s = _output(scales, "scales", _SCALE, rows, H // 32, q)
+    _dev(w, "w", q)
+    shape = w.shape
+    if w.dtype not in _BYTES or len(shape) != 3 or shape[2] != H // 2 or \
+            not w.is_contiguous():
+        raise ValueError("w must be contiguous MXFP4 [E, N, %d]" % (H // 2))
+    E, N, _ = shape
+    _dev(w_scales, "w_scales", q)
+    groups = H // 32
+    if w_scales.dtype not in _SCALE or w_scales.shape != (E, N, groups):
+        raise ValueError("w_scales must be uint8 %s" % ([E, N, groups],))
+    # rows start on 4 bytes and are read to the end of the last 4
+    ld_e, ld_ws, step = w_scales.stride()
+    if N == 1:
+        ld_ws = ld_e if E > 1 else -(-groups // 4) * 4
+    last = (E * N - 1) * ld_ws + -(-groups // 4) * 4
+    if ld_ws % 4 or ld_ws < groups or (groups > 1 and step != 1) or \
+            (E > 1 and ld_e != N * ld_ws) or w_scales.data_ptr() % 4 or \
+            w_scales.storage_offset() + last > \
+            w_scales.untyped_storage().nbytes():
+        raise ValueError("rows of w_scales must follow one another at a "
+                         "stride that is a multiple of 4 bytes, all of which "
+                         "are there (as mxfp4_quant_rows returns them)")
+    off = _dense(expert_offsets, "expert_offsets", torch.int32, (E + 1,), q)
+    cnt = _dense(counts, "counts", torch.int32, (E,), q)
+    b = None if bias is None else _dense(bias, "bias", torch.float32, (E, N),
+                                         q)
+    if expected_m is None:
+        expected_m = -(-rows // E) if E else 0
+    args = (q_p, ld_q, s_p, ld_s, rows, code, w.data_ptr() or None,
+            w_scales.data_ptr() or None, ld_ws, E, N, H, off, cnt, b,
+            ACTIVATIONS[act])
+    return args, rows, N // 2 if act == "silu_mul" else N, expected_m
+
+
+def moe_expert_matmul_mxfp4(q: torch.Tensor, scales: torch.Tensor,
+                            w: torch.Tensor, w_scales: torch.Tensor,
+                            expert_offsets: torch.Tensor,
+                            counts: torch.Tensor, fmt: str = "mxfp4",
+                            act: str = "none",
+                            bias: torch.Tensor | None = None,
+                            residual: torch.Tensor | None = None,
+                            out: torch.Tensor | None = None,
+                            expected_m: int | None = None) -> torch.Tensor:
+    """``moe_expert_matmul`` with weights in MXFP4 (``w [E, N, H/2]`` and
+    ``w_scales [E, N, H/32]`` as ``mxfp4_quant_rows`` returns them) and rows
+    in MXFP4 (``fmt="mxfp4"``: ``q [num_rows, H/2]``) or e4m3
+    (``"e8m0_g32"``: ``q [num_rows, H]``)."""
+    args, rows, cols, m = _matmul4_inputs(q, scales, w, w_scales,
+                                          expert_offsets, counts, fmt, act,
+                                          bias, expected_m)
+    res, ld_r = None, 0
+    if residual is not None:
+        res, ld_r = _output(residual, "residual", _BF16, rows, cols, q)
+    if out is None:
+        out = torch.empty((rows, cols), dtype=torch.bfloat16, device=q.device)
+    o, ld_o = _output(out, "out", _BF16, rows, cols, q)
+    _call("moe_expert_matmul_mxfp4", q, *args, res, ld_r, m, o, ld_o)
+    return out
+
+
+def moe_expert_matmul_mxfp4_quant(q: torch.Tensor, scales: torch.Tensor,
+                                  w: torch.Tensor, w_scales: torch.Tensor,
+                                  expert_offsets: torch.Tensor,
+                                  counts: torch.Tensor, fmt: str = "mxfp4",
+                                  act: str = "silu_mul",
+                                  bias: torch.Tensor | None = None,
+                                  out_fmt: str = "mxfp4",
+                                  q_out: torch.Tensor | None = None,
+                                  scales_out: torch.Tensor | None = None,
+                                  expected_m: int | None = None):
+    """``moe_expert_matmul_mxfp4`` with its rows quantized for the next
+    product: ``(q_out, scales_out)`` in ``out_fmt`` (``"mxfp4"`` or
+    ``"e8m0_g32"``), from the fp32 values."""
+    args, rows, cols, m = _matmul4_inputs(q, scales, w, w_scales,
+                                          expert_offsets, counts, fmt, act,
+                                          bias, expected_m)
+    code, per_byte = MX_FORMATS[out_fmt]
+    if q_out is None:
+        q_out = _empty_rows_u8(rows, cols // per_byte, q.device)
+    if scales_out is None:
+        scales_out = torch.empty((rows, cols // 32), dtype=torch.uint8,
+                                 device=q.device)
+    o, ld_o = _output(q_out, "q_out", _BYTES if per_byte == 2 else _FP8, rows,
+                      cols // per_byte, q)
+    so, ld_so = _output(scales_out, "scales_out", _SCALE, rows, cols // 32, q)
+    _call("moe_expert_matmul_mxfp4_quant", q, *args, m, code, o, ld_o, so,
+          ld_so)
     return q_out, scales_out
 
 

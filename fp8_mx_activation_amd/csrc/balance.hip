@@ -1,0 +1,749 @@
+// moe_balance_loss, moe_balance_loss_backward: the router's balance loss per
+// sequence, its log-sum-exp penalty, and their gradient to the logits.
+//
+//   p_te  = softmax(l_t)_e, or sigmoid(l_te) over the row's sum of them
+//   P_e   = mean of p_te over the sequence's n tokens
+//   loss  = E sum_e (c_e / sum_j c_j) P_e       c_e: the sequence's choices of e
+//   z     = mean of (log sum_e exp l_te)^2
+//   dl_te = grad E / (n sum_j c_j) p_te (c_e - sum_j p_tj c_j)
+//           (times 1 - sigmoid(l_te) for sigmoid scores)
+//           + grad_z 2 / n lse_t softmax(l_t)_e
+//
+// A row of E logits is held by L lanes, PER neighbouring experts each, so a
+// wavefront works on 64 / L tokens at once and a row's maximum and sums are
+// log2 L steps of DPP.  Sums over tokens stay in registers, one per expert,
+// until a block is through its share of a sequence; no float atomics, so equal
+// calls give equal bytes.  Choices are counted in LDS in whole numbers.
+#include <type_traits>
+
+#include "mxq_host.hpp"
+#include "route_device.hpp"
+
+namespace {
+
+using namespace mxq;
+
+// ------------------------------------------------ reductions over L lanes
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t paired(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF,
+                                               false);
+}
+
+// f over groups of L neighbouring lanes (a power of two from 4 on), for every
+// lane of a group: quad permutes, mirrors of 8 and 16 lanes, and swaps of rows.
+template <int L, typename F>
+__device__ __forceinline__ uint32_t over_group(uint32_t v, F f) {
+  v = f(v, paired<0xB1>(v));
+  v = f(v, paired<0x4E>(v));
+  if constexpr (L >= 8) v = f(v, paired<0x141>(v));
+  if constexpr (L >= 16) v = f(v, paired<0x140>(v));
+  if constexpr (L >= 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = f(r[0], r[1]);
+  }
+  if constexpr (L >= 64) {
+    const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    v = f(r[0], r[1]);
+  }
+  return v;
+}
+
+template <int L>
+__device__ __forceinline__ float group_sum(float v) {
+  return __uint_as_float(
+      over_group<L>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+        return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+      }));
+}
+
+template <int L>
+__device__ __forceinline__ float group_maxf(float v) {
+  return __uint_as_float(
+      over_group<L>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
+        return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+      }));
+}
+
+template <int L>
+__device__ __forceinline__ int group_maxi(int v) {
+  return (int)over_group<L>((uint32_t)v, [](uint32_t a, uint32_t b) {
+    return (uint32_t)max((int)a, (int)b);
+  });
+}
+
+// ------------------------------------------------------------- one row
+
+constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kLn2 = 0.693147180559945309f;
+
+// exp(x) for x <= 0.  The product with log2(e) is rounded once: exp is off by
+// a factor of at most 1 + (1.3 |x| + 2) 2^-24, which is little where it is not
+// tiny.
+__device__ __forceinline__ float exp_neg(float x) {
+  return __builtin_amdgcn_exp2f(x * kLog2e);
+}
+
+template <int PER>
+struct Row {
+  float p[PER];     // shares: softmax, or sigmoids over their sum
+  float back[PER];  // 1 - sigmoid
+  float soft[PER];  // softmax of a sigmoid router, where z is wanted
+  float top;        // largest logit
+  float lse;        // log-sum-exp, 0 of a row without a live logit
+};
+
+// Sigmoids are taken times exp(-min(top, 0)): their shares are right also
+// where the sigmoids themselves are too small for fp32.
+template <int L, int PER, bool SIGMOID, bool Z>
+__device__ __forceinline__ void row_shares(const float (&l)[PER],
+                                           Row<PER>& r) {
+  float m = l[0];
+#pragma unroll
+  for (int i = 1; i < PER; ++i) m = fmaxf(m, l[i]);
+  m = group_maxf<L>(m);
+  r.top = m;
+  m = fmaxf(m, -kFltMax);  // no live logit: every share is 0
+  float x[PER], total = 0.0f;
+  if (!SIGMOID || Z) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      x[i] = exp_neg(l[i] - m);
+      total += x[i];
+    }
+    total = group_sum<L>(total);
+    const float inv = total > 0.0f ? 1.0f / total : 0.0f;
+    if (Z)
+      r.lse = total > 0.0f
+                  ? m + kLn2 * __builtin_amdgcn_logf(total) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) (SIGMOID ? r.soft : r.p)[i] = x[i] * inv;
+  }
+  if (SIGMOID) {
+    const float m0 = fminf(m, 0.0f);
+    total = 0.0f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const float a = exp_neg(-fabsf(l[i]));
+      const float q = __builtin_amdgcn_rcpf(1.0f + a);
+      const bool pos = l[i] > 0.0f;
+      r.back[i] = (pos ? a : 1.0f) * q;
+      x[i] = (pos ? 1.0f : exp_neg(l[i] - m0)) * q;
+      total += x[i];
+    }
+    total = group_sum<L>(total);
+    const float inv = total > 0.0f ? 1.0f / total : 0.0f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) r.p[i] = x[i] * inv;
+  }
+}
+
+// ------------------------------------------------------------- sequences
+
+struct BalanceArgs {
+  const void* logits;
+  int64_t ld;
+  const int32_t* ids;  // [T, K]
+  int64_t T;
+  int32_t E, K, S;
+  const int32_t* offsets;  // [S + 1] or null
+  const int32_t* lens;     // [S] or null
+  int32_t vec;
+  float* loss;      // [S]
+  float* z;         // [S] or null
+  int32_t* counts;  // [S, E]
+  float* probs;     // [S, E]
+  // two launches: a block's sums of the tokens it has of a sequence
+  int64_t chunk;  // tokens per block
+  int32_t epad;   // columns of a row of sums
+  float* part_p;  // [blocks + S][epad]
+  int32_t* part_c;
+  float* part_z;  // [blocks + S]
+  double* piece;  // [S][column blocks][2]
+  uint32_t* done;  // [S]
+};
+
+// First token and number of tokens of sequence s, inside the batch whatever
+// the device data say.
+struct Tokens {
+  int64_t first, count;
+};
+
+__device__ __forceinline__ Tokens sequence(const int32_t* offsets,
+                                           const int32_t* lens, int64_t T,
+                                           int s) {
+  if (offsets == nullptr) {
+    const int64_t n = lens == nullptr ? T : min(T, (int64_t)max(lens[s], 0));
+    return Tokens{0, n};
+  }
+  const int64_t first = min(T, (int64_t)max(offsets[s], 0));
+  const int64_t end = min(T, (int64_t)max(offsets[s + 1], 0));
+  int64_t n = max(end - first, (int64_t)0);
+  if (lens != nullptr) n = min(n, (int64_t)max(lens[s], 0));
+  return Tokens{first, n};
+}
+
+// ------------------------------------------------------------- forward
+
+constexpr int kWaves = 8;
+constexpr int kThreads = kWaves * 64;
+
+// Sums over tokens [lo, hi) by one block: shares into sum[e], choices into
+// cnt[e], squared log-sum-exps into the return value (of every thread).
+template <int L, int PER, bool BF16, bool SIGMOID, bool Z>
+__device__ __forceinline__ float block_sums(const BalanceArgs& a, int64_t lo,
+                                            int64_t hi, float* sum /*[waves]
+                                            [L * PER]*/, int32_t* cnt,
+                                            float* zsum /*[waves]*/) {
+  constexpr int TG = 64 / L, W = L * PER, kSlots = kWaves * TG;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int e0 = (lane & (L - 1)) * PER;
+  for (int i = threadIdx.x; i < W; i += kThreads) cnt[i] = 0;
+  __syncthreads();
+  for (int64_t i = lo * a.K + threadIdx.x; i < hi * a.K; i += kThreads) {
+    const int id = a.ids[i];
+    if (id >= 0 && id < a.E) atomicAdd(&cnt[id], 1);
+  }
+  float acc[PER], zacc = 0.0f;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) acc[i] = 0.0f;
+  for (int64_t t0 = lo + wave * TG; t0 < hi; t0 += kSlots) {
+    const int64_t t = t0 + lane / L;
+    float l[PER];
+    load_logits<PER, BF16>(static_cast<const char*>(a.logits) +
+                               min(t, hi - 1) * a.ld * (BF16 ? 2 : 4),
+                           a.E, e0, a.vec != 0, l);
+    if (t >= hi) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) l[i] = -__builtin_inff();
+    }
+    Row<PER> r;
+    row_shares<L, PER, SIGMOID, Z>(l, r);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) acc[i] += r.p[i];
+    if (Z) zacc += r.lse * r.lse;
+  }
+  // tokens of a wavefront, then wavefronts
+#pragma unroll
+  for (int d = L; d < 64; d <<= 1) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) acc[i] += __shfl_xor(acc[i], d);
+    if (Z) zacc += __shfl_xor(zacc, d);
+  }
+  if (lane < L) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) sum[wave * W + e0 + i] = acc[i];
+  }
+  if (Z && lane == 0) zsum[wave] = zacc;
+  __syncthreads();
+  for (int e = threadIdx.x; e < W; e += kThreads) {
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) v += sum[w * W + e];
+    sum[e] = v;  // column e is this thread's alone
+  }
+  float z = 0.0f;
+  if (Z) {
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) z += zsum[w];
+  }
+  __syncthreads();
+  return z;
+}
+
+// One launch: block s has the whole of sequence s.
+template <int L, int PER, bool BF16, bool SIGMOID, bool Z>
+__global__ __launch_bounds__(kThreads) void balance_whole_kernel(
+    BalanceArgs a) {
+  constexpr int W = L * PER;
+  __shared__ float sum[kWaves * W];
+  __shared__ int32_t cnt[W];
+  __shared__ float zsum[kWaves];
+  __shared__ double red[2][kWaves];
+  const int s = blockIdx.x;
+  const Tokens q = sequence(a.offsets, a.lens, a.T, s);
+  const float z = block_sums<L, PER, BF16, SIGMOID, Z>(
+      a, q.first, q.first + q.count, sum, cnt, zsum);
+  const double inv = q.count > 0 ? 1.0 / (double)q.count : 0.0;
+  double dot = 0.0, total = 0.0;
+  for (int e = threadIdx.x; e < a.E; e += kThreads) {
+    const double p = sum[e] * inv;
+    a.probs[(int64_t)s * a.E + e] = (float)p;
+    a.counts[(int64_t)s * a.E + e] = cnt[e];
+    dot += p * cnt[e];
+    total += cnt[e];
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    dot += __shfl_xor(dot, d);
+    total += __shfl_xor(total, d);
+  }
+  if ((threadIdx.x & 63) == 0) {
+    red[0][threadIdx.x >> 6] = dot;
+    red[1][threadIdx.x >> 6] = total;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    dot = total = 0.0;
+    for (int w = 0; w < kWaves; ++w) {
+      dot += red[0][w];
+      total += red[1][w];
+    }
+    a.loss[s] = total > 0.0 ? (float)(a.E * dot / total) : 0.0f;
+    if (Z) a.z[s] = (float)(z * inv);
+  }
+}
+
+// First of two launches: block b has tokens [b * chunk, (b + 1) * chunk) and
+// leaves a row of sums for each sequence that it has tokens of.  Block and
+// sequence only go up from one such row to the next, so row b + s belongs to
+// this pair alone.
+template <int L, int PER, bool BF16, bool SIGMOID, bool Z>
+__global__ __launch_bounds__(kThreads) void balance_part_kernel(
+    BalanceArgs a) {
+  constexpr int W = L * PER;
+  __shared__ float sum[kWaves * W];
+  __shared__ int32_t cnt[W];
+  __shared__ float zsum[kWaves];
+  const int64_t from = blockIdx.x * a.chunk;
+  const int64_t to = min(from + a.chunk, a.T);
+  if (blockIdx.x == 0)
+    for (int s = threadIdx.x; s < a.S; s += kThreads) a.done[s] = 0;
+  __shared__ uint64_t has[kWaves];
+  for (int base = 0; base < a.S; base += kThreads) {
+    // which of the next sequences have tokens here
+    const int mine = base + (int)threadIdx.x;
+    const Tokens m = sequence(a.offsets, a.lens, a.T, min(mine, a.S - 1));
+    const uint64_t b = __ballot(mine < a.S && max(from, m.first) <
+                                                  min(to, m.first + m.count));
+    if ((threadIdx.x & 63) == 0) has[threadIdx.x >> 6] = b;
+    __syncthreads();
+    for (int w = 0; w < kWaves; ++w) {
+      for (uint64_t left = has[w]; left != 0; left &= left - 1) {
+        const int s = base + w * 64 + __ffsll((unsigned long long)left) - 1;
+        const Tokens q = sequence(a.offsets, a.lens, a.T, s);
+        const float z = block_sums<L, PER, BF16, SIGMOID, Z>(
+            a, max(from, q.first), min(to, q.first + q.count), sum, cnt, zsum);
+        const int64_t row = (int64_t)blockIdx.x + s;
+        for (int e = threadIdx.x; e < a.E; e += kThreads) {
+          a.part_p[row * a.epad + e] = sum[e];
+          a.part_c[row * a.epad + e] = cnt[e];
+        }
+        if (Z && threadIdx.x == 0) a.part_z[row] = z;
+        __syncthreads();
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// Second: a block joins 32 experts' sums of one sequence, in a fixed order; the
+// last block of a sequence joins what they add to its loss.
+constexpr int kCols = 32;
+constexpr int kJoinThreads = 256;
+
+__global__ __launch_bounds__(kJoinThreads) void balance_join_kernel(
+    BalanceArgs a, int32_t ncol) {
+  __shared__ double p[kJoinThreads / 8][kCols];
+  __shared__ int32_t c[kJoinThreads / 8][kCols];
+  __shared__ double zs[kJoinThreads];
+  const int s = blockIdx.x / ncol, j = blockIdx.x % ncol;
+  const Tokens q = sequence(a.offsets, a.lens, a.T, s);
+  const int r = threadIdx.x >> 3, c4 = (threadIdx.x & 7) * 4;
+  double v[4] = {0.0, 0.0, 0.0, 0.0}, z = 0.0;
+  int32_t n[4] = {0, 0, 0, 0};
+  if (q.count > 0) {
+    const int64_t b0 = q.first / a.chunk;
+    const int64_t b1 = (q.first + q.count - 1) / a.chunk;
+    for (int64_t b = b0 + r; b <= b1; b += kJoinThreads / 8) {
+      const int64_t at = (b + s) * a.epad + j * kCols + c4;
+      const float4 x = *reinterpret_cast<const float4*>(a.part_p + at);
+      const int4 k = *reinterpret_cast<const int4*>(a.part_c + at);
+      v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+      n[0] += k.x; n[1] += k.y; n[2] += k.z; n[3] += k.w;
+    }
+    if (a.z != nullptr && j == 0)
+      for (int64_t b = b0 + threadIdx.x; b <= b1; b += kJoinThreads)
+        z += a.part_z[b + s];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    p[r][c4 + i] = v[i];
+    c[r][c4 + i] = n[i];
+  }
+  zs[threadIdx.x] = z;
+  __syncthreads();
+  if (threadIdx.x >= 64) return;
+  const double inv = q.count > 0 ? 1.0 / (double)q.count : 0.0;
+  double dot = 0.0, total = 0.0;
+  z = 0.0;
+  const int e = j * kCols + (int)threadIdx.x;
+  if (threadIdx.x < kCols && e < a.E) {
+    double sum = 0.0;
+    int32_t k = 0;
+    for (int i = 0; i < kJoinThreads / 8; ++i) {
+      sum += p[i][threadIdx.x];
+      k += c[i][threadIdx.x];
+    }
+    sum *= inv;
+    a.probs[(int64_t)s * a.E + e] = (float)sum;
+    a.counts[(int64_t)s * a.E + e] = k;
+    dot = sum * k;
+    total = k;
+  }
+#pragma unroll
+  for (int i = 0; i < kJoinThreads / 64; ++i) z += zs[i * 64 + threadIdx.x];
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    dot += __shfl_xor(dot, d);
+    total += __shfl_xor(total, d);
+    z += __shfl_xor(z, d);
+  }
+  if (threadIdx.x != 0) return;
+  if (a.z != nullptr && j == 0) a.z[s] = (float)(z * inv);
+  if (ncol > 1) {
+    double* piece = a.piece + (int64_t)s * ncol * 2;
+    __hip_atomic_store(piece + 2 * j, dot, __ATOMIC_RELAXED,
+                       __HIP_MEMORY_SCOPE_AGENT);
+    __hip_atomic_store(piece + 2 * j + 1, total, __ATOMIC_RELAXED,
+                       __HIP_MEMORY_SCOPE_AGENT);
+    const uint32_t before =
+        __hip_atomic_fetch_add(a.done + s, 1u, __ATOMIC_ACQ_REL,
+                               __HIP_MEMORY_SCOPE_AGENT);
+    if (before + 1 != (uint32_t)ncol) return;
+    dot = total = 0.0;
+    for (int i = 0; i < ncol; ++i) {
+      dot += __hip_atomic_load(piece + 2 * i, __ATOMIC_RELAXED,
+                               __HIP_MEMORY_SCOPE_AGENT);
+      total += __hip_atomic_load(piece + 2 * i + 1, __ATOMIC_RELAXED,
+                                 __HIP_MEMORY_SCOPE_AGENT);
+    }
+  }
+  a.loss[s] = total > 0.0 ? (float)(a.E * dot / total) : 0.0f;
+}
+
+// ------------------------------------------------------------- backward
+
+struct BalanceBackArgs {
+  const float* grad;    // [S] or null
+  const float* grad_z;  // [S] or null
+  const void* logits;
+  int64_t ld;
+  const int32_t* counts;  // [S, E]
+  int64_t T;
+  int32_t E, S;
+  const int32_t* offsets;
+  const int32_t* lens;
+  const void* add;  // [T, ld_add] or null
+  int64_t ld_add;
+  int32_t vec, vec_add, vec_out;
+  void* out;
+  int64_t ld_out;
+  int64_t chunk;  // tokens per block
+};
+
+constexpr int kBackWaves = 4;
+
+// Counts enter as their differences to the largest logit's expert: the shares
+// add up to one, so that takes nothing away, and where one share is nearly all
+// of it the others' keep their bits.
+template <int L, int PER, bool BF16, bool SIGMOID, bool Z>
+__global__ __launch_bounds__(kBackWaves * 64) void balance_backward_kernel(
+    BalanceBackArgs a) {
+  constexpr int TG = 64 / L, kSlots = kBackWaves * TG;
+  constexpr int kSize = BF16 ? 2 : 4;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int e0 = (lane & (L - 1)) * PER, gid = lane / L;
+  const int64_t from = blockIdx.x * a.chunk;
+  const int64_t to = min(from + a.chunk, a.T);
+  int have = -1;  // the sequence whose counts and factors these are
+  int c[PER];
+  float coef = 0.0f, zcoef = 0.0f;
+  Tokens q{0, 0};
+#pragma unroll
+  for (int i = 0; i < PER; ++i) c[i] = 0;
+  for (int64_t tw = from + wave * TG; tw < to; tw += kSlots) {
+    const int64_t t = tw + gid;
+    const int64_t tc = min(t, to - 1);
+    float l[PER], add[PER];
+    load_logits<PER, BF16>(static_cast<const char*>(a.logits) +
+                               tc * a.ld * kSize,
+                           a.E, e0, a.vec != 0, l);
+    if (a.add != nullptr) {
+      load_row<PER, BF16>(static_cast<const char*>(a.add) +
+                              tc * a.ld_add * kSize,
+                          a.E, e0, a.vec_add != 0, add);
+    } else {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) add[i] = 0.0f;
+    }
+    int s = 0;
+    if (a.offsets != nullptr) {
+      // as many sequences as end at or before the token
+      for (int base = 0; base < a.S; base += 64) {
+        const int i = base + lane;
+        const int64_t end = a.offsets[min(i, a.S - 1) + 1];
+#pragma unroll
+        for (int g = 0; g < TG; ++g) {
+          const int n = __popcll(__ballot(i < a.S && end <= tw + g));
+          if (g == gid) s += n;
+        }
+      }
+      s = min(s, a.S - 1);  // past the last: not among its tokens
+    }
+    if (__ballot(s != have) != 0) {
+      have = s;
+      q = sequence(a.offsets, a.lens, a.T, s);
+      const float n = (float)max(q.count, (int64_t)1);
+      float total = 0.0f;
+      if (a.grad != nullptr) {
+        const int32_t* row = a.counts + (int64_t)s * a.E;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          c[i] = e0 + i < a.E ? row[e0 + i] : 0;
+          total += (float)c[i];
+        }
+        total = group_sum<L>(total);
+        coef = total > 0.0f ? a.grad[s] * ((float)a.E / n) / total : 0.0f;
+      }
+      if (Z) zcoef = 2.0f * a.grad_z[s] / n;
+    }
+    Row<PER> r;
+    row_shares<L, PER, SIGMOID, Z>(l, r);
+    int ct = INT32_MIN;
+    float dot = 0.0f, d[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) ct = l[i] == r.top ? max(ct, c[i]) : ct;
+    ct = group_maxi<L>(ct);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      d[i] = (float)(int)((uint32_t)c[i] - (uint32_t)ct);
+      dot += r.p[i] * d[i];
+    }
+    dot = group_sum<L>(dot);
+    const bool mine = t >= q.first && t < q.first + q.count;
+    const float w = mine ? coef : 0.0f;
+    const float wz = Z && mine ? zcoef * r.lse : 0.0f;
+    float g[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      g[i] = w * r.p[i] * (d[i] - dot);
+      if (SIGMOID) g[i] *= r.back[i];
+      if (Z) g[i] += wz * (SIGMOID ? r.soft : r.p)[i];
+      g[i] += add[i];
+    }
+    if (t < to)
+      store_row<PER, BF16>(static_cast<char*>(a.out) + t * a.ld_out * kSize,
+                           a.E, e0, a.vec_out != 0, g);
+  }
+}
+
+// ------------------------------------------------------------ entry points
+
+// Lanes that a row takes, with four experts each up to 256 and 8 or 16 above.
+inline int row_lanes(int32_t E) {
+  int L = 4;
+  while (L < 64 && L * 4 < E) L *= 2;
+  return L;
+}
+
+template <typename F>
+void by_row(int32_t E, F&& f) {
+  using std::integral_constant;
+  if (E <= 16)
+    f(integral_constant<int, 4>{}, integral_constant<int, 4>{});
+  else if (E <= 32)
+    f(integral_constant<int, 8>{}, integral_constant<int, 4>{});
+  else if (E <= 64)
+    f(integral_constant<int, 16>{}, integral_constant<int, 4>{});
+  else if (E <= 128)
+    f(integral_constant<int, 32>{}, integral_constant<int, 4>{});
+  else if (E <= 256)
+    f(integral_constant<int, 64>{}, integral_constant<int, 4>{});
+  else if (E <= 512)
+    f(integral_constant<int, 64>{}, integral_constant<int, 8>{});
+  else
+    f(integral_constant<int, 64>{}, integral_constant<int, 16>{});
+}
+
+template <typename F>
+void by_kind(bool bf16, bool sigmoid, bool z, F&& f) {
+  using Y = std::true_type;
+  using N = std::false_type;
+  auto two = [&](auto b) {
+    if (sigmoid)
+      z ? f(b, Y{}, Y{}) : f(b, Y{}, N{});
+    else
+      z ? f(b, N{}, Y{}) : f(b, N{}, N{});
+  };
+  bf16 ? two(Y{}) : two(N{});
+}
+
+// Blocks of the first of two launches, and whether one launch does: a block
+// for every sequence, if no wavefront then has more than eight rows to read.
+struct BalanceGeom {
+  bool whole;
+  int64_t blocks, chunk;
+  int32_t epad, ncol;
+};
+
+constexpr int64_t kMaxParts = 512;
+
+BalanceGeom balance_geom(int64_t T, int32_t E) {
+  const int64_t slots = kWaves * 64 / row_lanes(E);
+  BalanceGeom g{};
+  g.whole = T <= 8 * slots;
+  g.blocks = std::min(kMaxParts, std::max<int64_t>(1, ceil_div(T, slots)));
+  g.chunk = std::max<int64_t>(1, ceil_div(T, g.blocks));
+  g.ncol = (int32_t)ceil_div(E, kCols);
+  g.epad = g.ncol * kCols;
+  return g;
+}
+
+size_t balance_bytes(const BalanceGeom& g, int32_t S) {
+  if (g.whole) return 0;
+  const size_t rows = (size_t)(g.blocks + S);
+  return (size_t)S * g.ncol * 16 + rows * g.epad * 8 + rows * 4 +
+         (size_t)S * 4;
+}
+
+bool balance_sizes_ok(int64_t T, int32_t E, int32_t S) {
+  return T >= 0 && T <= INT32_MAX && E >= 1 && S >= 1;
+}
+
+}  // namespace
+
+extern "C" size_t moe_balance_loss_workspace_bytes(int64_t T, int32_t E,
+                                                   int32_t S) {
+  if (!balance_sizes_ok(T, E, S) || E > MXQ_MAX_ROUTE_EXPERTS) return 0;
+  return balance_bytes(balance_geom(T, E), S);
+}
+
+extern "C" mxq_status moe_balance_loss(
+    const void* logits, mxq_out_dtype dtype, int64_t ld_logits,
+    const int32_t* topk_ids, int64_t T, int32_t E, int32_t K,
+    mxq_score_fn score, const int32_t* seq_offsets, const int32_t* seq_lens,
+    int32_t S, float* loss, float* z_loss, int32_t* counts, float* probs,
+    void* workspace, size_t workspace_bytes, void* stream) {
+  if (dtype != MXQ_OUT_BF16 && dtype != MXQ_OUT_F32)
+    return MXQ_ERR_UNSUPPORTED;
+  if (score != MXQ_SCORE_SOFTMAX && score != MXQ_SCORE_SIGMOID)
+    return MXQ_ERR_UNSUPPORTED;
+  if (!balance_sizes_ok(T, E, S) || K < 1 || K > MXQ_MAX_TOPK ||
+      (S > 1 && seq_offsets == nullptr))
+    return MXQ_ERR_INVALID_ARGUMENT;
+  // choices of one expert are counted in 32 bits
+  if (E > MXQ_MAX_ROUTE_EXPERTS || T * K > INT32_MAX)
+    return MXQ_ERR_UNSUPPORTED;
+  if (loss == nullptr || counts == nullptr || probs == nullptr ||
+      (T > 0 && (logits == nullptr || topk_ids == nullptr)) || ld_logits < E)
+    return MXQ_ERR_INVALID_ARGUMENT;
+  const BalanceGeom g = balance_geom(T, E);
+  const int64_t joins = (int64_t)S * g.ncol;
+  if (joins > max_blocks(kJoinThreads) || S > max_blocks(kThreads))
+    return MXQ_ERR_UNSUPPORTED;
+  BalanceArgs a{};
+  a.logits = logits;
+  a.ld = ld_logits;
+  a.ids = topk_ids;
+  a.T = T;
+  a.E = E;
+  a.K = K;
+  a.S = S;
+  a.offsets = seq_offsets;
+  a.lens = seq_lens;
+  a.vec = row_vec(logits, ld_logits, dtype == MXQ_OUT_BF16 ? 2 : 4);
+  a.loss = loss;
+  a.z = z_loss;
+  a.counts = counts;
+  a.probs = probs;
+  a.chunk = g.chunk;
+  a.epad = g.epad;
+  if (!g.whole) {
+    if (workspace_bytes < balance_bytes(g, S)) return MXQ_ERR_WORKSPACE;
+    if (workspace == nullptr || !aligned16(workspace))
+      return MXQ_ERR_INVALID_ARGUMENT;
+    const int64_t rows = g.blocks + S;
+    a.piece = static_cast<double*>(workspace);
+    a.part_p = reinterpret_cast<float*>(a.piece + joins * 2);
+    a.part_c = reinterpret_cast<int32_t*>(a.part_p + rows * g.epad);
+    a.part_z = reinterpret_cast<float*>(a.part_c + rows * g.epad);
+    a.done = reinterpret_cast<uint32_t*>(a.part_z + rows);
+  }
+  hipStream_t s = as_stream(stream);
+  by_row(E, [&](auto l, auto p) {
+    constexpr int L = decltype(l)::value, PER = decltype(p)::value;
+    by_kind(dtype == MXQ_OUT_BF16, score == MXQ_SCORE_SIGMOID,
+            z_loss != nullptr, [&](auto b, auto sg, auto z) {
+              constexpr bool B = decltype(b)::value, SG = decltype(sg)::value,
+                             Z = decltype(z)::value;
+              if (g.whole)
+                balance_whole_kernel<L, PER, B, SG, Z>
+                    <<<(unsigned)S, kThreads, 0, s>>>(a);
+              else
+                balance_part_kernel<L, PER, B, SG, Z>
+                    <<<(unsigned)g.blocks, kThreads, 0, s>>>(a);
+            });
+  });
+  if (!g.whole)
+    balance_join_kernel<<<(unsigned)joins, kJoinThreads, 0, s>>>(a, g.ncol);
+  return launch_status();
+}
+
+extern "C" mxq_status moe_balance_loss_backward(
+    const float* grad_loss, const float* grad_z, const void* logits,
+    mxq_out_dtype dtype, int64_t ld_logits, const int32_t* counts, int64_t T,
+    int32_t E, mxq_score_fn score, const int32_t* seq_offsets,
+    const int32_t* seq_lens, int32_t S, const void* add, int64_t ld_add,
+    void* grad_logits, int64_t ld_grad, void* stream) {
+  if (dtype != MXQ_OUT_BF16 && dtype != MXQ_OUT_F32)
+    return MXQ_ERR_UNSUPPORTED;
+  if (score != MXQ_SCORE_SOFTMAX && score != MXQ_SCORE_SIGMOID)
+    return MXQ_ERR_UNSUPPORTED;
+  if (!balance_sizes_ok(T, E, S) || (S > 1 && seq_offsets == nullptr) ||
+      (grad_loss == nullptr && grad_z == nullptr) ||
+      (grad_loss != nullptr && counts == nullptr))
+    return MXQ_ERR_INVALID_ARGUMENT;
+  if (E > MXQ_MAX_ROUTE_EXPERTS) return MXQ_ERR_UNSUPPORTED;
+  if (T == 0) return MXQ_OK;
+  if (logits == nullptr || grad_logits == nullptr || ld_logits < E ||
+      ld_grad < E || (add != nullptr && ld_add < E))
+    return MXQ_ERR_INVALID_ARGUMENT;
+  const int64_t esz = dtype == MXQ_OUT_BF16 ? 2 : 4;
+  BalanceBackArgs a{};
+  a.grad = grad_loss;
+  a.grad_z = grad_z;
+  a.logits = logits;
+  a.ld = ld_logits;
+  a.counts = counts;
+  a.T = T;
+  a.E = E;
+  a.S = S;
+  a.offsets = seq_offsets;
+  a.lens = seq_lens;
+  a.add = add;
+  a.ld_add = ld_add;
+  a.vec = row_vec(logits, ld_logits, esz);
+  a.vec_add = row_vec(add, ld_add, esz);
+  a.vec_out = row_vec(grad_logits, ld_grad, esz);
+  a.out = grad_logits;
+  a.ld_out = ld_grad;
+  // up to 2048 blocks, each with whole rounds of its wavefronts
+  const int64_t slots = kBackWaves * 64 / row_lanes(E);
+  const int64_t rounds = ceil_div(ceil_div(T, slots), 2048);
+  a.chunk = slots * rounds;
+  const unsigned blocks = (unsigned)ceil_div(T, a.chunk);
+  hipStream_t s = as_stream(stream);
+  by_row(E, [&](auto l, auto p) {
+    constexpr int L = decltype(l)::value, PER = decltype(p)::value;
+    by_kind(dtype == MXQ_OUT_BF16, score == MXQ_SCORE_SIGMOID,
+            grad_z != nullptr, [&](auto b, auto sg, auto z) {
+              balance_backward_kernel<L, PER, decltype(b)::value,
+                                      decltype(sg)::value, decltype(z)::value>
+                  <<<blocks, kBackWaves * 64, 0, s>>>(a);
+            });
+  });
+  return launch_status();
+}

@@ -24,67 +24,7 @@ namespace {
 
 using namespace mxq;
 
-// ------------------------------------------------------------ copies to LDS
-
-__device__ __forceinline__ v4i buffer_of(const void* base, uint32_t bytes) {
-  const uint64_t p = reinterpret_cast<uint64_t>(base);
-  v4i r;
-  r.x = __builtin_amdgcn_readfirstlane((int)(uint32_t)p);
-  r.y = __builtin_amdgcn_readfirstlane((int)(uint32_t)(p >> 32) & 0xFFFF);
-  r.z = __builtin_amdgcn_readfirstlane((int)bytes);
-  r.w = 0x00020000;  // raw 32-bit data, no swizzle
-  return r;
-}
-
-// 16 bytes per lane from `buf` at voff + soff into LDS at lds + 16 * lane.
-// The lane's address registers are the only operands: nothing is returned to
-// registers, so there is no result to wait for but the vmcnt before the next
-// barrier.  The clobbers keep LDS accesses, and what the compiler may hold in
-// m0, on their side of the copy (it warns that m0 is a register it never
-// allocates; it does write it for instructions of its own).
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-__device__ __forceinline__ void copy_to_lds(const v4i& buf, uint32_t lds,
-                                            uint32_t voff, uint32_t soff) {
-  asm volatile(
-      "s_mov_b32 m0, %0\n\t"
-      "s_nop 0\n\t"
-      "buffer_load_dwordx4 %1, %2, %3 offen lds"
-      :
-      : "s"(lds), "v"(voff), "s"(buf), "s"(soff)
-      : "m0", "memory");
-}
-#pragma clang diagnostic pop
-
-// Waits until all but the last VM loads and copies and the last LGKM LDS reads
-// that this wavefront has issued are done.
-template <int VM, int LGKM>
-__device__ __forceinline__ void wait_for() {
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt((VM & 15) | ((VM >> 4) << 14) | 0x70 |
-                             (LGKM << 8));
-  asm volatile("" ::: "memory");
-}
-
-// The same for the whole block.
-template <int VM, int LGKM>
-__device__ __forceinline__ void landed_barrier() {
-  wait_for<VM, LGKM>();
-  asm volatile("s_barrier" ::: "memory");
-}
-
 constexpr int kMaxSteps = MXQ_MAX_HIDDEN / 128;
-
-// 16-byte chunk c of an LDS row of 128 bytes sits at place c ^ ((row >> 1) & 7):
-// 16 neighbouring rows of a fragment read then touch all 64 banks once.  A
-// copy fills places in order, so the order is turned on its global side.
-__device__ __forceinline__ int place(int c, int row) {
-  return c ^ ((row >> 1) & 7);
-}
-
-__device__ __forceinline__ v8i join(const v4i& a, const v4i& b) {
-  return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-}
 
 // ------------------------------------------------------------ few rows
 //
@@ -331,60 +271,6 @@ __global__ __launch_bounds__(256, 1) void matmul_small_kernel(
 //
 // A gated tile takes 128 gate rows and the 128 factor rows of the same
 // outputs; a wavefront holds both for 64 outputs.
-
-// The tile a block works on.  Experts' tiles are numbered expert by expert,
-// from device data; every wavefront finds its block's by itself.  Runs of
-// consecutive tiles go to one XCD (block b runs on XCD b % 8), and within a
-// run eight row tiles share a column of weights, so the 32 CUs of an XCD
-// read a window of 8 by 4 tiles through their L2.
-struct TileOf {
-  int e, m0, n;
-};
-
-constexpr int kGroupM = 8;
-
-template <int TM>
-__device__ __forceinline__ bool find_tile(const MatmulArgs& a, int tiles_n,
-                                          TileOf& t) {
-  const int lane = threadIdx.x & 63;
-  const int per = (a.E + 63) / 64;  // experts per lane, consecutive
-  int mine = 0;
-  for (int i = 0; i < per; ++i) {
-    const int e = lane * per + i;
-    if (e < a.E) mine += (expert_rows(a, e).count + TM - 1) / TM;
-    // regions that do not overlap hold 2^24 tiles at most; more, of offsets
-    // that no layout makes, must not overflow the sums
-    mine = min(mine, 1 << 24);
-  }
-  int upto = mine;  // row tiles of lanes up to this one
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int v = __shfl_up(upto, d);
-    if (lane >= d) upto += v;
-  }
-  const int tiles_m = __builtin_amdgcn_readlane(upto, 63);
-  const int64_t total = (int64_t)tiles_m * tiles_n;
-  const int64_t run = (total + 7) / 8;
-  const int64_t at = (int64_t)(blockIdx.x & 7) * run + (blockIdx.x >> 3);
-  if ((int64_t)(blockIdx.x >> 3) >= run || at >= total) return false;
-  const int64_t group = at / ((int64_t)kGroupM * tiles_n);
-  const int gm = min(kGroupM, tiles_m - (int)group * kGroupM);
-  const int in = (int)(at - group * kGroupM * tiles_n);
-  t.n = in / gm;
-  const int m = (int)group * kGroupM + in % gm;
-  const int owner = __ffsll((unsigned long long)__ballot(upto > m)) - 1;
-  int first = __builtin_amdgcn_readlane(upto - mine, owner);
-  int e = owner * per;
-  for (int i = 0; i < per; ++i) {
-    const int c = (expert_rows(a, owner * per + i).count + TM - 1) / TM;
-    e = owner * per + i;
-    if (m < first + c) break;
-    first += c;
-  }
-  t.e = __builtin_amdgcn_readfirstlane(e);
-  t.m0 = __builtin_amdgcn_readfirstlane((m - first) * TM);
-  return true;
-}
 
 constexpr int kStageLd = 260;  // floats per staged token (256 weight rows + pad)
 constexpr int kScaleLd = 36;   // bytes per row of a scale chunk (32 + pad)
@@ -867,10 +753,6 @@ mxq_status launch(const MatmulArgs& a, int64_t expected, hipStream_t s) {
   return launch_small<G, OUT == kOutG128 ? 2 : 1, OUT>(a, s);
 }
 
-inline bool aligned8(const void* p) {
-  return (reinterpret_cast<uintptr_t>(p) & 7u) == 0;
-}
-
 template <int OUT>
 mxq_status checked(const void* q, int64_t ld_q, const uint8_t* scales,
                    int64_t ld_s, int64_t num_rows, mxq_scale_fmt fmt,
@@ -980,6 +862,7 @@ extern "C" mxq_status moe_expert_matmul_quant(
                               w_fp8, w_scales, E, N, H, expert_offsets,
                               counts, bias, act, nullptr, 0, expected_m,
                               q_out, ld_out, scales_out, ld_so, stream);
+    default:  // quantized rows of e4m3 only
+      return MXQ_ERR_UNSUPPORTED;
   }
-  return MXQ_ERR_UNSUPPORTED;
 }

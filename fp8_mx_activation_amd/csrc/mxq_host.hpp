@@ -13,6 +13,10 @@ inline bool aligned16(const void* p) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
 }
 
+inline bool aligned8(const void* p) {
+  return (reinterpret_cast<uintptr_t>(p) & 7u) == 0;
+}
+
 inline hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s); }
 
 // Launch status of the kernel just enqueued.
@@ -26,6 +30,8 @@ inline int group_of(mxq_scale_fmt fmt) {
       return 128;
     case MXQ_SCALE_E8M0_G32:
       return 32;
+    case MXQ_SCALE_MXFP4:
+      break;  // rows of e4m3 only
   }
   return 0;
 }

@@ -74,11 +74,14 @@ typedef enum {
 
 typedef enum { MXQ_LAYOUT_COMPACT = 0, MXQ_LAYOUT_MASKED = 1 } mxq_layout_kind;
 
-/* Both formats store one byte per group meaning 2^(b-127); the exponent is
- * the smallest e with amax(group) <= 448 * 2^e, clamped to [-127, 127]. */
+/* The formats store one byte per group meaning 2^(b-127); the exponent is
+ * the smallest e with amax(group) <= 448 * 2^e (6 * 2^e for e2m1 payloads),
+ * clamped to [-127, 127].  MXQ_SCALE_MXFP4 is known to the calls on
+ * microscaled 4-bit floats only; to the others it is MXQ_ERR_UNSUPPORTED. */
 typedef enum {
   MXQ_SCALE_UE8M0_G128 = 0, /* 128 channels per scale [P1 impl. item 3] */
-  MXQ_SCALE_E8M0_G32 = 1    /* 32 channels per scale  [P4 impl. item 1] */
+  MXQ_SCALE_E8M0_G32 = 1,   /* 32 channels per scale  [P4 impl. item 1] */
+  MXQ_SCALE_MXFP4 = 2       /* e2m1 payload, 32 channels per scale */
 } mxq_scale_fmt;
 
 /* Exponent rule for the *_ex quantizers.  MXQ_RULE_NO_CLIP is the rule
@@ -178,6 +181,71 @@ mxq_status moe_route_backward(const float* grad_weights, const void* logits,
                               int32_t renormalize, float weight_scale,
                               void* grad_logits, int64_t ld_grad,
                               void* stream);
+
+/* Workspace bytes moe_balance_loss needs: 0 where few tokens take one launch
+ * (up to 64 of more than 128 experts, 1024 of up to 16).  Pure host function;
+ * 0 for sizes that moe_balance_loss refuses. */
+size_t moe_balance_loss_workspace_bytes(int64_t T, int32_t E, int32_t S);
+
+/* Balance loss of a routing, for each of S sequences of tokens.  Of sequence
+ * s's n tokens t, with c_e the choices of expert e among their topk_ids:
+ *   p_te      softmax of the row of logits, or its sigmoids over their sum
+ *   probs_e   mean over t of p_te
+ *   loss      E * sum over e of (c_e / sum of c) * probs_e: 1 when balanced
+ *   z_loss    mean over t of (log sum over e of exp(logits_te))^2
+ *
+ *   logits       bf16 or fp32 (dtype) [T, ld_logits], the first E columns.  A
+ *                logit of -inf or NaN has a share of 0, one of +inf counts as
+ *                the largest finite value, as in moe_route; a row without a
+ *                live logit adds nothing to probs and z_loss.
+ *   topk_ids     int32 [T, K]; ids outside [0, E) are not counted.
+ *   seq_offsets  int32 [S + 1], ascending: sequence s begins at token
+ *                seq_offsets[s] and ends before seq_offsets[s + 1].  NULL: one
+ *                sequence (S = 1) of all tokens.
+ *   seq_lens     int32 [S] or NULL: only the first seq_lens[s] tokens of
+ *                sequence s are its own, the others padding that enters
+ *                nothing.
+ *   loss, z_loss fp32 [S]; z_loss may be NULL.  Both 0, as probs and counts,
+ *                where a sequence has no token; loss too without a choice.
+ *   counts       int32 [S, E]: c_e.
+ *   probs        fp32 [S, E].
+ *   workspace    >= moe_balance_loss_workspace_bytes(T, E, S) bytes, 16-byte
+ *                aligned (NULL where that is 0); its contents need no clearing
+ *                and mean nothing afterwards.
+ * Offsets and lengths are cut to the tokens that exist.  Sums are taken in a
+ * fixed order, in fp32 within a block and 64 bits across.
+ * T * K < 2^31 and E <= MXQ_MAX_ROUTE_EXPERTS, else MXQ_ERR_UNSUPPORTED. */
+mxq_status moe_balance_loss(const void* logits, mxq_out_dtype dtype,
+                            int64_t ld_logits, const int32_t* topk_ids,
+                            int64_t T, int32_t E, int32_t K,
+                            mxq_score_fn score, const int32_t* seq_offsets,
+                            const int32_t* seq_lens, int32_t S, float* loss,
+                            float* z_loss, int32_t* counts, float* probs,
+                            void* workspace, size_t workspace_bytes,
+                            void* stream);
+
+/* Gradient of moe_balance_loss to its logits, the counts held fixed.
+ *
+ *   grad_loss    fp32 [S] or NULL: the gradient of each sequence's loss.
+ *   grad_z       fp32 [S] or NULL: of each z_loss.  One of the two at least.
+ *   counts       int32 [S, E], not negative: the forward call's, or sums of
+ *                them over several ranks' batches (the loss then weighs this
+ *                batch's shares by all their choices).  May be NULL without
+ *                grad_loss.
+ *   add          [T, ld_add] in the logits' dtype, or NULL: a gradient that
+ *                this one is added to before it is rounded, such as
+ *                moe_route_backward's; may be grad_logits itself.
+ *   grad_logits  [T, ld_grad] in the logits' dtype: all E columns of every
+ *                row are written, those of tokens in no sequence with add
+ *                (or 0).  Must not overlap logits, and add only where it is
+ *                the same rows.
+ * Dead logits (-inf, NaN) get add (or 0). */
+mxq_status moe_balance_loss_backward(
+    const float* grad_loss, const float* grad_z, const void* logits,
+    mxq_out_dtype dtype, int64_t ld_logits, const int32_t* counts, int64_t T,
+    int32_t E, mxq_score_fn score, const int32_t* seq_offsets,
+    const int32_t* seq_lens, int32_t S, const void* add, int64_t ld_add,
+    void* grad_logits, int64_t ld_grad, void* stream);
 
 /* ----------------------------------------------------------------- layout */
 
@@ -504,6 +572,88 @@ mxq_status moe_expert_matmul_quant(
     const void* q_fp8, int64_t ld_q, const uint8_t* scales, int64_t ld_s,
     int64_t num_rows, mxq_scale_fmt fmt, const void* w_fp8,
     const uint8_t* w_scales, int32_t E, int32_t N, int32_t H,
+    const int32_t* expert_offsets, const int32_t* counts, const float* bias,
+    mxq_act act, int64_t expected_m, mxq_scale_fmt out_fmt, void* q_out,
+    int64_t ld_out, uint8_t* scales_out, int64_t ld_so, void* stream);
+
+/* ------------------------------------- microscaled 4-bit floats (MXFP4) */
+
+/* A row of H channels (a multiple of 32) is H / 2 bytes of e2m1 codes (0, 0.5,
+ * 1, 1.5, 2, 3, 4, 6 and their negatives; channel 2i in the lower half of byte
+ * i) and H / 32 scale bytes, as in MXQ_SCALE_E8M0_G32. */
+
+/* Rows of bf16 or fp32 (dtype) to MXFP4: weights, or activations.
+ *
+ *   x        [rows, ld_x], H columns.
+ *   rule     MXQ_RULE_NO_CLIP: the smallest e with amax <= 6 * 2^e;
+ *            MXQ_RULE_OCP_FLOOR: floor(log2 amax) - 2, payloads above 6 taken
+ *            as 6.  Both clamped below at -127, which an all-zero group gets.
+ *   q_fp4    [rows, ld_q] bytes; x * 2^-e to the nearest code, ties to even.
+ *   scales   [rows, ld_s] bytes: e + 127.
+ * Rows of x and q_fp4 start on 16 bytes.  The outputs must not overlap x. */
+mxq_status mxfp4_quant_rows(const void* x, mxq_out_dtype dtype, int64_t ld_x,
+                            int64_t rows, int32_t H, mxq_scale_rule rule,
+                            void* q_fp4, int64_t ld_q, uint8_t* scales,
+                            int64_t ld_s, void* stream);
+
+/* moe_scatter_quant with MXFP4 rows: each token's row is quantized once and
+ * written to its destinations.  Arguments as there; q_fp4 [num_rows, ld_q],
+ * scales [num_rows, ld_s].  Rows that are no destination are untouched. */
+mxq_status moe_scatter_quant_mxfp4(const void* x_bf16, int64_t ld_x, int64_t T,
+                                   int32_t H, const int32_t* src2dst,
+                                   int32_t K, mxq_scale_rule rule, void* q_fp4,
+                                   int64_t ld_q, uint8_t* scales, int64_t ld_s,
+                                   int64_t num_rows, void* stream);
+
+/* MXFP4 payloads as e4m3 bytes of the same values, for a consumer of 8-bit
+ * rows: with the scale bytes as they are, the rows are MXQ_SCALE_E8M0_G32's.
+ * q_fp4 [rows, ld_q] and out_fp8 [rows, ld_out] bytes, rows starting on 16. */
+mxq_status mxfp4_to_e4m3(const void* q_fp4, int64_t ld_q, int64_t rows,
+                         int32_t H, void* out_fp8, int64_t ld_out,
+                         void* stream);
+
+/* MXFP4 rows to bf16, over the first num_rows rows: payload * 2^(b - 127),
+ * which bf16 holds as it is (overflow to inf; scale byte 255 gives NaN).
+ * out_bf16 [num_rows, ld_out]; rows of q_fp4 and out_bf16 start on 16 bytes. */
+mxq_status upscale_mxfp4_to_bf16(const void* q_fp4, int64_t ld_q,
+                                 const uint8_t* scales, int64_t ld_s,
+                                 int64_t num_rows, int32_t H, void* out_bf16,
+                                 int64_t ld_out, void* stream);
+
+/* moe_expert_matmul with weights in MXFP4, and rows in MXFP4 (fmt
+ * MXQ_SCALE_MXFP4) or e4m3 with 32-channel scales (MXQ_SCALE_E8M0_G32; other
+ * formats MXQ_ERR_UNSUPPORTED).  For the live rows r of expert e, in fp32:
+ *   a[r, n] = sum over k of dec(q[r, k]) * dec(w[e, n, k]) + bias[e, n]
+ *   out[r]  = bf16(act(a[r]) + residual[r])
+ *
+ *   q, scales        [num_rows, ld_q] and [num_rows, ld_s] bytes, as
+ *                    moe_scatter_quant_mxfp4, mxfp4_quant_rows, mxfp4_to_e4m3,
+ *                    moe_scatter_quant and mx_quant_live_rows write them.
+ *   w_fp4, w_scales  [E, N, H / 2] contiguous codes, and scale bytes of row
+ *                    (e, n) at (e * N + n) * ld_ws, as mxfp4_quant_rows
+ *                    writes them.  ld_ws and w_scales are multiples of 4, and
+ *                    a row's scales are read four at a time: up to three bytes
+ *                    behind the last of them must be readable.
+ * The other arguments, limits and errors are moe_expert_matmul's; H is a
+ * multiple of 32, and ld_ws * N < 2^31.  Sums are fp32; 32 products of 4-bit
+ * payloads add up exactly in the matrix unit, of those with 8-bit rows it
+ * drops what lies more than 13 bits below the largest. */
+mxq_status moe_expert_matmul_mxfp4(
+    const void* q, int64_t ld_q, const uint8_t* scales, int64_t ld_s,
+    int64_t num_rows, mxq_scale_fmt fmt, const void* w_fp4,
+    const uint8_t* w_scales, int64_t ld_ws, int32_t E, int32_t N, int32_t H,
+    const int32_t* expert_offsets, const int32_t* counts, const float* bias,
+    mxq_act act, const void* residual_bf16, int64_t ld_r, int64_t expected_m,
+    void* out_bf16, int64_t ld_out, void* stream);
+
+/* moe_expert_matmul_mxfp4 with its fp32 rows quantized for the next product:
+ * out_fmt MXQ_SCALE_MXFP4 (q_out [num_rows, ld_out] codes) or
+ * MXQ_SCALE_E8M0_G32 (e4m3), by the rule without clipping; the output columns
+ * must be a multiple of 32.  Otherwise as moe_expert_matmul_quant. */
+mxq_status moe_expert_matmul_mxfp4_quant(
+    const void* q, int64_t ld_q, const uint8_t* scales, int64_t ld_s,
+    int64_t num_rows, mxq_scale_fmt fmt, const void* w_fp4,
+    const uint8_t* w_scales, int64_t ld_ws, int32_t E, int32_t N, int32_t H,
     const int32_t* expert_offsets, const int32_t* counts, const float* bias,
     mxq_act act, int64_t expected_m, mxq_scale_fmt out_fmt, void* q_out,
     int64_t ld_out, uint8_t* scales_out, int64_t ld_so, void* stream);
