@@ -272,7 +272,6 @@ __global__ __launch_bounds__(256, 1) void matmul_small_kernel(
 // A gated tile takes 128 gate rows and the 128 factor rows of the same
 // outputs; a wavefront holds both for 64 outputs.
 
-constexpr int kStageLd = 260;  // floats per staged token (256 weight rows + pad)
 constexpr int kScaleLd = 36;   // bytes per row of a scale chunk (32 + pad)
 
 template <int XF>
@@ -593,88 +592,7 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs a,
   if (k + 1 < nsteps) step(k++, Yes{}, No{}, No{}, Yes{});
   step(k, No{}, No{}, Yes{}, No{});
 
-  // End of the rows.  128 token rows (64 of each wavefront row) at a time go
-  // through LDS as they are, so that a thread ends up with eight neighbouring
-  // channels of a row: gate and factor meet, a row is written in whole lines,
-  // and a quantization group lies within a wavefront.
-  float* stage = reinterpret_cast<float*>(lds);
-  constexpr int kOutLanes = GATED ? 16 : 32;  // threads per row
-  constexpr int kPerRound = 256 / kOutLanes;  // rows per round of the block
-  constexpr int kRounds = 128 / kPerRound;
-  const int orow = (int)threadIdx.x / kOutLanes;
-  const int oc = (int)threadIdx.x % kOutLanes * 8;
-  const int col = n0 + oc;
-  float b[8], bu[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) b[j] = bu[j] = 0.0f;
-  if (a.bias != nullptr) {
-    const float* br = a.bias + (int64_t)t.e * a.N;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      b[j] = br[min(col + j, a.NO - 1)];
-      if (GATED) bu[j] = br[a.NO + min(col + j, a.NO - 1)];
-    }
-  }
-  // where the gate of output oc stands in a staged row; its factor is 64 on
-  const int gate_at = GATED ? (oc >> 6) * 128 + (oc & 63) : oc;
-  // token (of the tile) of row i of pass p
-  auto token = [&](int p, int i) {
-    return (i >> 6) * 32 * XF + p * 64 + (i & 63);
-  };
-  constexpr int kPasses = XF / 2;
-  // A pass's residual is asked for a pass ahead, the first one's before its
-  // staging: the loads are in flight together and behind other work.
-  u32x4 res[2][kRounds];
-  auto ask = [&](int p) {
-#pragma unroll
-    for (int i = 0; i < kRounds; ++i)
-      res[p & 1][i] = load_residual(
-          a, row0 + min(token(p, i * kPerRound + orow), rows - 1), col);
-  };
-  const bool has_res = OUT == kOutBf16 && a.res != nullptr;
-  if (has_res) {
-    ask(0);
-  } else {
-#pragma unroll
-    for (int i = 0; i < kRounds; ++i)
-      res[0][i] = res[1][i] = u32x4{0, 0, 0, 0};
-  }
-#pragma unroll
-  for (int pass = 0; pass < kPasses; ++pass) {
-    __syncthreads();
-#pragma unroll
-    for (int f = 0; f < 4; ++f)
-#pragma unroll
-      for (int q4 = 0; q4 < 4; ++q4)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const v16f& v = acc[f][2 * pass + x];
-          *reinterpret_cast<v4f*>(stage +
-                                  (wm * 64 + x * 32 + r32) * kStageLd +
-                                  wn * 128 + f * 32 + 8 * q4 + 4 * g) =
-              v4f{v[4 * q4], v[4 * q4 + 1], v[4 * q4 + 2], v[4 * q4 + 3]};
-        }
-    __syncthreads();
-    if (has_res && pass + 1 < kPasses) ask(pass + 1);
-#pragma unroll
-    for (int i = 0; i < kRounds; ++i) {
-      const int at = i * kPerRound + orow;
-      const int tok = token(pass, at);
-      const float* src = stage + at * kStageLd + gate_at;
-      float v[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = src[j] + b[j];
-      if constexpr (GATED) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = silu(v[j]) * (src[64 + j] + bu[j]);
-      } else if (a.act == kActSilu) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = silu(v[j]);
-      }
-      store_channels<OUT>(a, row0 + min(tok, rows - 1), col,
-                          tok < rows && col < a.NO, v, res[pass & 1][i]);
-    }
-  }
+  finish_tile<XF, OUT, GATED>(a, t.e, row0, rows, n0, acc, lds);
 }
 
 // ------------------------------------------------------------ entry points

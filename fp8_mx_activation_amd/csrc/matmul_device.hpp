@@ -259,4 +259,102 @@ __device__ __forceinline__ bool find_tile(const MatmulArgs& a, int tiles_n,
   return true;
 }
 
+// ------------------------------------------------------------ end of a tile
+
+constexpr int kStageLd = 260;  // floats per staged token (256 weight rows + pad)
+
+// End of a tile of 64 XF token rows (`rows` of them live, from row0 on) by 256
+// weight rows of expert e, from output n0 on.  128 token rows (64 of each
+// wavefront row) at a time go through LDS as they are, so that a thread ends up
+// with eight neighbouring channels of a row: gate and factor meet, a row is
+// written in whole lines, and a quantization group lies within a wavefront.
+template <int XF, int OUT, bool GATED>
+__device__ __forceinline__ void finish_tile(const MatmulArgs& a, int e,
+                                            int64_t row0, int rows, int n0,
+                                            const v16f (&acc)[4][XF],
+                                            uint8_t* lds) {
+  float* stage = reinterpret_cast<float*>(lds);
+  constexpr int kOutLanes = GATED ? 16 : 32;  // threads per row
+  constexpr int kPerRound = 256 / kOutLanes;  // rows per round of the block
+  constexpr int kRounds = 128 / kPerRound;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  const int r32 = lane & 31, g = lane >> 5;
+  const int orow = (int)threadIdx.x / kOutLanes;
+  const int oc = (int)threadIdx.x % kOutLanes * 8;
+  const int col = n0 + oc;
+  float b[8], bu[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) b[j] = bu[j] = 0.0f;
+  if (a.bias != nullptr) {
+    const float* br = a.bias + (int64_t)e * a.N;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      b[j] = br[min(col + j, a.NO - 1)];
+      if (GATED) bu[j] = br[a.NO + min(col + j, a.NO - 1)];
+    }
+  }
+  // where the gate of output oc stands in a staged row; its factor is 64 on
+  const int gate_at = GATED ? (oc >> 6) * 128 + (oc & 63) : oc;
+  // token (of the tile) of row i of pass p
+  auto token = [&](int p, int i) {
+    return (i >> 6) * 32 * XF + p * 64 + (i & 63);
+  };
+  constexpr int kPasses = XF / 2;
+  // A pass's residual is asked for a pass ahead, the first one's before its
+  // staging: the loads are in flight together and behind other work.
+  u32x4 res[2][kRounds];
+  auto ask = [&](int p) {
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i)
+      res[p & 1][i] = load_residual(
+          a, row0 + min(token(p, i * kPerRound + orow), rows - 1), col);
+  };
+  const bool has_res = OUT == kOutBf16 && a.res != nullptr;
+  if (has_res) {
+    ask(0);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i)
+      res[0][i] = res[1][i] = u32x4{0, 0, 0, 0};
+  }
+#pragma unroll
+  for (int pass = 0; pass < kPasses; ++pass) {
+    __syncthreads();
+#pragma unroll
+    for (int f = 0; f < 4; ++f)
+#pragma unroll
+      for (int q4 = 0; q4 < 4; ++q4)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const v16f& v = acc[f][2 * pass + x];
+          *reinterpret_cast<v4f*>(stage +
+                                  (wm * 64 + x * 32 + r32) * kStageLd +
+                                  wn * 128 + f * 32 + 8 * q4 + 4 * g) =
+              v4f{v[4 * q4], v[4 * q4 + 1], v[4 * q4 + 2], v[4 * q4 + 3]};
+        }
+    __syncthreads();
+    if (has_res && pass + 1 < kPasses) ask(pass + 1);
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
+      const int at = i * kPerRound + orow;
+      const int tok = token(pass, at);
+      const float* src = stage + at * kStageLd + gate_at;
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = src[j] + b[j];
+      if constexpr (GATED) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = silu(v[j]) * (src[64 + j] + bu[j]);
+      } else if (a.act == kActSilu) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = silu(v[j]);
+      }
+      store_channels<OUT>(a, row0 + min(tok, rows - 1), col,
+                          tok < rows && col < a.NO, v, res[pass & 1][i]);
+    }
+  }
+}
+
 }  // namespace mxq

@@ -294,6 +294,409 @@ __global__ __launch_bounds__(256, 1) void matmul4_small_kernel(
   }
 }
 
+// ------------------------------------------------------------ many rows
+//
+// The tiles of the products with 8-bit weights: a block of four wavefronts,
+// one per SIMD, owns TM = 64 XF token rows of one expert by 256 weight rows;
+// each wavefront multiplies 32 XF tokens by 128 weight rows in 32x32x64 steps.
+// A token row's part of a step is 128 bytes, so K goes by in steps of 256
+// channels for 4-bit rows and of 128 for 8-bit ones, held in LDS twice: while
+// one step is multiplied, the next is on its way from memory straight into LDS.
+// Either way a step of a 256-row tile is 2048 cycles of MFMA per SIMD.
+//
+// A step is multiplied in two halves, A with the first half of the wavefront's
+// token fragments, B with the second.  B's token fragments are read from LDS
+// during A; the next step's weight fragments and first token fragments during
+// B, each weight fragment into the registers that its last MFMA has just left.
+// The copies of the step after the next are dealt out evenly over both.
+//
+// Scales.  A step needs eight bytes (8-bit rows: four) of every token and
+// weight row.  They come in chunks of 16 bytes per row, copied straight into
+// LDS as a step's data are, for the weights and for tokens whose scales start
+// on 4 bytes; a chunk that ends behind the row is put together at the start,
+// with 127 (a factor of one) for the blocks that are not there.  Tokens' scales
+// that start elsewhere go through registers, a chunk at a time; the compiler
+// then waits for all copies on their way once per chunk.
+template <bool X8, int XF>
+struct Tile {
+  static constexpr int kTM = 64 * XF;
+  static constexpr int kChannels = X8 ? 128 : 256;  // of a step
+  static constexpr int kWRow = kChannels / 2;       // bytes of a weight row
+  static constexpr int kX = kTM * 128;              // and of all token rows
+  static constexpr int kStage = kX + 256 * kWRow;
+  static constexpr int kPieces = kWRow / 32;  // MFMA steps: 16-byte pieces of a
+                                              // lane's weights
+  static constexpr int kSteps = X8 ? 4 : 2;   // per chunk of scales
+  static constexpr int kScaleStep = 16 / kSteps;
+  static constexpr int kChunk = (kTM + 256) * 16;
+  // three chunks: two that take turns, and the one that ends behind the row
+  static constexpr int kLoop = 2 * kStage + 3 * kChunk;
+  static constexpr int kEnd = 128 * kStageLd * 4;
+  static constexpr int kLds = kLoop > kEnd ? kLoop : kEnd;
+  // copies of a wavefront: of a weight fragment (both wavefront columns'), of
+  // half A of a step (weight fragments 0-2, token fragment 0) and of half B
+  static constexpr int kCopiesW = X8 ? 1 : 2;
+  static constexpr int kCopiesA = 3 * kCopiesW + 2;
+  static constexpr int kCopiesB = kCopiesW + 2 * (XF - 1);
+};
+
+// A uniform value for an operand that has to be in a scalar register.
+__device__ __forceinline__ uint32_t in_scalar(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_readfirstlane((int)v);
+}
+
+// 16-byte chunk c of an LDS row of 64 bytes sits at place c ^ ((row >> 2) & 3).
+__device__ __forceinline__ int place64(int c, int row) {
+  return c ^ ((row >> 2) & 3);
+}
+
+template <bool X8, int XF, int OUT, bool GATED>
+__global__ __launch_bounds__(256, 1) void matmul4_tile_kernel(
+    MatmulArgs a, int32_t tiles_n, int32_t xs_words) {
+  using T = Tile<X8, XF>;
+  constexpr int TM = T::kTM;
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  TileOf t;
+  if (!find_tile<TM>(a, tiles_n, t)) return;
+  const ExpertRows er = expert_rows(a, t.e);
+  const int rows = min(er.count - t.m0, TM);  // live rows of this tile
+  const int64_t row0 = er.first + t.m0;
+  const int n0 = t.n * (GATED ? 128 : 256);
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  const int r32 = lane & 31, g = lane >> 5;
+  const int H = a.H;
+  const int ld_w = H / 2;           // bytes of a weight row
+  const int ld_x = X8 ? H : H / 2;  // and of a token row
+  const int groups = H / 32;
+  const int nsteps = (H + T::kChannels - 1) / T::kChannels;
+
+  // weight row (within the expert's matrix) of local row lr of the tile
+  auto weight_row = [&](int lr) {
+    if (!GATED) return min(n0 + lr, a.N - 1);
+    const int c = min(n0 + (lr >> 7) * 64 + (lr & 63), a.NO - 1);
+    return (lr & 64) ? a.NO + c : c;
+  };
+
+  // Copies of 1 KB.  Of token rows, 8 rows each: lane l fills place l & 7 of
+  // row l >> 3; the 64 rows of fragment x of both wavefront rows are two
+  // copies per wavefront.  Of weight rows the same, or 16 rows of 64 bytes.
+  const int xrow = wave * 8 + (lane >> 3);
+  const int xchunk = place(lane & 7, xrow);
+  const int wrow = X8 ? wave * 16 + (lane >> 2) : xrow;
+  const int wchunk = X8 ? place64(lane & 3, wrow) : xchunk;
+  uint32_t xoff[XF][2], woff[4][T::kCopiesW];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int x = 0; x < XF; ++x)
+      xoff[x][i] = (uint32_t)(min((i * XF + x) * 32 + xrow, rows - 1) *
+                              (int)a.ld_q + 16 * xchunk);
+  // local row of row r (below 64) of weight fragment f of both columns
+  auto both = [](int f, int r) { return (r >> 5) * 128 + f * 32 + (r & 31); };
+#pragma unroll
+  for (int f = 0; f < 4; ++f)
+#pragma unroll
+    for (int i = 0; i < T::kCopiesW; ++i)
+      woff[f][i] = (uint32_t)(
+          (weight_row(both(f, X8 ? wrow : i * 32 + wrow)) - n0) * ld_w +
+          16 * wchunk);
+  const v4i xbuf = buffer_of(a.q + row0 * a.ld_q,
+                             (uint32_t)((rows - 1) * a.ld_q + ld_x));
+  const v4i wbuf = buffer_of(a.w + ((int64_t)t.e * a.N + n0) * ld_w,
+                             (uint32_t)((a.N - n0) * ld_w));
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(
+      __attribute__((address_space(3))) uint8_t*)lds;
+  // In a last step that ends inside its channels, chunks past H repeat chunk 0
+  // of the step: in bounds, and cleared when they are read.
+  auto x_back = [&](int k) {
+    return (uint32_t)(k * 128 + 16 * xchunk >= ld_x ? 16 * xchunk : 0);
+  };
+  auto w_back = [&](int k) {
+    return (uint32_t)(k * T::kWRow + 16 * wchunk >= ld_w ? 16 * wchunk : 0);
+  };
+  auto copy_w = [&](int k, int f, int i, uint32_t back) {
+    copy_to_lds(wbuf,
+                lds0 + (k & 1) * T::kStage + T::kX +
+                    (X8 ? f * 64 * 64 : (i * 128 + f * 32) * 128) +
+                    wave * 1024,
+                woff[f][i] - back, in_scalar(k * T::kWRow));
+  };
+  auto copy_x = [&](int k, int x, int i, uint32_t back) {
+    copy_to_lds(xbuf,
+                lds0 + (k & 1) * T::kStage + (i * XF + x) * 32 * 128 +
+                    wave * 1024,
+                xoff[x][i] - back, in_scalar(k * 128));
+  };
+  auto copy_a = [&](int k, int c, uint32_t wb, uint32_t xb) {
+    if (c < 3 * T::kCopiesW)
+      copy_w(k, c / T::kCopiesW, c % T::kCopiesW, wb);
+    else
+      copy_x(k, 0, c - 3 * T::kCopiesW, xb);
+  };
+  // token fragments of half A, then the weights', then those of half B
+  constexpr int kXA = XF / 2;
+  auto copy_b = [&](int k, int c, uint32_t wb, uint32_t xb) {
+    constexpr int first = 2 * (kXA - 1);
+    if (c < first)
+      copy_x(k, 1 + c / 2, c & 1, xb);
+    else if (c < first + T::kCopiesW)
+      copy_w(k, 3, c - first, wb);
+    else
+      copy_x(k, kXA + (c - first - T::kCopiesW) / 2,
+             (c - first - T::kCopiesW) & 1, xb);
+  };
+
+  // ---- scales
+  uint8_t* scale = lds + 2 * T::kStage;
+  const uint32_t scale0 = lds0 + 2 * T::kStage;
+  const int full = groups / 16;  // chunks that end within the row
+  // wavefront w brings the chunk of token rows [64 w, 64 w + 64) (of a tile of
+  // 128, the second two the first two's again) and of as many weight rows
+  const int srow = (wave % XF) * 64 + lane;
+  const uint32_t xsoff = (uint32_t)(min(srow, rows - 1) * (int)a.ld_s);
+  const uint32_t wsoff =
+      (uint32_t)((weight_row(wave * 64 + lane) - n0) * a.nbk);
+  const v4i xsbuf = buffer_of(a.s + row0 * a.ld_s,
+                              (uint32_t)((rows - 1) * a.ld_s + groups));
+  const v4i wsbuf = buffer_of(a.ws + ((int64_t)t.e * a.N + n0) * a.nbk,
+                              (uint32_t)((a.N - n0) * a.nbk));
+  auto copy_scales = [&](int j) {
+    const uint32_t at = scale0 + (j & 1) * T::kChunk;
+    if (xs_words)
+      copy_to_lds(xsbuf, at + (wave % XF) * 1024, xsoff, in_scalar(j * 16));
+    copy_to_lds(wsbuf, at + TM * 16 + wave * 1024, wsoff, in_scalar(j * 16));
+  };
+  const uint8_t* xs_row =
+      a.s + (row0 + min((int)threadIdx.x, rows - 1)) * a.ld_s;
+  uint32_t xs_next[4];
+  auto fetch_scales = [&](int j) {
+    if ((int)threadIdx.x >= TM) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      __builtin_memcpy(&xs_next[i], xs_row + j * 16 + 4 * i, 4);
+  };
+  auto put_scales = [&](int j) {
+    if ((int)threadIdx.x >= TM) return;
+    *reinterpret_cast<u32x4*>(scale + (j & 1) * T::kChunk + threadIdx.x * 16) =
+        u32x4{xs_next[0], xs_next[1], xs_next[2], xs_next[3]};
+  };
+  // the bytes that are left of row p, 127 behind them
+  auto last_scales = [&](const uint8_t* p, int at) {
+    uint32_t v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = 0x7F7F7F7Fu;
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const int c = full * 16 + 4 * i + b;
+        if (c < groups)
+          v[i] = (v[i] & ~(0xFFu << (8 * b))) | ((uint32_t)p[c] << (8 * b));
+      }
+    }
+    *reinterpret_cast<u32x4*>(scale + 2 * T::kChunk + at * 16) =
+        u32x4{v[0], v[1], v[2], v[3]};
+  };
+  constexpr int kWords = X8 ? 1 : 2;  // of a row's scales in a step
+  uint32_t sx[XF][kWords], sw[4][kWords], sx1[XF][kWords], sw1[4][kWords];
+  auto read_scales = [&](int k) {
+    const int j = k / T::kSteps;
+    const uint8_t* at = scale + (j == full ? 2 : j & 1) * T::kChunk +
+                        k % T::kSteps * T::kScaleStep;
+#pragma unroll
+    for (int x = 0; x < XF; ++x)
+      __builtin_memcpy(sx1[x], __builtin_assume_aligned(
+          at + (wm * 32 * XF + x * 32 + r32) * 16, T::kScaleStep),
+          T::kScaleStep);
+#pragma unroll
+    for (int f = 0; f < 4; ++f)
+      __builtin_memcpy(sw1[f], __builtin_assume_aligned(
+          at + (TM + wn * 128 + f * 32 + r32) * 16, T::kScaleStep),
+          T::kScaleStep);
+  };
+  // lane group g takes every second block's
+  auto use_scales = [&]() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+#pragma unroll
+      for (int x = 0; x < XF; ++x) sx[x][i] = sx1[x][i] >> (8 * g);
+#pragma unroll
+      for (int f = 0; f < 4; ++f) sw[f][i] = sw1[f][i] >> (8 * g);
+    }
+  };
+
+  v16f acc[4][XF];
+#pragma unroll
+  for (int f = 0; f < 4; ++f)
+#pragma unroll
+    for (int x = 0; x < XF; ++x)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[f][x][i] = 0.0f;
+
+  // fragments of a step, in 16-byte pieces
+  constexpr int kP = T::kPieces;
+  v4i fw[4][kP], fx[XF][4];
+  auto read_w = [&](int k, int f, int p, auto last) {
+    const int c = p * 2 + g;
+    const uint8_t* base = lds + (k & 1) * T::kStage + T::kX;
+    // the rows of a fragment of both columns follow each other where a
+    // wavefront's copy brings 16 of them
+    const uint8_t* at =
+        X8 ? base + (f * 64 + wn * 32 + r32) * 64 + place64(c, r32) * 16
+           : base + (wn * 128 + f * 32 + r32) * 128 + place(c, r32) * 16;
+    v4i v = *reinterpret_cast<const v4i*>(at);
+    if constexpr (decltype(last)::value)
+      if (k * T::kWRow + 16 * c >= ld_w) v = v4i{0, 0, 0, 0};
+    fw[f][p] = v;
+  };
+  auto read_x = [&](int k, int x, int p, auto last) {
+    const int c = p * 2 + g;
+    v4i v = *reinterpret_cast<const v4i*>(
+        lds + (k & 1) * T::kStage + (wm * 32 * XF + x * 32 + r32) * 128 +
+        place(c, r32) * 16);
+    if constexpr (decltype(last)::value)
+      if (k * 128 + 16 * c >= ld_x) v = v4i{0, 0, 0, 0};
+    fx[x][p] = v;
+  };
+  constexpr int kMfma = 4 * kP * kXA;  // of a half
+  // MFMA i of a half whose first token fragment is x0: weight fragments one
+  // after the other, the pieces of each in turn.  Piece p's scales are byte
+  // 2 p of the words that use_scales leaves.
+  auto multiply = [&](int i, int x0) {
+    const int f = i / (kP * kXA), p = i / kXA % kP, x = x0 + i % kXA;
+    const v8i w = half(fw[f][p]);
+    const v8i v = X8 ? join(fx[x][2 * p & 3], fx[x][(2 * p + 1) & 3])
+                     : half(fx[x][p & 3]);
+    constexpr int B = X8 ? kFmtFp8 : kFmtFp4;
+    if (p & 1)
+      acc[f][x] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+          w, v, acc[f][x], kFmtFp4, B, 2, (int)sw[f][p / 2], 2,
+          (int)sx[x][p / 2]);
+    else
+      acc[f][x] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+          w, v, acc[f][x], kFmtFp4, B, 0, (int)sw[f][p / 2], 0,
+          (int)sx[x][p / 2]);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  using Yes = std::true_type;
+  using No = std::false_type;
+  auto copy_all = [&](int k) {
+    const uint32_t wb = w_back(k), xb = x_back(k);
+#pragma unroll
+    for (int c = 0; c < T::kCopiesA; ++c) copy_a(k, c, wb, xb);
+#pragma unroll
+    for (int c = 0; c < T::kCopiesB; ++c) copy_b(k, c, wb, xb);
+  };
+
+  if (full > 0) copy_scales(0);
+  copy_all(0);
+  if (groups % 16 != 0) {
+    if ((int)threadIdx.x < TM) last_scales(xs_row, threadIdx.x);
+    last_scales(a.ws + ((int64_t)t.e * a.N + weight_row(threadIdx.x)) * a.nbk,
+                TM + threadIdx.x);
+  }
+  if (!xs_words && full > 0) {
+    fetch_scales(0);
+    put_scales(0);
+  }
+  landed_barrier<0, 0>();
+  if (nsteps > 1) copy_all(1);
+  read_scales(0);
+  use_scales();
+#pragma unroll
+  for (int x = 0; x < kXA; ++x)
+#pragma unroll
+    for (int p = 0; p < 4; ++p) read_x(0, x, p, Yes{});
+#pragma unroll
+  for (int f = 0; f < 4; ++f)
+#pragma unroll
+    for (int p = 0; p < kP; ++p) read_w(0, f, p, Yes{});
+  __builtin_amdgcn_sched_barrier(0);
+
+  // One step.  `more`: another one follows; `copy`: and one after that;
+  // `last`: this is, and `next_last`: the next one is, the last.  The waits
+  // count the copies that may still be on their way: at barrier A all of the
+  // next step's, at barrier B those of its second token fragments and of the
+  // step after it.  A chunk of scales is asked for before the copies of its
+  // first step, so it has landed where they have.  At barrier A the reads of
+  // weight fragment 3, always the last ones, may be under way too: its rows are
+  // overwritten after barrier B only.
+  auto step = [&](int k, auto more_, auto copy_, auto last, auto next_last) {
+    constexpr bool more = decltype(more_)::value;
+    constexpr bool copy = decltype(copy_)::value;
+    const uint32_t wb = w_back(k + 2), xb = x_back(k + 2);
+    const int chunk = (k + 2) / T::kSteps;  // of scales
+    const bool ask = copy && (k + 2) % T::kSteps == 0 && chunk < full;
+    landed_barrier<more ? T::kCopiesA + T::kCopiesB : 0, kP>();
+    if (ask) copy_scales(chunk);
+    if (more && !xs_words) {
+      // fetched two steps before the chunk's first, put down in the one
+      // before it, ahead of barrier B
+      const int next = (k + 1) / T::kSteps;
+      if ((k + 1) % T::kSteps == 0 && next < full) put_scales(next);
+      if (ask) fetch_scales(chunk);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < kMfma; ++i) {
+      if constexpr (copy) {
+#pragma unroll
+        for (int c = i * T::kCopiesA / kMfma; c < (i + 1) * T::kCopiesA / kMfma;
+             ++c)
+          copy_a(k + 2, c, wb, xb);
+      }
+      constexpr int kEach = kMfma / 8 > 1 ? 2 : 1;  // MFMAs per read
+      if (i % kEach == 0 && i / kEach < 4) {
+#pragma unroll
+        for (int x = kXA; x < XF; ++x) read_x(k, x, i / kEach, last);
+      }
+      multiply(i, 0);
+    }
+    if constexpr (more)
+      landed_barrier<copy ? T::kCopiesA + 2 * kXA : 2 * kXA, 0>();
+    if constexpr (more) read_scales(k + 1);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < kMfma; ++i) {
+      if constexpr (copy) {
+#pragma unroll
+        for (int c = i * T::kCopiesB / kMfma; c < (i + 1) * T::kCopiesB / kMfma;
+             ++c)
+          copy_b(k + 2, c, wb, xb);
+      }
+      if constexpr (more) {
+        // a weight fragment's registers take the next step's as soon as its
+        // MFMAs are issued
+        constexpr int kF = kP * kXA;  // MFMAs of a weight fragment
+        if (i < kF) {
+#pragma unroll
+          for (int p = i * 4 / kF; p < (i + 1) * 4 / kF; ++p)
+#pragma unroll
+            for (int x = 0; x < kXA; ++x) read_x(k + 1, x, p, next_last);
+        } else {
+#pragma unroll
+          for (int p = i % kF * kP / kF; p < (i % kF + 1) * kP / kF; ++p)
+            read_w(k + 1, i / kF - 1, p, next_last);
+        }
+      }
+      multiply(i, kXA);
+    }
+    if constexpr (more) {
+      use_scales();
+#pragma unroll
+      for (int p = 0; p < kP; ++p) read_w(k + 1, 3, p, next_last);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  int k = 0;
+  for (; k + 2 < nsteps; ++k) step(k, Yes{}, Yes{}, No{}, No{});
+  if (k + 1 < nsteps) step(k++, Yes{}, No{}, No{}, Yes{});
+  step(k, No{}, No{}, Yes{}, No{});
+
+  finish_tile<XF, OUT, GATED>(a, t.e, row0, rows, n0, acc, lds);
+}
+
 // ------------------------------------------------------------ entry points
 
 constexpr int kLds = 160 * 1024;  // of a CU
@@ -323,9 +726,40 @@ mxq_status launch_small(const MatmulArgs& a, hipStream_t s) {
   return launch_status();
 }
 
+template <bool X8, int XF, int OUT>
+mxq_status launch_tile(const MatmulArgs& a, hipStream_t s) {
+  const int64_t tn = ceil_div(a.NO, a.act == kActSiluMul ? 128 : 256);
+  // every expert ends in at most one partial row tile
+  const int64_t tm = a.num_rows / (64 * XF) + a.E;
+  const int64_t blocks = ceil_div(tm * tn, 8) * 8;
+  if (blocks > max_blocks(256)) return MXQ_ERR_UNSUPPORTED;
+  constexpr int lds = Tile<X8, XF>::kLds;
+  static_assert(lds <= kLds, "a tile fits a CU");
+  auto* k = a.act == kActSiluMul ? &matmul4_tile_kernel<X8, XF, OUT, true>
+                                 : &matmul4_tile_kernel<X8, XF, OUT, false>;
+  if (hipFuncSetAttribute(reinterpret_cast<const void*>(k),
+                          hipFuncAttributeMaxDynamicSharedMemorySize,
+                          lds) != hipSuccess) {
+    (void)hipGetLastError();
+    return MXQ_ERR_HIP;
+  }
+  const bool words =
+      (reinterpret_cast<uintptr_t>(a.s) & 3u) == 0 && a.ld_s % 4 == 0;
+  k<<<(unsigned)blocks, 256, lds, s>>>(a, (int32_t)tn, words);
+  return launch_status();
+}
+
 template <bool X8, int OUT>
 mxq_status launch(const MatmulArgs& a, int64_t expected, hipStream_t s) {
-  (void)expected;
+  constexpr int64_t kCus = 256;
+  if (expected > 12) {
+    const int64_t columns =
+        a.E * ceil_div(a.NO, a.act == kActSiluMul ? 128 : 256);
+    const int64_t rounds4 = ceil_div(columns * ceil_div(expected, 256), kCus);
+    const int64_t rounds2 = ceil_div(columns * ceil_div(expected, 128), kCus);
+    return rounds2 * 3 <= rounds4 * 5 ? launch_tile<X8, 2, OUT>(a, s)
+                                      : launch_tile<X8, 4, OUT>(a, s);
+  }
   if (ceil_div(a.N, 256) * a.E >= 256) return launch_small<X8, 3, 4, OUT>(a, s);
   return launch_small<X8, 3, 1, OUT>(a, s);
 }
