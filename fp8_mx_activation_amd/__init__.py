@@ -19,6 +19,7 @@ half.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -391,6 +392,16 @@ def _dense(t: torch.Tensor, name: str, dtype, shape: tuple,
     return t.data_ptr() or None
 
 
+def _dense_on(t: torch.Tensor, name: str, dtype, shape: tuple,
+              like: torch.Tensor, dev: int) -> int | None:
+    """``_dense`` with the device known: each attribute read once, and no
+    more said unless something is wrong."""
+    if t.get_device() == dev and t.dtype is dtype and t.shape == shape and \
+            t.is_contiguous():
+        return t.data_ptr() or None
+    return _dense(t, name, dtype, shape, like)
+
+
 def _matrix(t: torch.Tensor, name: str, dtypes,
             like: torch.Tensor | None = None):
     """What ``_dev``, ``_rows`` and ``_ptr`` check and give, with each
@@ -474,11 +485,12 @@ def moe_route_backward(grad_weights: torch.Tensor, logits: torch.Tensor,
     return grad_logits
 
 
+@functools.lru_cache(maxsize=256)
 def moe_balance_loss_workspace_bytes(T: int, E: int, S: int) -> int:
     return int(lib().moe_balance_loss_workspace_bytes(T, E, S))
 
 
-def _sequences(seq_offsets, seq_lens, like):
+def _sequences(seq_offsets, seq_lens, like, dev):
     """Pointers of the sequences' offsets and lengths, and their number."""
     off = lens = None
     S = 1
@@ -486,9 +498,10 @@ def _sequences(seq_offsets, seq_lens, like):
         if seq_offsets.dim() != 1 or seq_offsets.shape[0] < 2:
             raise ValueError("seq_offsets must be int32 [S + 1]")
         S = seq_offsets.shape[0] - 1
-        off = _dense(seq_offsets, "seq_offsets", torch.int32, (S + 1,), like)
+        off = _dense_on(seq_offsets, "seq_offsets", torch.int32, (S + 1,),
+                        like, dev)
     if seq_lens is not None:
-        lens = _dense(seq_lens, "seq_lens", torch.int32, (S,), like)
+        lens = _dense_on(seq_lens, "seq_lens", torch.int32, (S,), like, dev)
     return off, lens, S
 
 
@@ -511,24 +524,27 @@ def moe_balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor,
     if len(shape) != 2:
         raise ValueError("topk_ids must be int32 [T, K]")
     K = shape[1]
-    ids = _dense(topk_ids, "topk_ids", torch.int32, (T, K), logits)
-    off, lens, S = _sequences(seq_offsets, seq_lens, logits)
-    res, ptr = {}, {}
-    given = out or {}
-    for key, dtype, size in (("loss", torch.float32, (S,)),
-                             ("counts", torch.int32, (S, E)),
-                             ("probs", torch.float32, (S, E)),
-                             ("z_loss", torch.float32, (S,))):
-        if key == "z_loss" and not z_loss:
-            continue
-        t = given.get(key)
+    dev = logits.get_device()
+    ids = _dense_on(topk_ids, "topk_ids", torch.int32, (T, K), logits, dev)
+    off, lens, S = _sequences(seq_offsets, seq_lens, logits, dev)
+    get = (out or {}).get
+
+    def output(key, dtype, size):
+        t = get(key)
         if t is None:
             t = torch.empty(size, dtype=dtype, device=logits.device)
-        ptr[key] = _dense(t, "out[%r]" % key, dtype, size, logits)
-        res[key] = t
-    need = lib().moe_balance_loss_workspace_bytes(T, E, S)
+        return t, _dense_on(t, key, dtype, size, logits, dev)
+
+    loss, loss_p = output("loss", torch.float32, (S,))
+    cnt, cnt_p = output("counts", torch.int32, (S, E))
+    probs, probs_p = output("probs", torch.float32, (S, E))
+    res = {"loss": loss, "counts": cnt, "probs": probs}
+    z_p = None
+    if z_loss:
+        res["z_loss"], z_p = output("z_loss", torch.float32, (S,))
     if workspace is None:
         ws, size = None, 0
+        need = moe_balance_loss_workspace_bytes(T, E, S)
         if need:
             workspace = torch.empty(need, dtype=torch.uint8,
                                     device=logits.device)
@@ -539,8 +555,8 @@ def moe_balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor,
             raise ValueError("workspace must be a contiguous uint8 tensor")
         ws, size = workspace.data_ptr() or None, workspace.numel()
     _call("moe_balance_loss", logits, p, OUT_DTYPES[logits.dtype], ld, ids, T,
-          E, K, SCORE_FNS[scoring], off, lens, S, ptr["loss"],
-          ptr.get("z_loss"), ptr["counts"], ptr["probs"], ws, size)
+          E, K, SCORE_FNS[scoring], off, lens, S, loss_p, z_p, cnt_p, probs_p,
+          ws, size)
     return res
 
 
@@ -562,15 +578,16 @@ def moe_balance_loss_backward(grad_loss: torch.Tensor | None,
     ``grad_logits`` itself."""
     p, T, E, ld = _matrix(logits, "logits", OUT_DTYPES)
     dtype = (logits.dtype,)
-    off, lens, S = _sequences(seq_offsets, seq_lens, logits)
-    g = None if grad_loss is None else _dense(
-        grad_loss, "grad_loss", torch.float32, (S,), logits)
-    gz = None if grad_z is None else _dense(
-        grad_z, "grad_z", torch.float32, (S,), logits)
+    dev = logits.get_device()
+    off, lens, S = _sequences(seq_offsets, seq_lens, logits, dev)
+    g = None if grad_loss is None else _dense_on(
+        grad_loss, "grad_loss", torch.float32, (S,), logits, dev)
+    gz = None if grad_z is None else _dense_on(
+        grad_z, "grad_z", torch.float32, (S,), logits, dev)
     if grad_loss is None and grad_z is None:
         raise ValueError("grad_loss or grad_z must be given")
-    c = None if counts is None else _dense(counts, "counts", torch.int32,
-                                           (S, E), logits)
+    c = None if counts is None else _dense_on(
+        counts, "counts", torch.int32, (S, E), logits, dev)
     a, ld_a = None, 0
     if add is not None:
         a, rows, cols, ld_a = _matrix(add, "add", dtype, logits)
@@ -1211,13 +1228,16 @@ def _matmul4_inputs(q, scales, w, w_scales, expert_offsets, counts, fmt, act,
     q_p, rows, cols, ld_q = _matrix(q, "q", _BYTES if per_byte == 2 else _FP8)
     H = cols * per_byte
     s_p, ld_s = _output(scales, "scales", _SCALE, rows, H // 32, q)
-    _dev(w, "w", q)
+    dev = q.get_device()
     shape = w.shape
+    if w.get_device() != dev:
+        _dev(w, "w", q)
     if w.dtype not in _BYTES or len(shape) != 3 or shape[2] != H // 2 or \
             not w.is_contiguous():
         raise ValueError("w must be contiguous MXFP4 [E, N, %d]" % (H // 2))
     E, N, _ = shape
-    _dev(w_scales, "w_scales", q)
+    if w_scales.get_device() != dev:
+        _dev(w_scales, "w_scales", q)
     groups = H // 32
     if w_scales.dtype not in _SCALE or w_scales.shape != (E, N, groups):
         raise ValueError("w_scales must be uint8 %s" % ([E, N, groups],))
@@ -1226,21 +1246,23 @@ def _matmul4_inputs(q, scales, w, w_scales, expert_offsets, counts, fmt, act,
     if N == 1:
         ld_ws = ld_e if E > 1 else -(-groups // 4) * 4
     last = (E * N - 1) * ld_ws + -(-groups // 4) * 4
+    ws = w_scales.data_ptr()
     if ld_ws % 4 or ld_ws < groups or (groups > 1 and step != 1) or \
-            (E > 1 and ld_e != N * ld_ws) or w_scales.data_ptr() % 4 or \
+            (E > 1 and ld_e != N * ld_ws) or ws % 4 or \
             w_scales.storage_offset() + last > \
             w_scales.untyped_storage().nbytes():
         raise ValueError("rows of w_scales must follow one another at a "
                          "stride that is a multiple of 4 bytes, all of which "
                          "are there (as mxfp4_quant_rows returns them)")
-    off = _dense(expert_offsets, "expert_offsets", torch.int32, (E + 1,), q)
-    cnt = _dense(counts, "counts", torch.int32, (E,), q)
-    b = None if bias is None else _dense(bias, "bias", torch.float32, (E, N),
-                                         q)
+    off = _dense_on(expert_offsets, "expert_offsets", torch.int32, (E + 1,),
+                    q, dev)
+    cnt = _dense_on(counts, "counts", torch.int32, (E,), q, dev)
+    b = None if bias is None else _dense_on(bias, "bias", torch.float32,
+                                            (E, N), q, dev)
     if expected_m is None:
         expected_m = -(-rows // E) if E else 0
     args = (q_p, ld_q, s_p, ld_s, rows, code, w.data_ptr() or None,
-            w_scales.data_ptr() or None, ld_ws, E, N, H, off, cnt, b,
+            ws or None, ld_ws, E, N, H, off, cnt, b,
             ACTIVATIONS[act])
     return args, rows, N // 2 if act == "silu_mul" else N, expected_m
 

@@ -59,6 +59,7 @@ extern "C" {
 #define MXQ_MAX_MATMUL_LD (1 << 22) /* moe_expert_matmul: row strides, bytes */
 #define MXQ_MAX_MATMUL_ROWS ((1ll << 31) - (1 << 16)) /* moe_expert_matmul */
 #define MXQ_MAX_ROUTE_EXPERTS 1024 /* moe_route: global experts of a row */
+#define MXQ_MAX_BALANCE_TOKENS ((1ll << 31) - (1 << 16)) /* tokens, choices */
 /* Static device scratch of moe_layout_noalloc, per device (1 MiB). */
 #define MXQ_LAYOUT_NOALLOC_SCRATCH_BYTES (1u << 20)
 
@@ -183,7 +184,7 @@ mxq_status moe_route_backward(const float* grad_weights, const void* logits,
                               void* stream);
 
 /* Workspace bytes moe_balance_loss needs: 0 where few tokens take one launch
- * (up to 64 of more than 128 experts, 1024 of up to 16).  Pure host function;
+ * (up to 1024 of 16 experts, 256 of 256, 64 of 1024).  Pure host function;
  * 0 for sizes that moe_balance_loss refuses. */
 size_t moe_balance_loss_workspace_bytes(int64_t T, int32_t E, int32_t S);
 
@@ -214,7 +215,8 @@ size_t moe_balance_loss_workspace_bytes(int64_t T, int32_t E, int32_t S);
  *                and mean nothing afterwards.
  * Offsets and lengths are cut to the tokens that exist.  Sums are taken in a
  * fixed order, in fp32 within a block and 64 bits across.
- * T * K < 2^31 and E <= MXQ_MAX_ROUTE_EXPERTS, else MXQ_ERR_UNSUPPORTED. */
+ * T * K <= MXQ_MAX_BALANCE_TOKENS and E <= MXQ_MAX_ROUTE_EXPERTS, else
+ * MXQ_ERR_UNSUPPORTED. */
 mxq_status moe_balance_loss(const void* logits, mxq_out_dtype dtype,
                             int64_t ld_logits, const int32_t* topk_ids,
                             int64_t T, int32_t E, int32_t K,
@@ -239,7 +241,8 @@ mxq_status moe_balance_loss(const void* logits, mxq_out_dtype dtype,
  *                row are written, those of tokens in no sequence with add
  *                (or 0).  Must not overlap logits, and add only where it is
  *                the same rows.
- * Dead logits (-inf, NaN) get add (or 0). */
+ * Dead logits (-inf, NaN) get add (or 0).  T <= MXQ_MAX_BALANCE_TOKENS, else
+ * MXQ_ERR_UNSUPPORTED. */
 mxq_status moe_balance_loss_backward(
     const float* grad_loss, const float* grad_z, const void* logits,
     mxq_out_dtype dtype, int64_t ld_logits, const int32_t* counts, int64_t T,

@@ -39,7 +39,8 @@ def test_balance_loss(mxq):
     assert call(S=(1 << 31) - 1) == UNSUPPORTED
     need = mxq.moe_balance_loss_workspace_bytes(4000, 64, 3)
     assert need > 0 and call(size=need - 1) == WORKSPACE
-    for bad in (dict(T=-1), dict(T=1 << 31), dict(E=0), dict(K=0), dict(K=65),
+    assert call(T=1 << 31, K=1) == UNSUPPORTED
+    for bad in (dict(T=-1), dict(E=0), dict(K=0), dict(K=65),
                 dict(S=0), dict(off=None), dict(ld=63), dict(x=None),
                 dict(ids=None), dict(loss=None), dict(counts=None),
                 dict(probs=None), dict(ws=None), dict(ws=FAKE + 8)):
@@ -48,11 +49,11 @@ def test_balance_loss(mxq):
 
 def test_balance_loss_workspace(mxq):
     f = mxq.moe_balance_loss_workspace_bytes
-    assert f(64, 256, 1) == 0 and f(1024, 16, 1000) == 0
-    assert f(65, 256, 1) > 0 and f(1025, 16, 1) > 0
+    assert f(256, 256, 1) == 0 and f(1024, 16, 1000) == 0
+    assert f(257, 256, 1) > 0 and f(1025, 16, 1) > 0
     assert f(0, 8, 1) == 0 and f(-1, 8, 1) == 0 and f(9, 1025, 1) == 0
     # no more with more tokens, once every block has some
-    assert f(1 << 20, 256, 4) == f(1 << 30, 256, 4) < 1 << 20 << 1
+    assert f(1 << 20, 256, 4) == f(1 << 30, 256, 4) < 1 << 21
     assert f(1 << 20, 256, 5) > f(1 << 20, 256, 4)
 
 
@@ -65,7 +66,8 @@ def test_balance_loss_backward(mxq):
     assert call(dt=2) == UNSUPPORTED
     assert call(score=2) == UNSUPPORTED
     assert call(E=1025, ld=1025, lda=1025, ldo=1025) == UNSUPPORTED
-    for bad in (dict(T=-1), dict(T=1 << 31), dict(E=0), dict(S=0),
+    assert call(T=1 << 31) == UNSUPPORTED
+    for bad in (dict(T=-1), dict(E=0), dict(S=0),
                 dict(off=None), dict(ld=63), dict(lda=63), dict(ldo=63),
                 dict(x=None), dict(out=None), dict(counts=None),
                 dict(g=None, gz=None)):
