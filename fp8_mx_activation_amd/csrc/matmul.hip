@@ -291,7 +291,7 @@ __global__ __launch_bounds__(256, 1) void matmul_tile_kernel(MatmulArgs a,
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   TileOf t;
   if (!find_tile<TM>(a, tiles_n, t)) return;
-  const ExpertRows er = expert_rows(a, t.e);
+  const ExpertRows er = t.rows;
   const int rows = min(er.count - t.m0, TM);  // live rows of this tile
   const int64_t row0 = er.first + t.m0;
   const int n0 = t.n * (GATED ? 128 : 256);

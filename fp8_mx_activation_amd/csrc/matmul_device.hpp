@@ -209,22 +209,29 @@ __device__ __forceinline__ v8i join(const v4i& a, const v4i& b) {
 // from device data; every wavefront finds its block's by itself.  Runs of
 // consecutive tiles go to one XCD (block b runs on XCD b % 8), and within a
 // run eight row tiles share a column of weights, so the 32 CUs of an XCD
-// read a window of 8 by 4 tiles through their L2.
+// read a window of 8 by 4 tiles through their L2.  SPREAD: a row tile's columns
+// one after the other, on all XCDs, where row tiles differ in what they take and
+// weights are read once either way.
 struct TileOf {
   int e, m0, n;
+  ExpertRows rows;  // of expert e
 };
 
 constexpr int kGroupM = 8;
 
-template <int TM>
+template <int TM, bool SPREAD = false>
 __device__ __forceinline__ bool find_tile(const MatmulArgs& a, int tiles_n,
                                           TileOf& t) {
   const int lane = threadIdx.x & 63;
   const int per = (a.E + 63) / 64;  // experts per lane, consecutive
+  ExpertRows er{0, 0};
   int mine = 0;
   for (int i = 0; i < per; ++i) {
     const int e = lane * per + i;
-    if (e < a.E) mine += (expert_rows(a, e).count + TM - 1) / TM;
+    if (e < a.E) {
+      er = expert_rows(a, e);
+      mine += (er.count + TM - 1) / TM;
+    }
     // regions that do not overlap hold 2^24 tiles at most; more, of offsets
     // that no layout makes, must not overflow the sums
     mine = min(mine, 1 << 24);
@@ -238,24 +245,41 @@ __device__ __forceinline__ bool find_tile(const MatmulArgs& a, int tiles_n,
   const int tiles_m = __builtin_amdgcn_readlane(upto, 63);
   const int64_t total = (int64_t)tiles_m * tiles_n;
   const int64_t run = (total + 7) / 8;
-  const int64_t at = (int64_t)(blockIdx.x & 7) * run + (blockIdx.x >> 3);
-  if ((int64_t)(blockIdx.x >> 3) >= run || at >= total) return false;
-  const int64_t group = at / ((int64_t)kGroupM * tiles_n);
-  const int gm = min(kGroupM, tiles_m - (int)group * kGroupM);
-  const int in = (int)(at - group * kGroupM * tiles_n);
+  const int64_t at =
+      SPREAD ? (int64_t)blockIdx.x
+             : (int64_t)(blockIdx.x & 7) * run + (blockIdx.x >> 3);
+  if ((!SPREAD && (int64_t)(blockIdx.x >> 3) >= run) || at >= total)
+    return false;
+  constexpr int kGroup = SPREAD ? 1 : kGroupM;
+  const int64_t group = at / ((int64_t)kGroup * tiles_n);
+  const int gm = min(kGroup, tiles_m - (int)group * kGroup);
+  const int in = (int)(at - group * kGroup * tiles_n);
   t.n = in / gm;
-  const int m = (int)group * kGroupM + in % gm;
+  const int m = (int)group * kGroup + in % gm;
   const int owner = __ffsll((unsigned long long)__ballot(upto > m)) - 1;
   int first = __builtin_amdgcn_readlane(upto - mine, owner);
   int e = owner * per;
-  for (int i = 0; i < per; ++i) {
-    const int c = (expert_rows(a, owner * per + i).count + TM - 1) / TM;
-    e = owner * per + i;
-    if (m < first + c) break;
-    first += c;
+  if (per == 1) {
+    // the owner has read its one expert's rows
+    const uint64_t f = (uint64_t)er.first;
+    er.first = (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readlane(
+                             (int)(uint32_t)(f >> 32), owner)
+                         << 32 |
+                         (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)f,
+                                                             owner));
+    er.count = __builtin_amdgcn_readlane(er.count, owner);
+  } else {
+    for (int i = 0; i < per; ++i) {
+      e = owner * per + i;
+      er = expert_rows(a, e);
+      const int c = (er.count + TM - 1) / TM;
+      if (m < first + c) break;
+      first += c;
+    }
   }
   t.e = __builtin_amdgcn_readfirstlane(e);
   t.m0 = __builtin_amdgcn_readfirstlane((m - first) * TM);
+  t.rows = er;
   return true;
 }
 

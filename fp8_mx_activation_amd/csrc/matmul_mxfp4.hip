@@ -27,21 +27,94 @@ __device__ __forceinline__ v8i half(const v4i& a) {
   return __builtin_shufflevector(a, a, 0, 1, 2, 3, -1, -1, -1, -1);
 }
 
-// ------------------------------------------------------------ few rows
+// Up to 16 scale bytes of a row from byte `at` on, 127 behind the last of
+// `groups`.
+__device__ __forceinline__ u32x4 last_scales(const uint8_t* row, int at,
+                                             int groups) {
+  uint32_t v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] = 0x7F7F7F7Fu;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const int c = at + 4 * i + b;
+      if (c < groups)
+        v[i] = (v[i] & ~(0xFFu << (8 * b))) | ((uint32_t)row[c] << (8 * b));
+    }
+  }
+  return u32x4{v[0], v[1], v[2], v[3]};
+}
+
+// The end of few rows: token rows `rows` of them live, from row0 on, whose sums
+// over KS parts of K stand in part[ks][16 NT tokens][NB + 4]; gate rows are the
+// first half of the NB, their factors the second.
+template <int KS, int NB, int NT, int OUT>
+__device__ __forceinline__ void finish_few(const MatmulArgs& a, int e,
+                                           int64_t row0, int rows, int n0,
+                                           const float* part) {
+  constexpr int LDT = NB + 4;
+  const bool gated = a.act == kActSiluMul;
+  const int nbo = gated ? NB / 2 : NB;
+  const int lanes = nbo / 8;  // lanes per token
+  for (int i = threadIdx.x; i < 16 * NT * lanes; i += 256) {
+    if (NT > 1 && i / lanes >= (rows + 15) / 16 * 16) break;
+    const int tok = i / lanes;
+    const int c = i % lanes * 8;
+    float v[8];
+    auto sum = [&](int col, float (&o)[8]) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = 0.0f;
+#pragma unroll
+      for (int p = 0; p < KS; ++p) {
+        const float* src = part + (p * 16 * NT + tok) * LDT + col;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] += src[j];
+      }
+    };
+    const int col = n0 + c;
+    const bool in = col < a.NO;
+    sum(c, v);
+    if (a.bias != nullptr)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        v[j] += a.bias[(int64_t)e * a.N + min(col + j, a.NO - 1)];
+    if (gated) {
+      float u[8];
+      sum(nbo + c, u);
+      if (a.bias != nullptr)
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          u[j] += a.bias[(int64_t)e * a.N + a.NO + min(col + j, a.NO - 1)];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = silu(v[j]) * u[j];
+    } else if (a.act == kActSilu) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = silu(v[j]);
+    }
+    const bool live = in && tok < rows;
+    const int64_t row = row0 + min(tok, rows - 1);
+    u32x4 res{0, 0, 0, 0};
+    if constexpr (OUT == kOutBf16) res = load_residual(a, row, col);
+    store_channels<OUT>(a, row, col, live, v, res);
+  }
+}
+
+// ------------------------------------------------------------ few blocks
 //
-// With few rows an expert's weights are read once for all of them (16 at a
-// time), and the kernel is bound by that stream.  A block of four wavefronts
-// owns 64 NG weight rows of one expert and all rows of that expert; its
-// wavefronts take 64 weight rows each and, where NG < 4, split the K axis in
-// 4 / NG interleaved parts (neighbouring 128-byte lines are in flight at
-// once), joined in LDS at the end.
+// With few rows an expert's weights are read once for all of them, and the
+// kernels are bound by that stream.  Where few experts and few weight rows make
+// few blocks (up to 128 of 128 weight rows), a block of four wavefronts owns 64
+// weight rows of one expert and up to 16 of its rows at a time; its wavefronts
+// split the K axis in four interleaved parts (neighbouring 128-byte lines are
+// in flight at once), joined in LDS at the end.  One to four experts of 4096 x
+// 4096 with one row each: 11.1 us against 13.3 without the split.
 //
-// Each wavefront keeps a ring of three steps of 256 channels of its own in
-// LDS, filled by copies that bring whole lines of weights and need no
-// registers.  The weight rows are the MFMA's A operand, the token rows its B
-// operand: a lane ends up with four neighbouring output channels of one token.
-// Three steps; two of 8-bit rows whose scales, all of which are in LDS from the
-// start, leave no room for a third (above 20320 channels).
+// Each wavefront keeps a ring of steps of 256 channels of its own in LDS,
+// filled by copies that bring whole lines of weights and need no registers, and
+// no barrier orders them.  The weight rows are the MFMA's A operand, the token
+// rows its B operand: a lane ends up with four neighbouring output channels of
+// one token.  Three steps; two of 8-bit rows whose scales, all of which are in
+// LDS from the start, leave no room for a third (above 20320 channels).
 template <bool X8, int RING>
 struct SmallStep {
   static constexpr int kRow = X8 ? 256 : 128;  // bytes of a token row
@@ -70,12 +143,11 @@ __device__ __forceinline__ void copy4_to_lds(const v4i& buf, uint32_t lds,
 }
 #pragma clang diagnostic pop
 
-template <bool X8, int RING, int NG, int OUT>
+template <bool X8, int RING, int OUT>
 __global__ __launch_bounds__(256, 1) void matmul4_small_kernel(
     MatmulArgs a, int32_t blocks_n, int32_t ld_xs) {
   using St = SmallStep<X8, RING>;
-  constexpr int KS = 4 / NG;
-  constexpr int NB = 64 * NG;
+  constexpr int KS = 4, NB = 64;
   constexpr int LDT = NB + 4;  // floats per staged token
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int e = blockIdx.x / blocks_n;
@@ -86,7 +158,7 @@ __global__ __launch_bounds__(256, 1) void matmul4_small_kernel(
   const int n0 = (int)(blockIdx.x % blocks_n) * nbo;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int ng = wave / KS, ks = wave % KS;
+  const int ks = wave;
   const int r16 = lane & 15, g = lane >> 4;
   const int H = a.H;
   const int ld_w = H / 2;              // bytes of a weight row
@@ -110,13 +182,13 @@ __global__ __launch_bounds__(256, 1) void matmul4_small_kernel(
   uint32_t woff[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    woff[i] = (uint32_t)((weight_row(ng * 64 + 8 * i + (lane >> 3)) - n0) *
+    woff[i] = (uint32_t)((weight_row(8 * i + (lane >> 3)) - n0) *
                          ld_w);
   const v4i wbuf = buffer_of(a.w + ((int64_t)e * a.N + n0) * ld_w,
                              (uint32_t)((a.N - n0) * ld_w));
   // scales: lane l brings those of row l, four blocks at a time
   const uint32_t soff =
-      (uint32_t)((weight_row(ng * 64 + lane) - n0) * a.nbk);
+      (uint32_t)((weight_row(lane) - n0) * a.nbk);
   const v4i sbuf = buffer_of(a.ws + ((int64_t)e * a.N + n0) * a.nbk,
                              (uint32_t)((a.N - n0) * a.nbk));
 
@@ -246,50 +318,278 @@ __global__ __launch_bounds__(256, 1) void matmul4_small_kernel(
     float* part = reinterpret_cast<float*>(lds);
 #pragma unroll
     for (int f = 0; f < 4; ++f)
-      *reinterpret_cast<v4f*>(part + (ks * 16 + r16) * LDT + ng * 64 +
-                              f * 16 + 4 * g) = acc[f];
+      *reinterpret_cast<v4f*>(part + (ks * 16 + r16) * LDT + f * 16 +
+                              4 * g) = acc[f];
     __syncthreads();
-    const int lanes = nbo / 8;  // lanes per token
-    for (int i = threadIdx.x; i < 16 * lanes; i += 256) {
-      const int tok = i / lanes;
-      const int c = i % lanes * 8;
-      float v[8];
-      auto sum = [&](int col, float (&o)[8]) {
+    finish_few<KS, NB, 1, OUT>(a, e, row0, rows, n0, part);
+    __syncthreads();
+  }
+}
+
+// ------------------------------------------------------------ few rows
+//
+// Where there are blocks enough, a block's four wavefronts take 16 FW weight
+// rows each and share up to 16 NT token rows.  A step is 256 channels of all of
+// them.  The weights are a wavefront's own affair, as above; the token rows are
+// brought by all four, and one barrier a step says that they are there, and
+// that those of the step before may be overwritten.  Three steps are held: while
+// one is multiplied, two are on their way.
+//
+// FW = 2: blocks of 128 weight rows that fit a CU twice, so that the start and
+// the end of one (a chain of loads, the outputs) lie behind the other's stream.
+// FW = 4, NT = 4 (8-bit rows: 3): an expert's rows go through in one pass where
+// 16 or 32 at a time would read its weights twice.
+//
+// Scales come in chunks of 16 bytes per weight row, two steps' worth, copied
+// straight into LDS two steps ahead; what is left of a row behind whole chunks
+// is put there at the start, with 127 (a factor of one) for the blocks behind
+// the last.  The tokens' scales are all in LDS from the start of a pass.
+template <bool X8, int NT, int FW>
+struct Stream {
+  static constexpr int kRows = 64 * FW;    // weight rows of a block
+  static constexpr int kX = kRows * 128;   // bytes of a step's weights
+  static constexpr int kStage = kX + NT * 16 * (X8 ? 256 : 128);
+  static constexpr int kRing = 3;
+  static constexpr int kChunk = kRows * 16;  // scales: two in turn, the last
+  static constexpr int kScales = kRing * kStage;
+  static constexpr int kXScales = kScales + 3 * kChunk;
+  static constexpr int kCopiesX = NT * (X8 ? 4 : 2) / 4;  // of a wavefront
+  static_assert(NT * (X8 ? 4 : 2) % 4 == 0, "every wavefront copies as many");
+  static_assert(kScales >= NT * 16 * (kRows + 4) * 4,
+                "the sums fit the stages");
+};
+
+template <bool X8, int NT, int FW, int OUT>
+__global__ __launch_bounds__(256, 1) void matmul4_stream_kernel(
+    MatmulArgs a, int32_t blocks_n, int32_t ld_xs) {
+  using St = Stream<X8, NT, FW>;
+  constexpr int R = St::kRing, CX = St::kCopiesX, CW = 2 * FW;
+  constexpr int NB = St::kRows;
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  // every expert that holds rows is one tile of them all, so the blocks that
+  // have work come first and spread evenly
+  TileOf tile;
+  if (!find_tile<1 << 30, true>(a, blocks_n, tile)) return;
+  const int e = tile.e;
+  const ExpertRows er = tile.rows;
+  const bool gated = a.act == kActSiluMul;
+  const int nbo = gated ? NB / 2 : NB;
+  const int n0 = tile.n * nbo;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r16 = lane & 15, g = lane >> 4;
+  const int H = a.H;
+  const int ld_w = H / 2;           // bytes of a weight row
+  const int ld_x = X8 ? H : H / 2;  // and of a token row
+  const int groups = H / 32;
+  const int nsteps = (H + 255) / 256;
+  const int full = groups / 16;  // chunks of scales that end within the row
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(
+      __attribute__((address_space(3))) uint8_t*)lds;
+  uint8_t* scale = lds + St::kScales;
+  uint8_t* xscale = lds + St::kXScales;
+
+  // weight row (within the expert's matrix) of local row lr of the block
+  auto weight_row = [&](int lr) {
+    if (!gated) return min(n0 + lr, a.N - 1);
+    return lr < nbo ? min(n0 + lr, a.NO - 1)
+                    : a.NO + min(n0 + lr - nbo, a.NO - 1);
+  };
+  // weight copy i brings rows 8 i + (l >> 3); odd copies' chunks differ by 4
+  const int chunk0 = place(lane & 7, lane >> 3);
+  uint32_t woff[CW];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] = 0.0f;
+  for (int i = 0; i < CW; ++i)
+    woff[i] = (uint32_t)((weight_row(wave * 16 * FW + 8 * i + (lane >> 3)) - n0) *
+                         ld_w);
+  const v4i wbuf = buffer_of(a.w + ((int64_t)e * a.N + n0) * ld_w,
+                             (uint32_t)((a.N - n0) * ld_w));
+  const uint32_t soff =
+      (uint32_t)((weight_row(min(wave * 64 + lane, NB - 1)) - n0) * a.nbk);
+  const v4i sbuf = buffer_of(a.ws + ((int64_t)e * a.N + n0) * a.nbk,
+                             (uint32_t)((a.N - n0) * a.nbk));
+  // In a last step that ends inside the 256 channels, chunks past H repeat
+  // the step's first: in bounds, and cleared when they are read.
+  auto copy_w = [&](int i) {
+    const int k0 = i * 128;
+    const uint32_t at =
+        lds0 + (uint32_t)(i % R) * St::kStage + (uint32_t)wave * 2048 * FW;
+    const int c1 = chunk0 ^ 4;
+    const uint32_t o0 = k0 + 16 * chunk0 < ld_w ? 16 * chunk0 : 0;
+    const uint32_t o1 = k0 + 16 * c1 < ld_w ? 16 * c1 : 0;
 #pragma unroll
-        for (int p = 0; p < KS; ++p) {
-          const float* src = part + (p * 16 + tok) * LDT + col;
+    for (int j = 0; j < CW; ++j)
+      copy_to_lds(wbuf, at + j * 1024, woff[j] + (j & 1 ? o1 : o0), k0);
+  };
+  // 64 weight rows' by a wavefront: of 128 rows, by two
+  auto copy_scales = [&](int j) {
+    if (wave >= FW) return;
+    copy_to_lds(sbuf,
+                lds0 + St::kScales + (j & 1) * St::kChunk + wave * 1024, soff,
+                j * 16);
+  };
+  if (groups % 16 != 0 && (int)threadIdx.x < NB) {
+    const uint8_t* p =
+        a.ws + ((int64_t)e * a.N + weight_row(threadIdx.x)) * a.nbk;
+    *reinterpret_cast<u32x4*>(scale + 2 * St::kChunk + threadIdx.x * 16) =
+        last_scales(p, full * 16, groups);
+  }
+
+  for (int base = 0; base < er.count; base += 16 * NT) {
+    const int rows = min(er.count - base, 16 * NT);
+    const int64_t row0 = er.first + base;
+    const v4i xbuf = buffer_of(a.q + row0 * a.ld_q,
+                               (uint32_t)((rows - 1) * a.ld_q + ld_x));
+    // token copy c brings 8 rows' 128 bytes; of 8-bit rows the first 2 NT
+    // copies are the first halves, the others the second
+    uint32_t xoff[CX];
+    int xchunk[CX];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) o[j] += src[j];
-        }
-      };
-      const int col = n0 + c;
-      const bool in = col < a.NO;
-      sum(c, v);
-      if (a.bias != nullptr)
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          v[j] += a.bias[(int64_t)e * a.N + min(col + j, a.NO - 1)];
-      if (gated) {
-        float u[8];
-        sum(nbo + c, u);
-        if (a.bias != nullptr)
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            u[j] += a.bias[(int64_t)e * a.N + a.NO + min(col + j, a.NO - 1)];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = silu(v[j]) * u[j];
-      } else if (a.act == kActSilu) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = silu(v[j]);
-      }
-      const bool live = in && tok < rows;
-      const int64_t row = row0 + min(tok, rows - 1);
-      u32x4 res{0, 0, 0, 0};
-      if constexpr (OUT == kOutBf16) res = load_residual(a, row, col);
-      store_channels<OUT>(a, row, col, live, v, res);
+    for (int i = 0; i < CX; ++i) {
+      const int c = wave * CX + i;
+      const int r = c % (2 * NT) * 8 + (lane >> 3);
+      xoff[i] = (uint32_t)(min(r, rows - 1) * (int)a.ld_q);
+      xchunk[i] = place(lane & 7, r) + (c >= 2 * NT ? 8 : 0);
     }
+    auto copy_x = [&](int k) {
+      const int k0 = k * (X8 ? 256 : 128);
+#pragma unroll
+      for (int i = 0; i < CX; ++i)
+        copy_to_lds(xbuf,
+                    lds0 + (uint32_t)(k % R) * St::kStage + St::kX +
+                        (uint32_t)(wave * CX + i) * 1024,
+                    xoff[i] + (k0 + 16 * xchunk[i] < ld_x ? 16 * xchunk[i]
+                                                          : 0),
+                    k0);
+    };
+    {
+      const int words = (groups + 3) / 4;
+      for (int i = threadIdx.x; i < rows * words; i += 256) {
+        const uint8_t* p = a.s + (row0 + i / words) * a.ld_s;
+        const int c = i % words * 4;
+        uint32_t v = 0x7F7F7F7Fu;
+        if (c + 4 <= groups)
+          __builtin_memcpy(&v, p + c, 4);
+        else
+          for (int b = c; b < groups; ++b)
+            v = (v & ~(0xFFu << (8 * (b & 3)))) |
+                ((uint32_t)p[b] << (8 * (b & 3)));
+        *reinterpret_cast<uint32_t*>(xscale + i / words * ld_xs + c) = v;
+      }
+    }
+    if (full > 0) copy_scales(0);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      if (i < nsteps) copy_w(i);
+      if (i < nsteps && i < R - 1) copy_x(i);
+    }
+
+    v4f acc[FW][NT];
+#pragma unroll
+    for (int f = 0; f < FW; ++f)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) acc[f][t] = v4f{0, 0, 0, 0};
+
+    for (int i = 0; i < nsteps; ++i) {
+      // this step's weights, tokens and scales have landed: what follows them
+      // are the next two steps' weights and the next one's tokens
+      if (i + 2 < nsteps)
+        landed_barrier<2 * CW + CX, 0>();
+      else if (i + 1 < nsteps)
+        landed_barrier<CW + CX, 0>();
+      else
+        landed_barrier<0, 0>();
+      if (i + R - 1 < nsteps) copy_x(i + R - 1);
+      const uint8_t* at = lds + i % R * St::kStage;
+      const uint8_t* sc =
+          scale + (i / 2 == full ? 2 : i / 2 & 1) * St::kChunk + (i & 1) * 8;
+      v4i w[FW][2], x[NT][2], x8[NT][2];
+      uint32_t sw[FW][2], sx[NT][2];
+#pragma unroll
+      for (int f = 0; f < FW; ++f) {
+        const int r = wave * 16 * FW + f * 16 + r16;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          w[f][h] = *reinterpret_cast<const v4i*>(
+              at + r * 128 + place(4 * h + g, r16) * 16);
+        const uint2 v = *reinterpret_cast<const uint2*>(sc + r * 16);
+        sw[f][0] = v.x;
+        sw[f][1] = v.y;
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint8_t* xr = at + St::kX + (t * 16 + r16) * 128;
+          if constexpr (X8) {
+            xr += h * NT * 2048;
+            x[t][h] = *reinterpret_cast<const v4i*>(xr + place(g, r16) * 16);
+            x8[t][h] =
+                *reinterpret_cast<const v4i*>(xr + place(4 + g, r16) * 16);
+          } else {
+            x[t][h] = *reinterpret_cast<const v4i*>(
+                xr + place(4 * h + g, r16) * 16);
+          }
+          sx[t][h] = *reinterpret_cast<const uint32_t*>(
+              xscale + (t * 16 + r16) * ld_xs + i * 8 + 4 * h);
+        }
+      wait_for<63, 0>();  // read: the weights' place may be filled again
+      if ((i & 1) == 0 && i / 2 + 1 < full) copy_scales(i / 2 + 1);
+      if (i + R < nsteps) copy_w(i + R);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int f = 0; f < FW; ++f) sw[f][h] >>= 8 * g;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) sx[t][h] >>= 8 * g;
+      }
+      if (i * 256 + 256 > H) {
+        // blocks past H: zeros, whose scales have to be finite ones
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int k = i * 256 + 128 * h;
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            if (k + (X8 ? 16 : 32) * g >= H) x[t][h] = v4i{0, 0, 0, 0};
+            if (X8 && k + 64 + 16 * g >= H) x8[t][h] = v4i{0, 0, 0, 0};
+            if (k + 32 * g >= H) sx[t][h] = 127;
+          }
+          if (k + 32 * g < H) continue;
+#pragma unroll
+          for (int f = 0; f < FW; ++f) {
+            w[f][h] = v4i{0, 0, 0, 0};
+            sw[f][h] = 127;
+          }
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        if (t > 0 && rows <= 16 * t) continue;  // the same for all wavefronts
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int f = 0; f < FW; ++f)
+            acc[f][t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                half(w[f][h]), X8 ? join(x[t][h], x8[t][h]) : half(x[t][h]),
+                acc[f][t], kFmtFp4, X8 ? kFmtFp8 : kFmtFp4, 0, (int)sw[f][h],
+                0, (int)sx[t][h]);
+      }
+    }
+
+    // over the stages: part[token][channel]
+    __syncthreads();
+    float* part = reinterpret_cast<float*>(lds);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      if (rows <= 16 * t) continue;
+#pragma unroll
+      for (int f = 0; f < FW; ++f)
+        *reinterpret_cast<v4f*>(part + (t * 16 + r16) * (NB + 4) +
+                                wave * 16 * FW +
+                                f * 16 + 4 * g) = acc[f][t];
+    }
+    __syncthreads();
+    finish_few<1, NB, NT, OUT>(a, e, row0, rows, n0, part);
     __syncthreads();
   }
 }
@@ -358,7 +658,7 @@ __global__ __launch_bounds__(256, 1) void matmul4_tile_kernel(
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   TileOf t;
   if (!find_tile<TM>(a, tiles_n, t)) return;
-  const ExpertRows er = expert_rows(a, t.e);
+  const ExpertRows er = t.rows;
   const int rows = min(er.count - t.m0, TM);  // live rows of this tile
   const int64_t row0 = er.first + t.m0;
   const int n0 = t.n * (GATED ? 128 : 256);
@@ -482,22 +782,6 @@ __global__ __launch_bounds__(256, 1) void matmul4_tile_kernel(
     *reinterpret_cast<u32x4*>(scale + (j & 1) * T::kChunk + threadIdx.x * 16) =
         u32x4{xs_next[0], xs_next[1], xs_next[2], xs_next[3]};
   };
-  // the bytes that are left of row p, 127 behind them
-  auto last_scales = [&](const uint8_t* p, int at) {
-    uint32_t v[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[i] = 0x7F7F7F7Fu;
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const int c = full * 16 + 4 * i + b;
-        if (c < groups)
-          v[i] = (v[i] & ~(0xFFu << (8 * b))) | ((uint32_t)p[c] << (8 * b));
-      }
-    }
-    *reinterpret_cast<u32x4*>(scale + 2 * T::kChunk + at * 16) =
-        u32x4{v[0], v[1], v[2], v[3]};
-  };
   constexpr int kWords = X8 ? 1 : 2;  // of a row's scales in a step
   uint32_t sx[XF][kWords], sw[4][kWords], sx1[XF][kWords], sw1[4][kWords];
   auto read_scales = [&](int k) {
@@ -592,9 +876,12 @@ __global__ __launch_bounds__(256, 1) void matmul4_tile_kernel(
   if (full > 0) copy_scales(0);
   copy_all(0);
   if (groups % 16 != 0) {
-    if ((int)threadIdx.x < TM) last_scales(xs_row, threadIdx.x);
-    last_scales(a.ws + ((int64_t)t.e * a.N + weight_row(threadIdx.x)) * a.nbk,
-                TM + threadIdx.x);
+    u32x4* d = reinterpret_cast<u32x4*>(scale + 2 * T::kChunk);
+    if ((int)threadIdx.x < TM)
+      d[threadIdx.x] = last_scales(xs_row, full * 16, groups);
+    d[TM + threadIdx.x] = last_scales(
+        a.ws + ((int64_t)t.e * a.N + weight_row(threadIdx.x)) * a.nbk,
+        full * 16, groups);
   }
   if (!xs_words && full > 0) {
     fetch_scales(0);
@@ -701,21 +988,20 @@ __global__ __launch_bounds__(256, 1) void matmul4_tile_kernel(
 
 constexpr int kLds = 160 * 1024;  // of a CU
 
-template <bool X8, int RING, int NG, int OUT>
+template <bool X8, int RING, int OUT>
 mxq_status launch_small(const MatmulArgs& a, hipStream_t s) {
   using St = SmallStep<X8, RING>;
-  const int nbo = a.act == kActSiluMul ? 32 * NG : 64 * NG;
+  const int nbo = a.act == kActSiluMul ? 32 : 64;
   const int64_t bn = ceil_div(a.NO, nbo);
   if (bn * a.E > max_blocks(256)) return MXQ_ERR_UNSUPPORTED;
   const int ld_xs = small_scale_ld(a.H / 32);
   const int lds = St::kRings + 16 * ld_xs;
   if constexpr (RING == 3) {
-    if (lds > kLds) return launch_small<X8, 2, NG, OUT>(a, s);
+    if (lds > kLds) return launch_small<X8, 2, OUT>(a, s);
   }
-  static_assert(St::kRings >= 4 * 16 * (64 + 4) * 4 &&
-                    St::kRings >= 16 * (256 + 4) * 4,
+  static_assert(St::kRings >= 4 * 16 * (64 + 4) * 4,
                 "the joined K parts fit the rings");
-  auto* k = &matmul4_small_kernel<X8, RING, NG, OUT>;
+  auto* k = &matmul4_small_kernel<X8, RING, OUT>;
   if (hipFuncSetAttribute(reinterpret_cast<const void*>(k),
                           hipFuncAttributeMaxDynamicSharedMemorySize,
                           lds) != hipSuccess) {
@@ -724,6 +1010,33 @@ mxq_status launch_small(const MatmulArgs& a, hipStream_t s) {
   }
   k<<<(unsigned)(bn * a.E), 256, lds, s>>>(a, (int32_t)bn, ld_xs);
   return launch_status();
+}
+
+template <bool X8, int NT, int FW, int OUT>
+mxq_status launch_stream(const MatmulArgs& a, hipStream_t s) {
+  using St = Stream<X8, NT, FW>;
+  static_assert(FW == 4 || St::kXScales + 16 * NT * (MXQ_MAX_HIDDEN / 32 + 4) <=
+                               kLds,
+                "rows of any length fit");
+  const int64_t bn = ceil_div(a.NO, a.act == kActSiluMul ? 32 * FW : 64 * FW);
+  if (bn * a.E > max_blocks(256)) return MXQ_ERR_UNSUPPORTED;
+  const int ld_xs = small_scale_ld(a.H / 32);
+  const int lds = St::kXScales + 16 * NT * ld_xs;
+  auto* k = &matmul4_stream_kernel<X8, NT, FW, OUT>;
+  if (hipFuncSetAttribute(reinterpret_cast<const void*>(k),
+                          hipFuncAttributeMaxDynamicSharedMemorySize,
+                          lds) != hipSuccess) {
+    (void)hipGetLastError();
+    return MXQ_ERR_HIP;
+  }
+  k<<<(unsigned)(bn * a.E), 256, lds, s>>>(a, (int32_t)bn, ld_xs);
+  return launch_status();
+}
+
+// Whether a pass of 16 NT rows and all their scales fit a CU.
+template <bool X8, int NT, int FW>
+bool stream_fits(const MatmulArgs& a) {
+  return Stream<X8, NT, FW>::kXScales + 16 * NT * small_scale_ld(a.H / 32) <= kLds;
 }
 
 template <bool X8, int XF, int OUT>
@@ -749,19 +1062,41 @@ mxq_status launch_tile(const MatmulArgs& a, hipStream_t s) {
   return launch_status();
 }
 
+// The kernel for `expected` rows in a busy expert.  Measured with top-2
+// routings over 32 experts whose fullest holds 2.6 times the mean, gate/up
+// (4096 x 7168) and down (7168 x 2048) of 4-bit rows (and 8-bit ones), us:
+//   mean rows               4         8         12.5       25
+//   few rows, FW = 2     76, 41    88, 49    103, 54
+//               (8-bit)  83, 43   107, 54    131, 63
+//             FW = 4     80, 46    87, 55     94, 59    134, 73
+//               (8-bit)  82, 47    90, 57    106, 62    158, 82
+//   128-row tile        110, 59   114, 73    119, 81    124, 86
+//               (8-bit) 115, 60   120, 76    125, 84    133, 89
+// (the weights alone take 94 and 47 us at 5.3 TB/s; with few rows experts are
+// left out, and the last-level cache holds a part).  A 128-row tile of 8-bit
+// rows takes 0.6 of a 256-row one's time, both one to a CU, so the smaller one
+// is taken where that many rounds of the 256 CUs are over sooner; the same rule
+// serves 4-bit rows.
 template <bool X8, int OUT>
 mxq_status launch(const MatmulArgs& a, int64_t expected, hipStream_t s) {
   constexpr int64_t kCus = 256;
-  if (expected > 12) {
-    const int64_t columns =
-        a.E * ceil_div(a.NO, a.act == kActSiluMul ? 128 : 256);
-    const int64_t rounds4 = ceil_div(columns * ceil_div(expected, 256), kCus);
-    const int64_t rounds2 = ceil_div(columns * ceil_div(expected, 128), kCus);
-    return rounds2 * 3 <= rounds4 * 5 ? launch_tile<X8, 2, OUT>(a, s)
-                                      : launch_tile<X8, 4, OUT>(a, s);
+  constexpr int64_t kFew = X8 ? 4 : 12, kMore = 20, kSmall = 12;
+  constexpr int kWide = X8 ? 3 : 4;
+  const bool few_blocks = ceil_div(a.N, 128) * a.E <= kCus / 2;
+  if (few_blocks && expected <= kSmall) return launch_small<X8, 3, OUT>(a, s);
+  if (!few_blocks && expected <= kMore) {
+    if (expected > kFew && ceil_div(a.N, 256) * a.E >= kCus &&
+        stream_fits<X8, kWide, 4>(a))
+      return launch_stream<X8, kWide, 4, OUT>(a, s);
+    if (expected <= kSmall || !X8)
+      return launch_stream<X8, X8 ? 1 : 2, 2, OUT>(a, s);
   }
-  if (ceil_div(a.N, 256) * a.E >= 256) return launch_small<X8, 3, 4, OUT>(a, s);
-  return launch_small<X8, 3, 1, OUT>(a, s);
+  const int64_t columns =
+      a.E * ceil_div(a.NO, a.act == kActSiluMul ? 128 : 256);
+  const int64_t rounds4 = ceil_div(columns * ceil_div(expected, 256), kCus);
+  const int64_t rounds2 = ceil_div(columns * ceil_div(expected, 128), kCus);
+  return rounds2 * 3 <= rounds4 * 5 ? launch_tile<X8, 2, OUT>(a, s)
+                                    : launch_tile<X8, 4, OUT>(a, s);
 }
 
 template <int OUT>

@@ -17,8 +17,10 @@ from gpu_util import DEV, f32_to_dev, host, i32_to_dev, say, u8_to_dev
 pytestmark = pytest.mark.gpu
 
 FMTS = ("mxfp4", "e8m0_g32")
-# hints that reach every kernel, whatever the rows really are
+# hints that reach every kernel of few blocks, whatever the rows really are,
+# and those of many
 HINTS = (1, 13, 200, 1 << 20)
+MANY_HINTS = (1, 7, 13, 18)
 
 
 class Problem:
@@ -140,6 +142,64 @@ def test_exact_sums(counts, N, H, fmt, act):
                 residual=True, exact=True)
     say("mxfp4 exact sums", counts, N, H, fmt, act)
     check_bf16(p, exact=act == "none")
+
+
+# 140 experts: more blocks than CUs, of 128 weight rows and of 256
+MANY = [(0, 1, 16, 17, 3, 33, 48, 49, 0, 64, 65, 2)[i % 12]
+        for i in range(140)]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("act", ["none", "silu_mul"])
+@pytest.mark.parametrize("N,H", [(272, 32), (400, 224), (520, 512),
+                                 (264, 1056)])
+def test_many_blocks(N, H, act, fmt):
+    p = Problem(N + H, MANY, N, H, fmt, act, bias=True, residual=True, pad=2,
+                exact=True)
+    say("mxfp4 many blocks", N, H, act, fmt)
+    check_bf16(p, MANY_HINTS, exact=act == "none")
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("out_fmt", FMTS)
+@pytest.mark.parametrize("act,N", [("none", 288), ("silu_mul", 576)])
+def test_many_blocks_quantized(act, N, out_fmt, fmt):
+    say("mxfp4 many blocks, quantized", act, N, out_fmt, fmt)
+    check_quant(Problem(3, MANY, N, 416, fmt, act, bias=True, pad=1), out_fmt,
+                MANY_HINTS)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("hint", MANY_HINTS)
+def test_many_blocks_device_data_and_strides(hint, fmt):
+    """Offsets and counts that no layout makes, scales of tokens that start
+    on no word, NaN of one row and one weight row."""
+    p = Problem(5, MANY, 272, 352, fmt, exact=True)
+    p.s[int(p.offsets[3]) + 4, 5] = 255
+    p.ws[7, 200, 10] = 255
+    d = p.dev()
+    d["scales"], _ = wide(d["scales"], 3, 2)
+    d["q"], _ = wide(d["q"], 16, 32)
+    out = mxq.moe_expert_matmul_mxfp4(**d, expected_m=hint).cpu()
+    nan = torch.isnan(out) & torch.from_numpy(p.live)[:, None]
+    a, n = int(p.offsets[7]), int(p.counts[7])
+    want = torch.zeros_like(nan)
+    want[int(p.offsets[3]) + 4] = True
+    want[a:a + n, 200] = True
+    assert torch.equal(nan, want)
+    counts, offsets = p.counts.copy(), p.offsets.copy()
+    counts[0], counts[5], counts[9] = -3, 1 << 30, 1 << 30
+    offsets[20] = -7
+    offsets[30] = p.rows + 50
+    d["counts"], d["expert_offsets"] = i32_to_dev(counts), i32_to_dev(offsets)
+    out = torch.full((p.rows + 4, p.cols), 5.0, dtype=torch.bfloat16,
+                     device=DEV)
+    mxq.moe_expert_matmul_mxfp4(**d, out=out, expected_m=hint)
+    live = np.zeros(p.rows + 4, bool)
+    for e in range(p.E):
+        a, n = ref.live_rows(offsets, counts, p.rows, e)
+        live[a:a + n] = n > 0
+    assert (out.cpu().double().numpy()[~live] == 5).all()
 
 
 @pytest.mark.parametrize("fmt", FMTS)
@@ -318,10 +378,13 @@ def test_shapes_at_the_ends(fmt):
     check_bf16(Problem(43, [1], 8, 32, fmt, exact=True), exact=True)
     check_bf16(Problem(44, [3], 4, 32, fmt, exact=True), exact=True)
     counts = [(i * 7) % 4 for i in range(1024)]
-    check_bf16(Problem(47, counts, 8, 32, fmt, pad=1, exact=True), exact=True)
+    check_bf16(Problem(47, counts, 8, 32, fmt, pad=1, exact=True),
+               HINTS + MANY_HINTS, exact=True)
     # the widest rows
     for H in (20320, 32768):
         check_bf16(Problem(48, [3, 40], 64, H, fmt, exact=True), exact=True)
+    check_bf16(Problem(49, [3, 40] * 65, 12, 32768, fmt, pad=0, exact=True),
+               MANY_HINTS, exact=True)
 
 
 def test_as_quantized():

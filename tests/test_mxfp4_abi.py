@@ -143,7 +143,7 @@ def test_expert_matmul(mxq, fmt, pay):
     # 2^32 threads: blocks of weight rows, tiles
     assert call(E=1024, N=1 << 24, H=32, ldq=32, lds=1,
                 ldo=1 << 24) == UNSUPPORTED
-    for m in (13, 1 << 30):
+    for m in (200, 1 << 30):
         assert call(rows=(1 << 31) - (1 << 16), E=1024, N=1024, H=32, ldq=32,
                     lds=1, m=m, ldo=1024) == UNSUPPORTED
     for bad in (dict(E=0), dict(E=1025), dict(N=0), dict(H=0), dict(H=48),
