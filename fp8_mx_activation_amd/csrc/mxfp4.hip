@@ -5,9 +5,9 @@
 //        floor(log2 amax) - 2
 //   q    = e2m1(x * 2^-e), nearest even; scale byte e + 127
 //
-// Every kernel is bound by what it reads and writes.  A lane owns eight
-// neighbouring channels: 16 bytes of bf16 or of e4m3's two lanes' worth, 4
-// bytes of codes; a group's four lanes are a DPP quad.
+// Every kernel is bound by what it reads and writes.  A lane owns 16
+// neighbouring channels, 32 bytes of bf16 and 8 of codes; a group's two lanes
+// are neighbours.
 #include <algorithm>
 
 #include "mxfp4_device.hpp"
@@ -18,47 +18,84 @@ namespace {
 using namespace mxq;
 
 constexpr int kThreads = 256;
-constexpr int kDepth = 4;  // units of eight channels a lane has in flight
-constexpr int kUnits = kThreads * kDepth;
+constexpr int kUnits = kThreads * 2;  // of 16 channels, of a block
 
-// Eight channels as fp32.
+// Sixteen channels as they lie in memory: 32 bytes of bf16, 64 of fp32.
 template <bool F32>
-__device__ __forceinline__ void load8(const void* row, int c, float (&v)[8]) {
-  if constexpr (F32) {
-    const float4* p = reinterpret_cast<const float4*>(
-        static_cast<const float*>(row) + c);
-    const float4 a = p[0], b = p[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  } else {
-    const u32x4 a = load16(static_cast<const uint16_t*>(row) + c);
-    v[0] = bf16_lo(a.x); v[1] = bf16_hi(a.x);
-    v[2] = bf16_lo(a.y); v[3] = bf16_hi(a.y);
-    v[4] = bf16_lo(a.z); v[5] = bf16_hi(a.z);
-    v[6] = bf16_lo(a.w); v[7] = bf16_hi(a.w);
-  }
+struct Raw16 {
+  u32x4 v[F32 ? 4 : 2];
+};
+
+template <bool F32>
+__device__ __forceinline__ Raw16<F32> load_raw(const void* row, int c) {
+  Raw16<F32> r;
+  const char* p = static_cast<const char*>(row) + (int64_t)c * (F32 ? 4 : 2);
+#pragma unroll
+  for (int i = 0; i < (F32 ? 4 : 2); ++i) r.v[i] = load16_nt(p + 16 * i);
+  return r;
 }
 
-// Calls f(slot, row, unit of the row) for the units of the block's rows that
-// this lane owns, kDepth at a time.  A group's units lie in one quad: all four
-// are there or none.
-template <typename Load, typename Use>
+// The codes of a lane's 16 channels, whose group it shares with its neighbour,
+// and the group's exponent.  Both lanes must be active.
+template <bool F32, int RULE>
+__device__ __forceinline__ uint2 quant16_e2m1(const Raw16<F32>& r, int& e) {
+  float a[8], b[8];
+  if constexpr (F32) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const u32x4 x = r.v[i], y = r.v[2 + i];
+      a[4 * i] = __uint_as_float(x.x);
+      a[4 * i + 1] = __uint_as_float(x.y);
+      a[4 * i + 2] = __uint_as_float(x.z);
+      a[4 * i + 3] = __uint_as_float(x.w);
+      b[4 * i] = __uint_as_float(y.x);
+      b[4 * i + 1] = __uint_as_float(y.y);
+      b[4 * i + 2] = __uint_as_float(y.z);
+      b[4 * i + 3] = __uint_as_float(y.w);
+    }
+  } else {
+    auto eight = [](const u32x4& w, float (&v)[8]) {
+      v[0] = bf16_lo(w.x); v[1] = bf16_hi(w.x);
+      v[2] = bf16_lo(w.y); v[3] = bf16_hi(w.y);
+      v[4] = bf16_lo(w.z); v[5] = bf16_hi(w.z);
+      v[6] = bf16_lo(w.w); v[7] = bf16_hi(w.w);
+    };
+    eight(r.v[0], a);
+    eight(r.v[1], b);
+  }
+  e = e2m1_exponent<RULE>(group_max<2>(max(absmax8(a), absmax8(b))));
+  const float f = pow2_neg(e);
+  return uint2{pack8_e2m1(a, f), pack8_e2m1(b, f)};
+}
+
+// Calls load and then use (slot, row, unit of the row) for the units (upr of
+// them in a row) of the block's rows that this lane owns, DEPTH at a time.  A
+// group's units lie in neighbouring lanes: all are there or none.
+template <int DEPTH, typename Load, typename Use>
 __device__ __forceinline__ void over_units(int64_t rows, int32_t upr,
                                            int32_t rpb, Load load, Use use) {
   const int64_t row0 = (int64_t)blockIdx.x * rpb;
   const int n = (int)min((int64_t)rpb, rows - row0) * upr;
-  for (int base = threadIdx.x; base < n; base += kUnits) {
+  for (int base = threadIdx.x; base < n; base += DEPTH * kThreads) {
+    int64_t r[DEPTH];
+    int u[DEPTH];
 #pragma unroll
-    for (int i = 0; i < kDepth; ++i) {
-      const int u = base + i * kThreads;
-      if (u < n) load(i, row0 + u / upr, u % upr);
+    for (int i = 0; i < DEPTH; ++i) {
+      const int at = base + i * kThreads;
+      r[i] = row0 + at / upr;
+      u[i] = at % upr;
+      if (at < n) load(i, r[i], u[i]);
     }
 #pragma unroll
-    for (int i = 0; i < kDepth; ++i) {
-      const int u = base + i * kThreads;
-      if (u < n) use(i, row0 + u / upr, u % upr);
-    }
+    for (int i = 0; i < DEPTH; ++i)
+      if (base + i * kThreads < n) use(i, r[i], u[i]);
   }
+}
+
+__device__ __forceinline__ void store8_nt(void* p, const uint2& v) {
+  uint32_t* d = reinterpret_cast<uint32_t*>(p);
+  __builtin_nontemporal_store(v.x, d);
+  __builtin_nontemporal_store(v.y, d + 1);
 }
 
 template <bool F32, int RULE>
@@ -66,68 +103,68 @@ __global__ __launch_bounds__(kThreads) void quant_rows_kernel(
     const void* __restrict__ x, int64_t ld_x, int64_t rows, int32_t upr,
     int32_t rpb, uint8_t* __restrict__ q, int64_t ld_q,
     uint8_t* __restrict__ s, int64_t ld_s) {
-  float v[kDepth][8];
-  over_units(
+  Raw16<F32> v[2];
+  over_units<2>(
       rows, upr, rpb,
       [&](int i, int64_t r, int u) {
-        load8<F32>(static_cast<const char*>(x) + r * ld_x * (F32 ? 4 : 2),
-                   u * 8, v[i]);
+        v[i] = load_raw<F32>(
+            static_cast<const char*>(x) + r * ld_x * (F32 ? 4 : 2), u * 16);
       },
       [&](int i, int64_t r, int u) {
         int e;
-        const uint32_t w = quant8_e2m1<RULE>(v[i], e);
-        *reinterpret_cast<uint32_t*>(q + r * ld_q + u * 4) = w;
-        if (u % 4 == 0) s[r * ld_s + u / 4] = (uint8_t)(e + 127);
+        store8_nt(q + r * ld_q + u * 8, quant16_e2m1<F32, RULE>(v[i], e));
+        if (u % 2 == 0) s[r * ld_s + u / 2] = (uint8_t)(e + 127);
       });
 }
 
 __global__ __launch_bounds__(kThreads) void to_e4m3_kernel(
     const uint8_t* __restrict__ q, int64_t ld_q, int64_t rows, int32_t upr,
     int32_t rpb, uint8_t* __restrict__ out, int64_t ld_out) {
-  uint32_t w[kDepth];
-  over_units(
+  uint2 w[2];
+  over_units<2>(
       rows, upr, rpb,
       [&](int i, int64_t r, int u) {
-        w[i] = *reinterpret_cast<const uint32_t*>(q + r * ld_q + u * 4);
+        w[i] = *reinterpret_cast<const uint2*>(q + r * ld_q + u * 8);
       },
       [&](int i, int64_t r, int u) {
-        *reinterpret_cast<uint2*>(out + r * ld_out + u * 8) =
-            e2m1_to_e4m3(w[i]);
+        const uint2 a = e2m1_to_e4m3(w[i].x), b = e2m1_to_e4m3(w[i].y);
+        store16_nt(out + r * ld_out + u * 16, u32x4{a.x, a.y, b.x, b.y});
       });
+}
+
+// Eight codes times f = 2^(b - 127) as bf16: exact but where they overflow.
+__device__ __forceinline__ u32x4 e2m1_to_bf16(uint32_t w, float f) {
+  auto two = [&](auto pair) {
+    const uint32_t h = __builtin_bit_cast(uint32_t, pair);
+    const float lo = bf16_lo(h) * f, hi = bf16_hi(h) * f;
+    return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)lo) |
+           ((uint32_t)__builtin_bit_cast(uint16_t, (__bf16)hi) << 16);
+  };
+  return u32x4{two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 0)),
+               two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 1)),
+               two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 2)),
+               two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 3))};
 }
 
 __global__ __launch_bounds__(kThreads) void upscale_kernel(
     const uint8_t* __restrict__ q, int64_t ld_q, const uint8_t* __restrict__ s,
     int64_t ld_s, int64_t rows, int32_t upr, int32_t rpb,
     uint16_t* __restrict__ out, int64_t ld_out) {
-  uint32_t w[kDepth], b[kDepth];
-  over_units(
-      rows, upr, rpb,
+  // units of eight channels: a wavefront's stores are whole lines (streaming
+  // stores of 16 channels a lane in two halves took twice the time)
+  uint32_t w[4], b[4];
+  over_units<4>(
+      rows, 2 * upr, rpb,
       [&](int i, int64_t r, int u) {
         w[i] = *reinterpret_cast<const uint32_t*>(q + r * ld_q + u * 4);
         b[i] = s[r * ld_s + u / 4];
       },
       [&](int i, int64_t r, int u) {
-        // 2^(b - 127): subnormal for 0, NaN for 255; a payload's two bits
-        // times it are bf16 numbers but where they overflow
+        // subnormal for 0, NaN for 255
         const float f = __uint_as_float(b[i] == 0     ? 0x400000u
                                         : b[i] == 255 ? 0x7FC00000u
                                                       : b[i] << 23);
-        auto two = [&](auto pair) {
-          const uint32_t h = __builtin_bit_cast(uint32_t, pair);
-          const float lo = bf16_lo(h) * f, hi = bf16_hi(h) * f;
-          return (uint32_t)__builtin_bit_cast(uint16_t, (__bf16)lo) |
-                 ((uint32_t)__builtin_bit_cast(uint16_t, (__bf16)hi) << 16);
-        };
-        store16(out + r * ld_out + u * 8,
-                u32x4{two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(
-                          w[i], 1.0f, 0)),
-                      two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(
-                          w[i], 1.0f, 1)),
-                      two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(
-                          w[i], 1.0f, 2)),
-                      two(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(
-                          w[i], 1.0f, 3))});
+        store16_nt(out + r * ld_out + u * 8, e2m1_to_bf16(w[i], f));
       });
 }
 
@@ -146,11 +183,10 @@ __global__ __launch_bounds__(1024) void scatter_kernel(
   const bool valid = lane < K && d_lane >= 0 && (int64_t)d_lane < num_rows;
   if (__ballot(valid) == 0) return;  // the same in every wavefront
   const uint16_t* xr = x + t * ld_x;
-  for (int c = threadIdx.x * 8; c < H; c += blockDim.x * 8) {
-    float v[8];
-    load8<false>(xr, c, v);
+  for (int c = threadIdx.x * 16; c < H; c += blockDim.x * 16) {
     int e;
-    *reinterpret_cast<uint32_t*>(row + c / 2) = quant8_e2m1<RULE>(v, e);
+    *reinterpret_cast<uint2*>(row + c / 2) =
+        quant16_e2m1<false, RULE>(load_raw<false>(xr, c), e);
     if ((c & 31) == 0) row[H / 2 + c / 32] = (uint8_t)(e + 127);
   }
   __syncthreads();
@@ -165,7 +201,7 @@ __global__ __launch_bounds__(1024) void scatter_kernel(
   }
 }
 
-// Rows per block: about kUnits units of eight channels.
+// Rows per block: about kUnits units of 16 channels.
 struct RowsGrid {
   int32_t upr, rpb;
   int64_t blocks;
@@ -173,7 +209,7 @@ struct RowsGrid {
 
 RowsGrid rows_grid(int64_t rows, int32_t H) {
   RowsGrid g;
-  g.upr = H / 8;
+  g.upr = H / 16;
   g.rpb = std::max(1, kUnits / g.upr);
   g.blocks = ceil_div(rows, g.rpb);
   return g;
@@ -233,7 +269,7 @@ extern "C" mxq_status moe_scatter_quant_mxfp4(
       scales == nullptr || ld_x < H || ld_q < H / 2 || ld_s < H / 32 ||
       !row_bytes_ok(x_bf16, ld_x * 2) || !row_bytes_ok(q_fp4, ld_q))
     return MXQ_ERR_INVALID_ARGUMENT;
-  const int threads = std::max(row_block_threads(H, 8), std::min(K, 8) * 64);
+  const int threads = std::max(row_block_threads(H, 16), std::min(K, 8) * 64);
   if (T > max_blocks(threads)) return MXQ_ERR_UNSUPPORTED;
   auto* k = rule == MXQ_RULE_NO_CLIP ? &scatter_kernel<kNoClip>
                                      : &scatter_kernel<kOcpFloor>;
