@@ -288,11 +288,11 @@ __device__ __forceinline__ bool find_tile(const MatmulArgs& a, int tiles_n,
 constexpr int kStageLd = 260;  // floats per staged token (256 weight rows + pad)
 
 // End of a tile of 64 XF token rows (`rows` of them live, from row0 on) by 256
-// weight rows of expert e, from output n0 on.  128 token rows (64 of each
-// wavefront row) at a time go through LDS as they are, so that a thread ends up
-// with eight neighbouring channels of a row: gate and factor meet, a row is
-// written in whole lines, and a quantization group lies within a wavefront.
-template <int XF, int OUT, bool GATED>
+// weight rows of expert e, from output n0 on.  64 PX token rows (PX fragments
+// of each wavefront row) at a time go through LDS as they are, so that a thread
+// ends up with eight neighbouring channels of a row: gate and factor meet, a row
+// is written in whole lines, and a quantization group lies within a wavefront.
+template <int XF, int OUT, bool GATED, int PX = 2>
 __device__ __forceinline__ void finish_tile(const MatmulArgs& a, int e,
                                             int64_t row0, int rows, int n0,
                                             const v16f (&acc)[4][XF],
@@ -300,7 +300,7 @@ __device__ __forceinline__ void finish_tile(const MatmulArgs& a, int e,
   float* stage = reinterpret_cast<float*>(lds);
   constexpr int kOutLanes = GATED ? 16 : 32;  // threads per row
   constexpr int kPerRound = 256 / kOutLanes;  // rows per round of the block
-  constexpr int kRounds = 128 / kPerRound;
+  constexpr int kRounds = 64 * PX / kPerRound;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave >> 1, wn = wave & 1;
@@ -323,9 +323,9 @@ __device__ __forceinline__ void finish_tile(const MatmulArgs& a, int e,
   const int gate_at = GATED ? (oc >> 6) * 128 + (oc & 63) : oc;
   // token (of the tile) of row i of pass p
   auto token = [&](int p, int i) {
-    return (i >> 6) * 32 * XF + p * 64 + (i & 63);
+    return i / (32 * PX) * 32 * XF + p * 32 * PX + i % (32 * PX);
   };
-  constexpr int kPasses = XF / 2;
+  constexpr int kPasses = XF / PX;
   // A pass's residual is asked for a pass ahead, the first one's before its
   // staging: the loads are in flight together and behind other work.
   u32x4 res[2][kRounds];
@@ -351,10 +351,10 @@ __device__ __forceinline__ void finish_tile(const MatmulArgs& a, int e,
 #pragma unroll
       for (int q4 = 0; q4 < 4; ++q4)
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const v16f& v = acc[f][2 * pass + x];
+        for (int x = 0; x < PX; ++x) {
+          const v16f& v = acc[f][PX * pass + x];
           *reinterpret_cast<v4f*>(stage +
-                                  (wm * 64 + x * 32 + r32) * kStageLd +
+                                  (wm * 32 * PX + x * 32 + r32) * kStageLd +
                                   wn * 128 + f * 32 + 8 * q4 + 4 * g) =
               v4f{v[4 * q4], v[4 * q4 + 1], v[4 * q4 + 2], v[4 * q4 + 3]};
         }

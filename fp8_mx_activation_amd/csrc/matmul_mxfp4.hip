@@ -599,10 +599,18 @@ __global__ __launch_bounds__(256, 1) void matmul4_stream_kernel(
 // The tiles of the products with 8-bit weights: a block of four wavefronts,
 // one per SIMD, owns TM = 64 XF token rows of one expert by 256 weight rows;
 // each wavefront multiplies 32 XF tokens by 128 weight rows in 32x32x64 steps.
-// A token row's part of a step is 128 bytes, so K goes by in steps of 256
-// channels for 4-bit rows and of 128 for 8-bit ones, held in LDS twice: while
-// one step is multiplied, the next is on its way from memory straight into LDS.
-// Either way a step of a 256-row tile is 2048 cycles of MFMA per SIMD.
+// K goes by in steps of 128 channels, or 256 where rows of 4 bits meet a tile of
+// 256, held in LDS twice: while one step is multiplied, the next is on its way
+// from memory straight into LDS.  A step of a 256-row tile is 2048 cycles of
+// MFMA per SIMD.
+//
+// Two tiles of 128 rows fit a CU, of 256 one.  The larger one reads 2/3 of the
+// LDS bytes and 2/3 of the memory's per product; of two smaller ones, one's
+// start and end (its first copies, its output: 6 us of a pair's time for 4-bit
+// rows, 14 for 8-bit ones, against 16 and 21 of one large tile's) pass while the
+// other multiplies.  Per 256 channels the pair takes 2.6 us (3.0), the large
+// tile 1.7 (2.7): short rows want the smaller one, long rows in 4 bits the
+// larger.
 //
 // A step is multiplied in two halves, A with the first half of the wavefront's
 // token fragments, B with the second.  B's token fragments are read from LDS
@@ -610,34 +618,41 @@ __global__ __launch_bounds__(256, 1) void matmul4_stream_kernel(
 // B, each weight fragment into the registers that its last MFMA has just left.
 // The copies of the step after the next are dealt out evenly over both.
 //
-// Scales.  A step needs eight bytes (8-bit rows: four) of every token and
-// weight row.  They come in chunks of 16 bytes per row, copied straight into
-// LDS as a step's data are, for the weights and for tokens whose scales start
-// on 4 bytes; a chunk that ends behind the row is put together at the start,
-// with 127 (a factor of one) for the blocks that are not there.  Tokens' scales
+// Scales.  A step needs four or eight bytes of every token and weight row.  They
+// come in chunks of 16 bytes per row, copied straight into LDS as a step's data
+// are, for the weights and for tokens whose scales start on 4 bytes; a chunk
+// that ends behind the row is put together at the start, with 127 (a factor of
+// one) for the blocks that are not there, in a place of its own.  Tokens' scales
 // that start elsewhere go through registers, a chunk at a time; the compiler
-// then waits for all copies on their way once per chunk.
+// then waits for all copies on their way once per chunk.  So does the tokens'
+// last chunk where its place would keep the second tile off the CU.
 template <bool X8, int XF>
 struct Tile {
   static constexpr int kTM = 64 * XF;
-  static constexpr int kChannels = X8 ? 128 : 256;  // of a step
-  static constexpr int kWRow = kChannels / 2;       // bytes of a weight row
-  static constexpr int kX = kTM * 128;              // and of all token rows
+  static constexpr int kChannels = X8 || XF == 2 ? 128 : 256;  // of a step
+  static constexpr int kWRow = kChannels / 2;          // bytes of a weight row
+  static constexpr int kXRow = X8 ? kChannels : kWRow;  // and of a token row
+  static constexpr int kX = kTM * kXRow;                // and of all of them
   static constexpr int kStage = kX + 256 * kWRow;
-  static constexpr int kPieces = kWRow / 32;  // MFMA steps: 16-byte pieces of a
-                                              // lane's weights
-  static constexpr int kSteps = X8 ? 4 : 2;   // per chunk of scales
+  // 16-byte pieces of a lane's row, of weights one for an MFMA
+  static constexpr int kPieces = kWRow / 32, kXPieces = kXRow / 32;
+  static constexpr int kSteps = 512 / kChannels;  // per chunk of scales
   static constexpr int kScaleStep = 16 / kSteps;
   static constexpr int kChunk = (kTM + 256) * 16;
-  // three chunks: two that take turns, and the one that ends behind the row
-  static constexpr int kLoop = 2 * kStage + 3 * kChunk;
-  static constexpr int kEnd = 128 * kStageLd * 4;
+  // two chunks that take turns, and the one that ends behind the row; of
+  // 128-row tiles of 8-bit rows two fit a CU with the weights' part of it
+  static constexpr bool kLate = X8 && XF == 2;  // the tokens' takes a turn
+  static constexpr int kLast = kLate ? 256 * 16 : kChunk;
+  static constexpr int kLoop = 2 * kStage + 2 * kChunk + kLast;
+  static constexpr int kPX = XF == 2 ? 1 : 2;  // fragments the end stages
+  static constexpr int kEnd = 64 * kPX * kStageLd * 4;
   static constexpr int kLds = kLoop > kEnd ? kLoop : kEnd;
-  // copies of a wavefront: of a weight fragment (both wavefront columns'), of
+  static constexpr int kPerCu = XF == 2 ? 2 : 1;
+  // copies of a wavefront: of a fragment (both wavefront columns' or rows'), of
   // half A of a step (weight fragments 0-2, token fragment 0) and of half B
-  static constexpr int kCopiesW = X8 ? 1 : 2;
-  static constexpr int kCopiesA = 3 * kCopiesW + 2;
-  static constexpr int kCopiesB = kCopiesW + 2 * (XF - 1);
+  static constexpr int kCopiesW = kWRow / 64, kCopiesX = kXRow / 64;
+  static constexpr int kCopiesA = 3 * kCopiesW + kCopiesX;
+  static constexpr int kCopiesB = kCopiesW + kCopiesX * (XF - 1);
 };
 
 // A uniform value for an operand that has to be in a scalar register.
@@ -651,7 +666,8 @@ __device__ __forceinline__ int place64(int c, int row) {
 }
 
 template <bool X8, int XF, int OUT, bool GATED>
-__global__ __launch_bounds__(256, 1) void matmul4_tile_kernel(
+__global__
+__launch_bounds__(256, (Tile<X8, XF>::kPerCu)) void matmul4_tile_kernel(
     MatmulArgs a, int32_t tiles_n, int32_t xs_words) {
   using T = Tile<X8, XF>;
   constexpr int TM = T::kTM;
@@ -679,28 +695,34 @@ __global__ __launch_bounds__(256, 1) void matmul4_tile_kernel(
     return (lr & 64) ? a.NO + c : c;
   };
 
-  // Copies of 1 KB.  Of token rows, 8 rows each: lane l fills place l & 7 of
-  // row l >> 3; the 64 rows of fragment x of both wavefront rows are two
-  // copies per wavefront.  Of weight rows the same, or 16 rows of 64 bytes.
-  const int xrow = wave * 8 + (lane >> 3);
-  const int xchunk = place(lane & 7, xrow);
-  const int wrow = X8 ? wave * 16 + (lane >> 2) : xrow;
-  const int wchunk = X8 ? place64(lane & 3, wrow) : xchunk;
-  uint32_t xoff[XF][2], woff[4][T::kCopiesW];
+  // Copies of 1 KB: of rows of 128 bytes, 8 rows, where lane l fills place
+  // l & 7 of row l >> 3, or 16 rows of 64 bytes.  The 64 rows of a fragment
+  // are of both wavefront rows or columns; 32 of one follow 32 of the other,
+  // or, where a row is 128 bytes, all rows of one the other's.
+  const int row128 = wave * 8 + (lane >> 3), row64 = wave * 16 + (lane >> 2);
+  const int chunk128 = place(lane & 7, row128);
+  const int chunk64 = place64(lane & 3, row64);
+  const int xchunk = T::kXRow == 64 ? chunk64 : chunk128;
+  const int wchunk = T::kWRow == 64 ? chunk64 : chunk128;
+  uint32_t xoff[XF][T::kCopiesX], woff[4][T::kCopiesW];
+  // local row of row r (below 64) of token fragment x, of weight fragment f
+  auto both_x = [](int x, int r) { return ((r >> 5) * XF + x) * 32 + (r & 31); };
+  auto both_w = [](int f, int r) { return (r >> 5) * 128 + f * 32 + (r & 31); };
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+  for (int x = 0; x < XF; ++x)
 #pragma unroll
-    for (int x = 0; x < XF; ++x)
-      xoff[x][i] = (uint32_t)(min((i * XF + x) * 32 + xrow, rows - 1) *
-                              (int)a.ld_q + 16 * xchunk);
-  // local row of row r (below 64) of weight fragment f of both columns
-  auto both = [](int f, int r) { return (r >> 5) * 128 + f * 32 + (r & 31); };
+    for (int i = 0; i < T::kCopiesX; ++i)
+      xoff[x][i] = (uint32_t)(
+          min(both_x(x, T::kXRow == 64 ? row64 : i * 32 + row128), rows - 1) *
+              (int)a.ld_q +
+          16 * xchunk);
 #pragma unroll
   for (int f = 0; f < 4; ++f)
 #pragma unroll
     for (int i = 0; i < T::kCopiesW; ++i)
       woff[f][i] = (uint32_t)(
-          (weight_row(both(f, X8 ? wrow : i * 32 + wrow)) - n0) * ld_w +
+          (weight_row(both_w(f, T::kWRow == 64 ? row64 : i * 32 + row128)) -
+           n0) * ld_w +
           16 * wchunk);
   const v4i xbuf = buffer_of(a.q + row0 * a.ld_q,
                              (uint32_t)((rows - 1) * a.ld_q + ld_x));
@@ -711,7 +733,7 @@ __global__ __launch_bounds__(256, 1) void matmul4_tile_kernel(
   // In a last step that ends inside its channels, chunks past H repeat chunk 0
   // of the step: in bounds, and cleared when they are read.
   auto x_back = [&](int k) {
-    return (uint32_t)(k * 128 + 16 * xchunk >= ld_x ? 16 * xchunk : 0);
+    return (uint32_t)(k * T::kXRow + 16 * xchunk >= ld_x ? 16 * xchunk : 0);
   };
   auto w_back = [&](int k) {
     return (uint32_t)(k * T::kWRow + 16 * wchunk >= ld_w ? 16 * wchunk : 0);
@@ -719,15 +741,16 @@ __global__ __launch_bounds__(256, 1) void matmul4_tile_kernel(
   auto copy_w = [&](int k, int f, int i, uint32_t back) {
     copy_to_lds(wbuf,
                 lds0 + (k & 1) * T::kStage + T::kX +
-                    (X8 ? f * 64 * 64 : (i * 128 + f * 32) * 128) +
+                    (T::kWRow == 64 ? f * 64 * 64 : (i * 128 + f * 32) * 128) +
                     wave * 1024,
                 woff[f][i] - back, in_scalar(k * T::kWRow));
   };
   auto copy_x = [&](int k, int x, int i, uint32_t back) {
     copy_to_lds(xbuf,
-                lds0 + (k & 1) * T::kStage + (i * XF + x) * 32 * 128 +
+                lds0 + (k & 1) * T::kStage +
+                    (T::kXRow == 64 ? x * 64 * 64 : (i * XF + x) * 32 * 128) +
                     wave * 1024,
-                xoff[x][i] - back, in_scalar(k * 128));
+                xoff[x][i] - back, in_scalar(k * T::kXRow));
   };
   auto copy_a = [&](int k, int c, uint32_t wb, uint32_t xb) {
     if (c < 3 * T::kCopiesW)
@@ -738,14 +761,14 @@ __global__ __launch_bounds__(256, 1) void matmul4_tile_kernel(
   // token fragments of half A, then the weights', then those of half B
   constexpr int kXA = XF / 2;
   auto copy_b = [&](int k, int c, uint32_t wb, uint32_t xb) {
-    constexpr int first = 2 * (kXA - 1);
+    constexpr int kC = T::kCopiesX, first = kC * (kXA - 1);
     if (c < first)
-      copy_x(k, 1 + c / 2, c & 1, xb);
+      copy_x(k, 1 + c / kC, c % kC, xb);
     else if (c < first + T::kCopiesW)
       copy_w(k, 3, c - first, wb);
     else
-      copy_x(k, kXA + (c - first - T::kCopiesW) / 2,
-             (c - first - T::kCopiesW) & 1, xb);
+      copy_x(k, kXA + (c - first - T::kCopiesW) / kC,
+             (c - first - T::kCopiesW) % kC, xb);
   };
 
   // ---- scales
@@ -758,36 +781,52 @@ __global__ __launch_bounds__(256, 1) void matmul4_tile_kernel(
   const uint32_t xsoff = (uint32_t)(min(srow, rows - 1) * (int)a.ld_s);
   const uint32_t wsoff =
       (uint32_t)((weight_row(wave * 64 + lane) - n0) * a.nbk);
-  const v4i xsbuf = buffer_of(a.s + row0 * a.ld_s,
+  const uint8_t* xs_first = a.s + row0 * a.ld_s;
+  const uint8_t* ws_first = a.ws + ((int64_t)t.e * a.N + n0) * a.nbk;
+  const v4i xsbuf = buffer_of(xs_first,
                               (uint32_t)((rows - 1) * a.ld_s + groups));
-  const v4i wsbuf = buffer_of(a.ws + ((int64_t)t.e * a.N + n0) * a.nbk,
-                              (uint32_t)((a.N - n0) * a.nbk));
+  const v4i wsbuf = buffer_of(ws_first, (uint32_t)((a.N - n0) * a.nbk));
   auto copy_scales = [&](int j) {
     const uint32_t at = scale0 + (j & 1) * T::kChunk;
     if (xs_words)
       copy_to_lds(xsbuf, at + (wave % XF) * 1024, xsoff, in_scalar(j * 16));
     copy_to_lds(wsbuf, at + TM * 16 + wave * 1024, wsoff, in_scalar(j * 16));
   };
-  const uint8_t* xs_row =
-      a.s + (row0 + min((int)threadIdx.x, rows - 1)) * a.ld_s;
-  uint32_t xs_next[4];
-  auto fetch_scales = [&](int j) {
-    if ((int)threadIdx.x >= TM) return;
+  // Through registers, chunk j of a row.  Where the tokens' last chunk takes a
+  // turn, words that reach behind its end (of 32 scales or more) are read where
+  // they do not, and shifted.
+  auto word_at = [&](int j, int i) {
+    const int at = j * 16 + 4 * i;
+    return T::kLate ? min(at, groups - 4) : at;
+  };
+  auto fetch = [&](int j, uint32_t (&v)[4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      __builtin_memcpy(&xs_next[i], xs_row + j * 16 + 4 * i, 4);
+      __builtin_memcpy(&v[i], xs_first + xsoff + word_at(j, i), 4);
   };
-  auto put_scales = [&](int j) {
-    if ((int)threadIdx.x >= TM) return;
+  auto put = [&](int j, const uint32_t (&v)[4]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int bits = 8 * (j * 16 + 4 * i - word_at(j, i));
+      w[i] = bits == 0   ? v[i]
+             : bits < 32 ? (v[i] >> bits) | (0x7F7F7F7Fu << (32 - bits))
+                         : 0x7F7F7F7Fu;
+    }
     *reinterpret_cast<u32x4*>(scale + (j & 1) * T::kChunk + threadIdx.x * 16) =
-        u32x4{xs_next[0], xs_next[1], xs_next[2], xs_next[3]};
+        u32x4{w[0], w[1], w[2], w[3]};
   };
-  constexpr int kWords = X8 ? 1 : 2;  // of a row's scales in a step
+  uint32_t xs_next[4];
+  constexpr int kWords = T::kScaleStep / 4;  // of a row's scales in a step
   uint32_t sx[XF][kWords], sw[4][kWords], sx1[XF][kWords], sw1[4][kWords];
   auto read_scales = [&](int k) {
     const int j = k / T::kSteps;
-    const uint8_t* at = scale + (j == full ? 2 : j & 1) * T::kChunk +
-                        k % T::kSteps * T::kScaleStep;
+    const int in_row = k % T::kSteps * T::kScaleStep;
+    const uint8_t* at =
+        scale + (!T::kLate && j == full ? 2 : j & 1) * T::kChunk + in_row;
+    const uint8_t* at_w = T::kLate && j == full
+                              ? scale + 2 * T::kChunk + in_row
+                              : at + TM * 16;
 #pragma unroll
     for (int x = 0; x < XF; ++x)
       __builtin_memcpy(sx1[x], __builtin_assume_aligned(
@@ -796,7 +835,7 @@ __global__ __launch_bounds__(256, 1) void matmul4_tile_kernel(
 #pragma unroll
     for (int f = 0; f < 4; ++f)
       __builtin_memcpy(sw1[f], __builtin_assume_aligned(
-          at + (TM + wn * 128 + f * 32 + r32) * 16, T::kScaleStep),
+          at_w + (wn * 128 + f * 32 + r32) * 16, T::kScaleStep),
           T::kScaleStep);
   };
   // lane group g takes every second block's
@@ -820,14 +859,14 @@ __global__ __launch_bounds__(256, 1) void matmul4_tile_kernel(
 
   // fragments of a step, in 16-byte pieces
   constexpr int kP = T::kPieces;
-  v4i fw[4][kP], fx[XF][4];
+  constexpr int kPX = T::kXPieces;
+  v4i fw[4][kP], fx[XF][kPX];
   auto read_w = [&](int k, int f, int p, auto last) {
     const int c = p * 2 + g;
     const uint8_t* base = lds + (k & 1) * T::kStage + T::kX;
-    // the rows of a fragment of both columns follow each other where a
-    // wavefront's copy brings 16 of them
     const uint8_t* at =
-        X8 ? base + (f * 64 + wn * 32 + r32) * 64 + place64(c, r32) * 16
+        T::kWRow == 64
+            ? base + (f * 64 + wn * 32 + r32) * 64 + place64(c, r32) * 16
            : base + (wn * 128 + f * 32 + r32) * 128 + place(c, r32) * 16;
     v4i v = *reinterpret_cast<const v4i*>(at);
     if constexpr (decltype(last)::value)
@@ -836,11 +875,14 @@ __global__ __launch_bounds__(256, 1) void matmul4_tile_kernel(
   };
   auto read_x = [&](int k, int x, int p, auto last) {
     const int c = p * 2 + g;
-    v4i v = *reinterpret_cast<const v4i*>(
-        lds + (k & 1) * T::kStage + (wm * 32 * XF + x * 32 + r32) * 128 +
-        place(c, r32) * 16);
+    const uint8_t* base = lds + (k & 1) * T::kStage;
+    const uint8_t* at =
+        T::kXRow == 64
+            ? base + (x * 64 + wm * 32 + r32) * 64 + place64(c, r32) * 16
+            : base + (wm * 32 * XF + x * 32 + r32) * 128 + place(c, r32) * 16;
+    v4i v = *reinterpret_cast<const v4i*>(at);
     if constexpr (decltype(last)::value)
-      if (k * 128 + 16 * c >= ld_x) v = v4i{0, 0, 0, 0};
+      if (k * T::kXRow + 16 * c >= ld_x) v = v4i{0, 0, 0, 0};
     fx[x][p] = v;
   };
   constexpr int kMfma = 4 * kP * kXA;  // of a half
@@ -850,8 +892,8 @@ __global__ __launch_bounds__(256, 1) void matmul4_tile_kernel(
   auto multiply = [&](int i, int x0) {
     const int f = i / (kP * kXA), p = i / kXA % kP, x = x0 + i % kXA;
     const v8i w = half(fw[f][p]);
-    const v8i v = X8 ? join(fx[x][2 * p & 3], fx[x][(2 * p + 1) & 3])
-                     : half(fx[x][p & 3]);
+    const v8i v = X8 ? join(fx[x][2 * p % kPX], fx[x][(2 * p + 1) % kPX])
+                     : half(fx[x][p % kPX]);
     constexpr int B = X8 ? kFmtFp8 : kFmtFp4;
     if (p & 1)
       acc[f][x] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
@@ -876,16 +918,17 @@ __global__ __launch_bounds__(256, 1) void matmul4_tile_kernel(
   if (full > 0) copy_scales(0);
   copy_all(0);
   if (groups % 16 != 0) {
-    u32x4* d = reinterpret_cast<u32x4*>(scale + 2 * T::kChunk);
-    if ((int)threadIdx.x < TM)
-      d[threadIdx.x] = last_scales(xs_row, full * 16, groups);
-    d[TM + threadIdx.x] = last_scales(
-        a.ws + ((int64_t)t.e * a.N + weight_row(threadIdx.x)) * a.nbk,
-        full * 16, groups);
+    uint8_t* last = scale + 2 * T::kChunk;
+    if ((!T::kLate || full < 2) && (int)threadIdx.x < TM)
+      reinterpret_cast<u32x4*>(
+          T::kLate ? scale + full * T::kChunk : last)[threadIdx.x] =
+          last_scales(xs_first + xsoff, full * 16, groups);
+    reinterpret_cast<u32x4*>(last + (T::kLate ? 0 : TM * 16))[threadIdx.x] =
+        last_scales(ws_first + wsoff, full * 16, groups);
   }
-  if (!xs_words && full > 0) {
-    fetch_scales(0);
-    put_scales(0);
+  if (!xs_words && full > 0 && (int)threadIdx.x < TM) {
+    fetch(0, xs_next);
+    put(0, xs_next);
   }
   landed_barrier<0, 0>();
   if (nsteps > 1) copy_all(1);
@@ -894,7 +937,7 @@ __global__ __launch_bounds__(256, 1) void matmul4_tile_kernel(
 #pragma unroll
   for (int x = 0; x < kXA; ++x)
 #pragma unroll
-    for (int p = 0; p < 4; ++p) read_x(0, x, p, Yes{});
+    for (int p = 0; p < kPX; ++p) read_x(0, x, p, Yes{});
 #pragma unroll
   for (int f = 0; f < 4; ++f)
 #pragma unroll
@@ -914,15 +957,24 @@ __global__ __launch_bounds__(256, 1) void matmul4_tile_kernel(
     constexpr bool copy = decltype(copy_)::value;
     const uint32_t wb = w_back(k + 2), xb = x_back(k + 2);
     const int chunk = (k + 2) / T::kSteps;  // of scales
-    const bool ask = copy && (k + 2) % T::kSteps == 0 && chunk < full;
+    const bool first = copy && (k + 2) % T::kSteps == 0;
+    const bool ask = first && chunk < full;
+    const bool ask_last = T::kLate && first && chunk == full && full > 1;
     landed_barrier<more ? T::kCopiesA + T::kCopiesB : 0, kP>();
     if (ask) copy_scales(chunk);
-    if (more && !xs_words) {
+    if constexpr (more) {
       // fetched two steps before the chunk's first, put down in the one
       // before it, ahead of barrier B
       const int next = (k + 1) / T::kSteps;
-      if ((k + 1) % T::kSteps == 0 && next < full) put_scales(next);
-      if (ask) fetch_scales(chunk);
+      const bool down = (k + 1) % T::kSteps == 0;
+      const bool down_last = T::kLate && down && next == full && full > 1;
+      if (!xs_words || T::kLate) {
+        if ((int)threadIdx.x < TM) {
+          if (down_last || (down && !xs_words && next < full))
+            put(next, xs_next);
+          if (ask_last || (ask && !xs_words)) fetch(chunk, xs_next);
+        }
+      }
     }
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -934,14 +986,14 @@ __global__ __launch_bounds__(256, 1) void matmul4_tile_kernel(
           copy_a(k + 2, c, wb, xb);
       }
       constexpr int kEach = kMfma / 8 > 1 ? 2 : 1;  // MFMAs per read
-      if (i % kEach == 0 && i / kEach < 4) {
+      if (i % kEach == 0 && i / kEach < kPX) {
 #pragma unroll
         for (int x = kXA; x < XF; ++x) read_x(k, x, i / kEach, last);
       }
       multiply(i, 0);
     }
     if constexpr (more)
-      landed_barrier<copy ? T::kCopiesA + 2 * kXA : 2 * kXA, 0>();
+      landed_barrier<(copy ? T::kCopiesA : 0) + T::kCopiesX * kXA, 0>();
     if constexpr (more) read_scales(k + 1);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -958,7 +1010,7 @@ __global__ __launch_bounds__(256, 1) void matmul4_tile_kernel(
         constexpr int kF = kP * kXA;  // MFMAs of a weight fragment
         if (i < kF) {
 #pragma unroll
-          for (int p = i * 4 / kF; p < (i + 1) * 4 / kF; ++p)
+          for (int p = i * kPX / kF; p < (i + 1) * kPX / kF; ++p)
 #pragma unroll
             for (int x = 0; x < kXA; ++x) read_x(k + 1, x, p, next_last);
         } else {
@@ -981,7 +1033,7 @@ __global__ __launch_bounds__(256, 1) void matmul4_tile_kernel(
   if (k + 1 < nsteps) step(k++, Yes{}, No{}, No{}, Yes{});
   step(k, No{}, No{}, Yes{}, No{});
 
-  finish_tile<XF, OUT, GATED>(a, t.e, row0, rows, n0, acc, lds);
+  finish_tile<XF, OUT, GATED, T::kPX>(a, t.e, row0, rows, n0, acc, lds);
 }
 
 // ------------------------------------------------------------ entry points
@@ -1047,7 +1099,7 @@ mxq_status launch_tile(const MatmulArgs& a, hipStream_t s) {
   const int64_t blocks = ceil_div(tm * tn, 8) * 8;
   if (blocks > max_blocks(256)) return MXQ_ERR_UNSUPPORTED;
   constexpr int lds = Tile<X8, XF>::kLds;
-  static_assert(lds <= kLds, "a tile fits a CU");
+  static_assert(lds * Tile<X8, XF>::kPerCu <= kLds, "the tiles fit a CU");
   auto* k = a.act == kActSiluMul ? &matmul4_tile_kernel<X8, XF, OUT, true>
                                  : &matmul4_tile_kernel<X8, XF, OUT, false>;
   if (hipFuncSetAttribute(reinterpret_cast<const void*>(k),
@@ -1063,24 +1115,29 @@ mxq_status launch_tile(const MatmulArgs& a, hipStream_t s) {
 }
 
 // The kernel for `expected` rows in a busy expert.  Measured with top-2
-// routings over 32 experts whose fullest holds 2.6 times the mean, gate/up
+// (below 25 mean rows) and top-8 routings over 32 experts, gate/up
 // (4096 x 7168) and down (7168 x 2048) of 4-bit rows (and 8-bit ones), us:
-//   mean rows               4         8         12.5       25
-//   few rows, FW = 2     76, 41    88, 49    103, 54
-//               (8-bit)  83, 43   107, 54    131, 63
-//             FW = 4     80, 46    87, 55     94, 59    134, 73
-//               (8-bit)  82, 47    90, 57    106, 62    158, 82
-//   128-row tile        110, 59   114, 73    119, 81    124, 86
-//               (8-bit) 115, 60   120, 76    125, 84    133, 89
+//   mean rows               4         8        12        16        25
+//   few rows, FW = 2     76, 41    88, 49   103, 54
+//               (8-bit)  83, 43   107, 54   131, 63
+//             FW = 4     80, 46    87, 55    98, 56    99, 62   134, 73
+//               (8-bit)  82, 47    90, 57   107, 76   112, 80   158, 82
+//   128-row tiles                          114, 63   115, 64   120, 67
+//               (8-bit)                    121, 76   123, 77   130, 82
 // (the weights alone take 94 and 47 us at 5.3 TB/s; with few rows experts are
-// left out, and the last-level cache holds a part).  A 128-row tile of 8-bit
-// rows takes 0.6 of a 256-row one's time, both one to a CU, so the smaller one
-// is taken where that many rounds of the 256 CUs are over sooner; the same rule
-// serves 4-bit rows.
+// left out, and the last-level cache holds a part).  With more rows:
+//   mean rows               40        80       160       320       2048
+//   128-row tiles       127, 71  156, 84   207, 111  290, 158  1326, 798
+//               (8-bit) 135, 86  172, 104  229, 140  349, 214  1677, 1132
+//   256-row tiles       128, 99  134, 109  182, 139  254, 199  1070, 865
+//               (8-bit) 204, 148 198, 161  291, 207  392, 304  1630, 1260
+// With K = 4096 and 2560 gate/up of 4-bit rows takes 325 and 59 us in 128-row
+// tiles and 322 and 58 in 256-row ones (320 rows; I = 4096 and 1024); with
+// 2048 rows it is 1513 and 244 against 1335 and 255.
 template <bool X8, int OUT>
 mxq_status launch(const MatmulArgs& a, int64_t expected, hipStream_t s) {
   constexpr int64_t kCus = 256;
-  constexpr int64_t kFew = X8 ? 4 : 12, kMore = 20, kSmall = 12;
+  constexpr int64_t kFew = X8 ? 4 : 12, kMore = X8 ? 16 : 20, kSmall = 12;
   constexpr int kWide = X8 ? 3 : 4;
   const bool few_blocks = ceil_div(a.N, 128) * a.E <= kCus / 2;
   if (few_blocks && expected <= kSmall) return launch_small<X8, 3, OUT>(a, s);
@@ -1091,12 +1148,9 @@ mxq_status launch(const MatmulArgs& a, int64_t expected, hipStream_t s) {
     if (expected <= kSmall || !X8)
       return launch_stream<X8, X8 ? 1 : 2, 2, OUT>(a, s);
   }
-  const int64_t columns =
-      a.E * ceil_div(a.NO, a.act == kActSiluMul ? 128 : 256);
-  const int64_t rounds4 = ceil_div(columns * ceil_div(expected, 256), kCus);
-  const int64_t rounds2 = ceil_div(columns * ceil_div(expected, 128), kCus);
-  return rounds2 * 3 <= rounds4 * 5 ? launch_tile<X8, 2, OUT>(a, s)
-                                    : launch_tile<X8, 4, OUT>(a, s);
+  const bool wide = X8 ? a.H > 4096 && expected >= 512
+                       : a.H > 2560 && expected >= 64;
+  return wide ? launch_tile<X8, 4, OUT>(a, s) : launch_tile<X8, 2, OUT>(a, s);
 }
 
 template <int OUT>

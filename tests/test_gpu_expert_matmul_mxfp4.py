@@ -304,6 +304,79 @@ def wide(t, left, right, fill=0x7F):
     return v, big
 
 
+# rows of more than 2560 channels, and of 8 bits of more than 4096, go through
+# 256-row tiles where there are many; scales in chunks of 512 channels, the last
+# one whole, cut or missing
+LONG = (1056, 1504, 2048, 2592, 4128, 4608, 5216)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("act,N", [("none", 272), ("silu_mul", 400)])
+@pytest.mark.parametrize("H", LONG)
+def test_long_rows(H, act, N, fmt):
+    say("mxfp4 long rows", H, act, N, fmt)
+    p = Problem(H, [300, 1, 0, 257, 64], N, H, fmt, act, bias=True,
+                residual=act == "none", exact=True)
+    check_bf16(p, (13, 1 << 20), exact=act == "none")
+    # scales of tokens that start on no word: the same bytes
+    d = p.dev()
+    for hint in (13, 1 << 20):
+        plain = mxq.moe_expert_matmul_mxfp4(**d, expected_m=hint)
+        far, _ = wide(d["scales"], 3, 2, 0xFF)
+        out = mxq.moe_expert_matmul_mxfp4(**{**d, "scales": far},
+                                          expected_m=hint)
+        live = torch.from_numpy(p.live).to(DEV)
+        assert torch.equal(out[live], plain[live]), hint
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("out_fmt", FMTS)
+@pytest.mark.parametrize("act,N", [("none", 288), ("silu_mul", 576)])
+@pytest.mark.parametrize("H", (1120, 4192))
+def test_long_rows_quantized(H, act, N, out_fmt, fmt):
+    say("mxfp4 long rows, quantized", H, act, N, out_fmt, fmt)
+    check_quant(Problem(6, [260, 70, 0, 1], N, H, fmt, act, bias=True, pad=1),
+                out_fmt, (13, 1 << 20))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("H", (1504, 4128))
+def test_long_rows_nan_and_device_data(H, fmt):
+    """A scale of 255 in the last block of one row and of one weight row, and
+    offsets and counts that no layout makes."""
+    p = Problem(8, [260, 70, 3], 272, H, fmt, exact=True)
+    p.s[150, H // 32 - 1] = 255
+    p.ws[1, 200, H // 32 - 1] = 255
+    a = int(p.offsets[1])
+    want = torch.zeros((p.rows, 272), dtype=torch.bool)
+    want[150] = True
+    want[a:a + 70, 200] = True
+    for hint in (13, 1 << 20):
+        for wider in (False, True):
+            d = p.dev()
+            if wider:
+                d["scales"], _ = wide(d["scales"], 3, 2, 0xFF)
+            out = mxq.moe_expert_matmul_mxfp4(**d, expected_m=hint).cpu()
+            nan = torch.isnan(out) & torch.from_numpy(p.live)[:, None]
+            assert torch.equal(nan, want), (hint, wider)
+    for counts, offsets in (
+            ([-5, 1 << 30, 10], p.offsets),
+            ([260, 260, 260], np.array([0, 200, 300, 1 << 30])),
+            ([260, 70, 3], np.array([-8, 100, p.rows, p.rows + 60]))):
+        d = p.dev()
+        d["counts"], d["expert_offsets"] = i32_to_dev(counts), \
+            i32_to_dev(offsets)
+        live = np.zeros(p.rows + 4, bool)
+        for e in range(3):
+            a, n = ref.live_rows(offsets, counts, p.rows, e)
+            live[a:a + n] = n > 0
+        for hint in (13, 1 << 20):
+            out = torch.full((p.rows + 4, p.cols), 5.0, dtype=torch.bfloat16,
+                             device=DEV)
+            mxq.moe_expert_matmul_mxfp4(**d, out=out, expected_m=hint)
+            assert (out.cpu().double().numpy()[~live] == 5).all()
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("hint", HINTS)
 def test_strides(hint, fmt):
