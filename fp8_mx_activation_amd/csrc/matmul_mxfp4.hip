@@ -340,6 +340,10 @@ __global__ __launch_bounds__(256, 1) void matmul4_small_kernel(
 // FW = 4, NT = 4 (8-bit rows: 3): an expert's rows go through in one pass where
 // 16 or 32 at a time would read its weights twice.
 //
+// One row of each of eight experts, 4096 x 7168 gated (125 MB): 24.9 us, 5.0
+// TB/s, a block's start and end the rest; 8-bit rows of 128 tokens, top-2 over 32
+// experts: 90 us (5.6 TB/s), and 7168 x 2048 55 us (4.5).
+//
 // Scales come in chunks of 16 bytes per weight row, two steps' worth, copied
 // straight into LDS two steps ahead; what is left of a row behind whole chunks
 // is put there at the start, with 127 (a factor of one) for the blocks behind
@@ -706,8 +710,12 @@ __launch_bounds__(256, (Tile<X8, XF>::kPerCu)) void matmul4_tile_kernel(
   const int wchunk = T::kWRow == 64 ? chunk64 : chunk128;
   uint32_t xoff[XF][T::kCopiesX], woff[4][T::kCopiesW];
   // local row of row r (below 64) of token fragment x, of weight fragment f
-  auto both_x = [](int x, int r) { return ((r >> 5) * XF + x) * 32 + (r & 31); };
-  auto both_w = [](int f, int r) { return (r >> 5) * 128 + f * 32 + (r & 31); };
+  auto both_x = [](int x, int r) {
+    return ((r >> 5) * XF + x) * 32 + (r & 31);
+  };
+  auto both_w = [](int f, int r) {
+    return (r >> 5) * 128 + f * 32 + (r & 31);
+  };
 #pragma unroll
   for (int x = 0; x < XF; ++x)
 #pragma unroll
@@ -1088,7 +1096,8 @@ mxq_status launch_stream(const MatmulArgs& a, hipStream_t s) {
 // Whether a pass of 16 NT rows and all their scales fit a CU.
 template <bool X8, int NT, int FW>
 bool stream_fits(const MatmulArgs& a) {
-  return Stream<X8, NT, FW>::kXScales + 16 * NT * small_scale_ld(a.H / 32) <= kLds;
+  return Stream<X8, NT, FW>::kXScales + 16 * NT * small_scale_ld(a.H / 32) <=
+         kLds;
 }
 
 template <bool X8, int XF, int OUT>

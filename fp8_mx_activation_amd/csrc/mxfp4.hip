@@ -7,7 +7,9 @@
 //
 // Every kernel is bound by what it reads and writes.  A lane owns 16
 // neighbouring channels, 32 bytes of bf16 and 8 of codes; a group's two lanes
-// are neighbours.
+// are neighbours.  16384 rows of 7168 channels (297 MB) are quantized in 52.8 us
+// (5.6 TB/s) and turned back to bf16 in 49.1 (6.0); 40832 rows of 4 bits become
+// e4m3 in 70 us (6.3).  With 8 channels a lane the first two took 77 and 60 us.
 #include <algorithm>
 
 #include "mxfp4_device.hpp"
@@ -170,7 +172,8 @@ __global__ __launch_bounds__(kThreads) void upscale_kernel(
 
 // One block per token: the row is quantized once into LDS and written from
 // there to its destinations, all of the block's threads sharing the 16-byte
-// chunks of all of them.
+// chunks of all of them.  4096 rows of 7168 channels to 32768 destinations
+// (184 MB) take 36 us (5.1 TB/s), 128 rows to 1024 4.3 us.
 template <int RULE>
 __global__ __launch_bounds__(1024) void scatter_kernel(
     const uint16_t* __restrict__ x, int64_t ld_x, int32_t H,
