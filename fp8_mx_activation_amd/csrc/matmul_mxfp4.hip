@@ -1143,6 +1143,8 @@ mxq_status launch_tile(const MatmulArgs& a, hipStream_t s) {
 // With K = 4096 and 2560 gate/up of 4-bit rows takes 325 and 59 us in 128-row
 // tiles and 322 and 58 in 256-row ones (320 rows; I = 4096 and 1024); with
 // 2048 rows it is 1513 and 244 against 1335 and 255.
+// So 4-bit rows of more than 2560 channels take 256-row tiles from 64 rows on,
+// 8-bit ones of more than 4096 from 512 on.
 template <bool X8, int OUT>
 mxq_status launch(const MatmulArgs& a, int64_t expected, hipStream_t s) {
   constexpr int64_t kCus = 256;
