@@ -1144,14 +1144,25 @@ mxq_status launch_tile(const MatmulArgs& a, hipStream_t s) {
 // tiles and 322 and 58 in 256-row ones (320 rows; I = 4096 and 1024); with
 // 2048 rows it is 1513 and 244 against 1335 and 255.
 // So 4-bit rows of more than 2560 channels take 256-row tiles from 64 rows on,
-// 8-bit ones of more than 4096 from 512 on.
+// 8-bit ones of more than 4096 from 512 on, but not where these would leave half
+// of the CUs without one: 64 rows of one expert and of each of four take 46 and
+// 48 in the larger tiles, 35 and 38 in the smaller ones.
+//
+// Few blocks, gate/up (4096 x 7168):
+//   experts, mean rows   1, 16  1, 32  1, 64  4, 16  4, 32
+//   K split                 12     19     34     26     44
+//   (8-bit)                 13     21     37     27     47
+//   128-row tiles           34     35     35     36     37
+//   (8-bit)                 46     46     46     46     47
+// (of two experts with K = 1024 and 512 the two are even at 16 rows).
 template <bool X8, int OUT>
 mxq_status launch(const MatmulArgs& a, int64_t expected, hipStream_t s) {
   constexpr int64_t kCus = 256;
   constexpr int64_t kFew = X8 ? 4 : 12, kMore = X8 ? 16 : 20, kSmall = 12;
   constexpr int kWide = X8 ? 3 : 4;
   const bool few_blocks = ceil_div(a.N, 128) * a.E <= kCus / 2;
-  if (few_blocks && expected <= kSmall) return launch_small<X8, 3, OUT>(a, s);
+  if (few_blocks && expected <= (a.E == 1 ? 32 : 24))
+    return launch_small<X8, 3, OUT>(a, s);
   if (!few_blocks && expected <= kMore) {
     if (expected > kFew && ceil_div(a.N, 256) * a.E >= kCus &&
         stream_fits<X8, kWide, 4>(a))
@@ -1159,8 +1170,12 @@ mxq_status launch(const MatmulArgs& a, int64_t expected, hipStream_t s) {
     if (expected <= kSmall || !X8)
       return launch_stream<X8, X8 ? 1 : 2, 2, OUT>(a, s);
   }
-  const bool wide = X8 ? a.H > 4096 && expected >= 512
-                       : a.H > 2560 && expected >= 64;
+  const int64_t tiles =
+      a.E * ceil_div(a.NO, a.act == kActSiluMul ? 128 : 256) *
+      ceil_div(expected, 256);
+  const bool wide = tiles > kCus / 2 &&
+                    (X8 ? a.H > 4096 && expected >= 512
+                        : a.H > 2560 && expected >= 64);
   return wide ? launch_tile<X8, 4, OUT>(a, s) : launch_tile<X8, 2, OUT>(a, s);
 }
 

@@ -19,7 +19,7 @@ pytestmark = pytest.mark.gpu
 FMTS = ("mxfp4", "e8m0_g32")
 # hints that reach every kernel of few blocks, whatever the rows really are,
 # and those of many
-HINTS = (1, 13, 200, 1 << 20)
+HINTS = (1, 13, 40, 200, 1 << 20)
 MANY_HINTS = (1, 7, 13, 18)
 
 
@@ -308,6 +308,7 @@ def wide(t, left, right, fill=0x7F):
 # 256-row tiles where there are many; scales in chunks of 512 channels, the last
 # one whole, cut or missing
 LONG = (1056, 1504, 2048, 2592, 4128, 4608, 5216)
+LONG_HINTS = (13, 40, 1 << 20)  # the K split, and both sizes of tiles
 
 
 @pytest.mark.parametrize("fmt", FMTS)
@@ -317,10 +318,10 @@ def test_long_rows(H, act, N, fmt):
     say("mxfp4 long rows", H, act, N, fmt)
     p = Problem(H, [300, 1, 0, 257, 64], N, H, fmt, act, bias=True,
                 residual=act == "none", exact=True)
-    check_bf16(p, (13, 1 << 20), exact=act == "none")
+    check_bf16(p, LONG_HINTS, exact=act == "none")
     # scales of tokens that start on no word: the same bytes
     d = p.dev()
-    for hint in (13, 1 << 20):
+    for hint in LONG_HINTS:
         plain = mxq.moe_expert_matmul_mxfp4(**d, expected_m=hint)
         far, _ = wide(d["scales"], 3, 2, 0xFF)
         out = mxq.moe_expert_matmul_mxfp4(**{**d, "scales": far},
@@ -336,7 +337,7 @@ def test_long_rows(H, act, N, fmt):
 def test_long_rows_quantized(H, act, N, out_fmt, fmt):
     say("mxfp4 long rows, quantized", H, act, N, out_fmt, fmt)
     check_quant(Problem(6, [260, 70, 0, 1], N, H, fmt, act, bias=True, pad=1),
-                out_fmt, (13, 1 << 20))
+                out_fmt, LONG_HINTS)
 
 
 @pytest.mark.parametrize("fmt", FMTS)
@@ -351,7 +352,7 @@ def test_long_rows_nan_and_device_data(H, fmt):
     want = torch.zeros((p.rows, 272), dtype=torch.bool)
     want[150] = True
     want[a:a + 70, 200] = True
-    for hint in (13, 1 << 20):
+    for hint in LONG_HINTS:
         for wider in (False, True):
             d = p.dev()
             if wider:
@@ -370,7 +371,7 @@ def test_long_rows_nan_and_device_data(H, fmt):
         for e in range(3):
             a, n = ref.live_rows(offsets, counts, p.rows, e)
             live[a:a + n] = n > 0
-        for hint in (13, 1 << 20):
+        for hint in LONG_HINTS:
             out = torch.full((p.rows + 4, p.cols), 5.0, dtype=torch.bfloat16,
                              device=DEV)
             mxq.moe_expert_matmul_mxfp4(**d, out=out, expected_m=hint)
