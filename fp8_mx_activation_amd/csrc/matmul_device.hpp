@@ -4,6 +4,7 @@
 #pragma once
 
 #include "mxfp4_device.hpp"
+#include "row_tiles.hpp"
 
 namespace mxq {
 
@@ -209,9 +210,10 @@ __device__ __forceinline__ v8i join(const v4i& a, const v4i& b) {
 // from device data; every wavefront finds its block's by itself.  Runs of
 // consecutive tiles go to one XCD (block b runs on XCD b % 8), and within a
 // run eight row tiles share a column of weights, so the 32 CUs of an XCD
-// read a window of 8 by 4 tiles through their L2.  SPREAD: a row tile's columns
-// one after the other, on all XCDs, where row tiles differ in what they take and
-// weights are read once either way.
+// read a window of 8 by 4 tiles through their L2.  TM = kAllRows (every expert
+// that holds rows is one tile of them all): a tile's columns one after the
+// other, on all XCDs, where tiles differ in what they take and weights are read
+// once either way.
 struct TileOf {
   int e, m0, n;
   ExpertRows rows;  // of expert e
@@ -219,9 +221,10 @@ struct TileOf {
 
 constexpr int kGroupM = 8;
 
-template <int TM, bool SPREAD = false>
+template <int TM>
 __device__ __forceinline__ bool find_tile(const MatmulArgs& a, int tiles_n,
                                           TileOf& t) {
+  constexpr bool kSpread = TM == kAllRows;
   const int lane = threadIdx.x & 63;
   const int per = (a.E + 63) / 64;  // experts per lane, consecutive
   ExpertRows er{0, 0};
@@ -230,7 +233,7 @@ __device__ __forceinline__ bool find_tile(const MatmulArgs& a, int tiles_n,
     const int e = lane * per + i;
     if (e < a.E) {
       er = expert_rows(a, e);
-      mine += (er.count + TM - 1) / TM;
+      mine += row_tiles<TM>(er.count);
     }
     // regions that do not overlap hold 2^24 tiles at most; more, of offsets
     // that no layout makes, must not overflow the sums
@@ -246,11 +249,11 @@ __device__ __forceinline__ bool find_tile(const MatmulArgs& a, int tiles_n,
   const int64_t total = (int64_t)tiles_m * tiles_n;
   const int64_t run = (total + 7) / 8;
   const int64_t at =
-      SPREAD ? (int64_t)blockIdx.x
-             : (int64_t)(blockIdx.x & 7) * run + (blockIdx.x >> 3);
-  if ((!SPREAD && (int64_t)(blockIdx.x >> 3) >= run) || at >= total)
+      kSpread ? (int64_t)blockIdx.x
+              : (int64_t)(blockIdx.x & 7) * run + (blockIdx.x >> 3);
+  if ((!kSpread && (int64_t)(blockIdx.x >> 3) >= run) || at >= total)
     return false;
-  constexpr int kGroup = SPREAD ? 1 : kGroupM;
+  constexpr int kGroup = kSpread ? 1 : kGroupM;
   const int64_t group = at / ((int64_t)kGroup * tiles_n);
   const int gm = min(kGroup, tiles_m - (int)group * kGroup);
   const int in = (int)(at - group * kGroup * tiles_n);
@@ -272,7 +275,7 @@ __device__ __forceinline__ bool find_tile(const MatmulArgs& a, int tiles_n,
     for (int i = 0; i < per; ++i) {
       e = owner * per + i;
       er = expert_rows(a, e);
-      const int c = (er.count + TM - 1) / TM;
+      const int c = row_tiles<TM>(er.count);
       if (m < first + c) break;
       first += c;
     }

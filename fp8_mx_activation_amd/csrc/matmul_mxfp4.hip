@@ -373,7 +373,7 @@ __global__ __launch_bounds__(256, 1) void matmul4_stream_kernel(
   // every expert that holds rows is one tile of them all, so the blocks that
   // have work come first and spread evenly
   TileOf tile;
-  if (!find_tile<1 << 30, true>(a, blocks_n, tile)) return;
+  if (!find_tile<kAllRows>(a, blocks_n, tile)) return;
   const int e = tile.e;
   const ExpertRows er = tile.rows;
   const bool gated = a.act == kActSiluMul;
