@@ -688,13 +688,17 @@ __global__ __launch_bounds__(kBackWaves * 64) void balance_backward_kernel(
     dot = group_sum<L>(dot);
     const bool mine = t >= q.first && t < q.end;
     const float w = mine ? coef : 0.0f;
-    const float wz = Z && mine ? zcoef * r.lse : 0.0f;
+    // where 2 grad_z / n lse passes fp32's range, the log-sum-exp meets the
+    // share first: a share of 0 then stays 0
+    const bool far = Z && fabsf(zcoef * r.lse) > kFltMax;
+    const float wz = Z && mine ? zcoef * (far ? 1.0f : r.lse) : 0.0f;
+    const float zl = far ? r.lse : 1.0f;
     float g[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       g[i] = w * r.p[i] * (d[i] - dot);
       if (SIGMOID) g[i] *= r.back[i];
-      if (Z) g[i] += wz * (SIGMOID ? r.soft : r.p)[i];
+      if (Z) g[i] += wz * (zl * (SIGMOID ? r.soft : r.p)[i]);
       g[i] += add[i];
     }
     if (t < to)
