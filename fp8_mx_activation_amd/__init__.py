@@ -1150,7 +1150,8 @@ def mxfp4_quant_rows(x: torch.Tensor, rule: str = "no_clip",
     """Rows of ``x`` ([rows, H] or weights [E, N, H], bf16 or float32) to
     MXFP4: ``(q [..., H/2] uint8, scales [..., H/32] uint8)``, H a multiple of
     32.  ``rule`` is ``"no_clip"`` or ``"ocp_floor"`` (see
-    ``mxfp4_quant_rows`` in mxq.h).  Rows of scales allocated here start on 16
+    ``mxfp4_quant_rows`` in mxq.h); a group with a NaN gets scale byte 255,
+    which stands for NaN.  Rows of scales allocated here start on 16
     bytes (a view of a padded buffer where H/32 is no multiple of 16), as
     ``moe_expert_matmul_mxfp4`` takes them."""
     lead = x.shape[:-1]

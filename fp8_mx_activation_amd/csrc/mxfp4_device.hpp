@@ -9,12 +9,15 @@ namespace mxq {
 // Exponent of a group's scale from the fp32 magnitude bits of its largest
 // value: the smallest e with amax <= 6 * 2^e (6 = 1.5 * 2^2), or
 // floor(log2 amax) - 2, clamped below at -127; the largest finite fp32 gives
-// 126.
+// 126.  e2m1 has no NaN: a group that holds one (whose bits lie above
+// infinity's) gets 128, scale byte 255, which makes all of it NaN whatever its
+// codes are.
 template <int RULE>
 __device__ __forceinline__ int e2m1_exponent(uint32_t m) {
   int e = (int)(m >> 23) - 129;
   if constexpr (RULE == kNoClip) e += (m & 0x7FFFFFu) > 0x400000u ? 1 : 0;
-  return e < -127 ? -127 : e;
+  e = e < -127 ? -127 : e;
+  return m > 0x7F800000u ? 128 : e;
 }
 
 // Eight values over their scale -> eight codes, nearest even, with gfx950's

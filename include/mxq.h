@@ -583,7 +583,9 @@ mxq_status moe_expert_matmul_quant(
 
 /* A row of H channels (a multiple of 32) is H / 2 bytes of e2m1 codes (0, 0.5,
  * 1, 1.5, 2, 3, 4, 6 and their negatives; channel 2i in the lower half of byte
- * i) and H / 32 scale bytes, as in MXQ_SCALE_E8M0_G32. */
+ * i) and H / 32 scale bytes, as in MXQ_SCALE_E8M0_G32.  e2m1 has no NaN: the
+ * calls that write it give a group with a NaN among its values scale byte 255
+ * (codes unspecified), which is NaN to those that read it. */
 
 /* Rows of bf16 or fp32 (dtype) to MXFP4: weights, or activations.
  *
@@ -652,7 +654,8 @@ mxq_status moe_expert_matmul_mxfp4(
 /* moe_expert_matmul_mxfp4 with its fp32 rows quantized for the next product:
  * out_fmt MXQ_SCALE_MXFP4 (q_out [num_rows, ld_out] codes) or
  * MXQ_SCALE_E8M0_G32 (e4m3), by the rule without clipping; the output columns
- * must be a multiple of 32.  Otherwise as moe_expert_matmul_quant. */
+ * must be a multiple of 32.  Otherwise as moe_expert_matmul_quant, but for
+ * MXFP4 groups with a NaN, whose scale byte is 255. */
 mxq_status moe_expert_matmul_mxfp4_quant(
     const void* q, int64_t ld_q, const uint8_t* scales, int64_t ld_s,
     int64_t num_rows, mxq_scale_fmt fmt, const void* w_fp4,
