@@ -295,8 +295,11 @@ constexpr int kStageLd = 260;  // floats per staged token (256 weight rows + pad
 // of each wavefront row) at a time go through LDS as they are, so that a thread
 // ends up with eight neighbouring channels of a row: gate and factor meet, a row
 // is written in whole lines, and a quantization group lies within a wavefront.
+// The arguments come by value: through a reference the compiler asks again for
+// what they hold at every store (8-bit weights, 65536 rows, down: 1278 us, not
+// 1262).
 template <int XF, int OUT, bool GATED, int PX = 2>
-__device__ __forceinline__ void finish_tile(const MatmulArgs& a, int e,
+__device__ __forceinline__ void finish_tile(const MatmulArgs a, int e,
                                             int64_t row0, int rows, int n0,
                                             const v16f (&acc)[4][XF],
                                             uint8_t* lds) {
