@@ -114,7 +114,7 @@ __device__ __forceinline__ void finish_few(const MatmulArgs& a, int e,
 // no barrier orders them.  The weight rows are the MFMA's A operand, the token
 // rows its B operand: a lane ends up with four neighbouring output channels of
 // one token.  Three steps; two of 8-bit rows whose scales, all of which are in
-// LDS from the start, leave no room for a third (above 20320 channels).
+// LDS from the start, leave no room for a third (above 20224 channels).
 template <bool X8, int RING>
 struct SmallStep {
   static constexpr int kRow = X8 ? 256 : 128;  // bytes of a token row
@@ -1056,8 +1056,12 @@ mxq_status launch_small(const MatmulArgs& a, hipStream_t s) {
   if (bn * a.E > max_blocks(256)) return MXQ_ERR_UNSUPPORTED;
   const int ld_xs = small_scale_ld(a.H / 32);
   const int lds = St::kRings + 16 * ld_xs;
-  if constexpr (RING == 3) {
+  // whole words of the longest rows' scales, and one
+  constexpr int kMost = 16 * (MXQ_MAX_HIDDEN / 32 + 4);
+  if constexpr (X8 && RING == 3) {
     if (lds > kLds) return launch_small<X8, 2, OUT>(a, s);
+  } else {
+    static_assert(St::kRings + kMost <= kLds, "rows of any length fit");
   }
   static_assert(St::kRings >= 4 * 16 * (64 + 4) * 4,
                 "the joined K parts fit the rings");
