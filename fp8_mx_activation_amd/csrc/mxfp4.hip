@@ -5,11 +5,12 @@
 //        floor(log2 amax) - 2
 //   q    = e2m1(x * 2^-e), nearest even; scale byte e + 127
 //
-// Every kernel is bound by what it reads and writes.  A lane owns 16
-// neighbouring channels, 32 bytes of bf16 and 8 of codes; a group's two lanes
-// are neighbours.  16384 rows of 7168 channels (297 MB) are quantized in 52.8 us
-// (5.6 TB/s) and turned back to bf16 in 49.1 (6.0); 40832 rows of 4 bits become
-// e4m3 in 70 us (6.3).  With 8 channels a lane the first two took 77 and 60 us.
+// Every kernel is bound by what it reads and writes.  To quantize or to widen to
+// e4m3, a lane owns 16 neighbouring channels (32 bytes of bf16, 8 of codes); a
+// group's two lanes are neighbours.  16384 rows of 7168 bf16 channels (297 MB)
+// are quantized in 52.8 us (5.6 TB/s; 8 channels a lane with ordinary loads and
+// stores 77); 40832 rows of 4 bits become e4m3 in 70 us (6.3 TB/s).  Back to bf16
+// a lane owns 8: 49.1 us for the 16384 rows (6.0; 60 with ordinary stores).
 #include <algorithm>
 
 #include "mxfp4_device.hpp"
