@@ -1158,7 +1158,16 @@ mxq_status launch_tile(const MatmulArgs& a, hipStream_t s) {
 //   (8-bit)                 13     21     37     27     47
 //   128-row tiles           34     35     35     36     37
 //   (8-bit)                 46     46     46     46     47
-// (of two experts with K = 1024 and 512 the two are even at 16 rows).
+// Two experts of 4096 weight rows and 20 rows each: 512 channels 5.7 (6.0) against
+// 8.6 (9.5) in tiles, 1024 6.5 (7.0) against 10.6 (12.4), 4096 12.5 (13.6) against
+// 21.7 (28.8); a hundred experts of 64 weight rows, 7168 channels, 24 rows: 18 (20)
+// against 34 (46).
+//
+// Between these, too few blocks of 256 weight rows: gate/up of 6, 10 and 15 experts
+// takes, with FW = 2, 19, 33 and 39 us for 16 rows of 4 bits each and 21, 34 and 40
+// for 20 (one pass), 36, 40 and 45 in tiles.  8-bit rows: 16 in one pass 19, 33 and
+// 40, 20 in two passes 33, 59 and 72, in tiles 46, 47 and 50.  Where 13 to 16 are
+// expected a routing's busy experts hold more than 16, hence tiles from there on.
 template <bool X8, int OUT>
 mxq_status launch(const MatmulArgs& a, int64_t expected, hipStream_t s) {
   constexpr int64_t kCus = 256;

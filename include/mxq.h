@@ -551,8 +551,9 @@ mxq_status requant_per_token_to_per_tensor(
  * num_rows <= MXQ_MAX_MATMUL_ROWS, ld_q and ld_s <= MXQ_MAX_MATMUL_LD, else
  * MXQ_ERR_UNSUPPORTED.  Sums are fp32, but for the matrix unit's own
  * 32-product groups, in which it drops what lies more than 13 bits below the
- * group's largest product (sums of normal values keep 16 bits).  Scale byte 255 and e4m3 NaN bytes in a live row
- * or its expert's weights give NaN in what they enter. */
+ * group's largest product (sums of normal values keep 16 bits).  Scale byte
+ * 255 and e4m3 NaN bytes in a live row or its expert's weights give NaN in
+ * what they enter. */
 mxq_status moe_expert_matmul(const void* q_fp8, int64_t ld_q,
                              const uint8_t* scales, int64_t ld_s,
                              int64_t num_rows, mxq_scale_fmt fmt,
@@ -639,6 +640,11 @@ mxq_status upscale_mxfp4_to_bf16(const void* q_fp4, int64_t ld_q,
  *                    writes them.  ld_ws and w_scales are multiples of 4, and
  *                    a row's scales are read four at a time: up to three bytes
  *                    behind the last of them must be readable.
+ *   expected_m       as there; here the kernels for few rows serve up to 32
+ *                    rows of one expert, 24 of few experts and 20 (16 of 8-bit
+ *                    rows) of many.  Too large a guess costs up to twice, of
+ *                    few experts up to 5 times; too small a one 3 times at
+ *                    160 rows (80 of 8 bits) and more beyond.
  * The other arguments, limits and errors are moe_expert_matmul's; H is a
  * multiple of 32, and ld_ws * N < 2^31.  Sums are fp32; 32 products of 4-bit
  * payloads add up exactly in the matrix unit, of those with 8-bit rows it
