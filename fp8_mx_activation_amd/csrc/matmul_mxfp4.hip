@@ -1166,8 +1166,12 @@ mxq_status launch_tile(const MatmulArgs& a, hipStream_t s) {
 // Between these, too few blocks of 256 weight rows: gate/up of 6, 10 and 15 experts
 // takes, with FW = 2, 19, 33 and 39 us for 16 rows of 4 bits each and 21, 34 and 40
 // for 20 (one pass), 36, 40 and 45 in tiles.  8-bit rows: 16 in one pass 19, 33 and
-// 40, 20 in two passes 33, 59 and 72, in tiles 46, 47 and 50.  Where 13 to 16 are
-// expected a routing's busy experts hold more than 16, hence tiles from there on.
+// 40, 20 in two passes 33, 59 and 72, in tiles 46, 47 and 50.  A routing's busy
+// experts hold more than the mean (top-2 routings, six each): mean 12 rows of 8
+// bits 32, 41 and 58 against 45, 47 and 50, mean 16 39, 52 and 74 against 46, 47 and
+// 50, hence tiles above 12; of 4 bits mean 12 21, 33 and 47 against 36, 39 and 44,
+// mean 16 23, 40 and 56 against 36, 40 and 45, mean 20 24, 43 and 61 against 36, 39
+// and 45.
 template <bool X8, int OUT>
 mxq_status launch(const MatmulArgs& a, int64_t expected, hipStream_t s) {
   constexpr int64_t kCus = 256;
